@@ -66,8 +66,8 @@ typedef enum {
 } pkv_status;
 
 /* Pool geometry. page_size, num_q_heads, num_kv_heads and head_dim must be
- * 16, 32, 8 and 64. max_seq_len is a multiple of 16, at most 2048, and sets
- * the block-table row length (max_seq_len / 16). max_splits bounds the
+ * 16, 32, 8 and 64. max_seq_len is a multiple of 16, at most 2048 (more with
+ * PKV_FLAG_LONG_CONTEXT), and sets the block-table row length (max_seq_len / 16). max_splits bounds the
  * split-KV count per sequence (0 selects 64; at most 128) and sizes the
  * handle's split workspace. flags: PKV_FLAG_* below (0 for none).
  * num_pages is the number of pages in the pool the caller allocates: 4096
@@ -104,13 +104,22 @@ typedef struct {
  * between them or leave this flag off.) Off by default. */
 #define PKV_FLAG_PDL 1
 
+/* A handle whose max_seq_len may be any multiple of 16 up to
+ * PKV_MAX_LONG_CONTEXT. Where max_seq_len exceeds 2,048 it serves the calls
+ * without a context limit of their own: pkv_append, pkv_append_rope,
+ * pkv_prefill_fill, and those of pkv_window.h, pkv_axes.h and pkv_pages.h; the other
+ * attention calls return PKV_ERR_UNSUPPORTED (pkv_plan_decode INVALID_ARG). */
+#define PKV_FLAG_LONG_CONTEXT 2
+#define PKV_MAX_LONG_CONTEXT 1048576
+
 typedef struct pkv_pool* pkv_pool_t;
 
 /* Validates the geometry and creates a handle on the current device. The
  * handle owns only device scratch: the split-KV partials (two layer-parity
  * copies of max_batch x 32 x max_splits x (64 + 2) floats), one ticket
  * counter per (sequence, kv head) and parity, one layer counter per sequence
- * (pkv_append_attend_layers) and the sticky error flag.
+ * (pkv_append_attend_layers), 12 bytes per pool page (pkv_pages.h) and the
+ * sticky error flag.
  * It does not own the pools, tables or tensors. A handle's launches share
  * that scratch, so they must be ordered in one stream (calls issued to
  * several streams at once need a handle each). Returns INVALID_ARG for a

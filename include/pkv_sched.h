@@ -108,6 +108,44 @@ pkv_status pkv_sched_extend_batch(pkv_sched_t sched, const int* ids, const int* 
  * credits to the pool. INVALID_ARG if it is not active. */
 pkv_status pkv_sched_finish(pkv_sched_t sched, int request_id);
 
+/* Forks an active request after its first `length` tokens (1 <= length, at
+ * most what pkv_sched_extend has made addressable): a new active request, last
+ * in admission order, that shares the parent's pages of positions below
+ * floor(length / page_size) * page_size and owns a page per layer for the rest.
+ * Its budget is that of a submission with `length` prompt tokens and
+ * max_new_tokens, reserved in full (a page it shares counts for both), so it
+ * can always finish whoever ends first. A fork extends work that was admitted,
+ * so it does not queue: PKV_ERR_REJECTED, changing nothing, if the free credits
+ * do not cover it now. Shared pages are freed when their last owner gives
+ * them back.
+ *
+ * *count (0, or num_layers when length is not a whole number of pages) page
+ * copies are due before the child is used: the first *tokens tokens of src[i] to
+ * dst[i] (pkv_copy_pages of pkv_pages.h). INVALID_ARG if capacity is below
+ * num_layers, the request is not active, length is out of range or the child's
+ * submission would be invalid. */
+pkv_status pkv_sched_fork(pkv_sched_t sched, int request_id, int length, int max_new_tokens,
+                          int* child_id, int32_t* src, int32_t* dst, int capacity, int* count,
+                          int* tokens);
+
+/* Gives back, in every layer, the request's pages all of whose positions lie in
+ * [sinks, first_visible): what attention behind a window starting at
+ * first_visible with `sinks` first tokens never reads again (pkv_window.h).
+ * Their block-table entries become -1 and their credits return to the pool.
+ * *released (may be NULL) is the number of pages. INVALID_ARG for an inactive
+ * request, negative arguments or first_visible beyond the addressable length. */
+pkv_status pkv_sched_release(pkv_sched_t sched, int request_id, int first_visible, int sinks,
+                             int* released);
+
+/* Renumbers up to `capacity` assigned pages so that those in use come first: the
+ * highest assigned ids move to the lowest free ones. Writes the moves to src
+ * and dst and their number to *count. The tables of pkv_sched_block_tables name
+ * the new ids from now on, so the moves must be carried out on the device
+ * (pkv_compact_pages of pkv_pages.h on the tables in use, or pkv_copy_pages
+ * before new tables are used) before any other use of the pool. */
+pkv_status pkv_sched_compact(pkv_sched_t sched, int32_t* src, int32_t* dst, int capacity,
+                             int* count);
+
 /* The active requests in admission order: one decode step's batch. Writes up
  * to `capacity` ids and the full count to *count (INVALID_ARG if capacity is
  * smaller than the count); records the largest batch for the counters. */

@@ -34,7 +34,10 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_append", "pkv_decode_att
             "pkv_sched_decode_batch",
             "pkv_sched_block_tables", "pkv_sched_get_stats", "pkv_prefill_fill",
             "pkv_prefill_attention", "pkv_prefill", "pkv_plan_decode",
-            "pkv_pool_device_figures", "pkv_status_string")
+            "pkv_pool_device_figures", "pkv_window_attention", "pkv_window_append_attend",
+            "pkv_window_prefill_attention", "pkv_prefill_fill_axes", "pkv_copy_pages",
+            "pkv_compact_pages", "pkv_sched_fork", "pkv_sched_release", "pkv_sched_compact",
+            "pkv_status_string")
 
 
 class PkvError(RuntimeError):
@@ -61,7 +64,14 @@ class PoolConfig(ctypes.Structure):
         "max_seq_len", "max_batch", "max_splits", "flags")]
 
 
-PKV_FLAG_PDL = 1
+PKV_FLAG_PDL, PKV_FLAG_LONG_CONTEXT = 1, 2
+PKV_MAX_LONG_CONTEXT = 1048576
+PKV_MAX_AXES = 4
+
+
+class AxesRopeConfig(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int),
+                ("num_axes", ctypes.c_int), ("axis_of_pair", ctypes.c_uint8 * (HEAD_DIM // 2))]
 
 
 class DeviceFigures(ctypes.Structure):
@@ -125,6 +135,15 @@ def load(path: str = None):
     lib.pkv_prefill.argtypes = [P, i, P, P, P, P, P, P, P, P, P, i, i, i, P]
     lib.pkv_plan_decode.argtypes = [ctypes.POINTER(DeviceFigures), i, i, ctypes.POINTER(Plan)]
     lib.pkv_pool_device_figures.argtypes = [P, ctypes.POINTER(DeviceFigures)]
+    lib.pkv_window_attention.argtypes = [P, i, P, P, P, P, P, P, i, i, P, P, i, i, i, P]
+    lib.pkv_window_append_attend.argtypes = [P, i, P, P, P, P, P, P, P, P, i, i, P, P, i, i, i, P]
+    lib.pkv_window_prefill_attention.argtypes = [P, i, P, P, P, P, P, P, P, i, i, i, i, i, P]
+    lib.pkv_prefill_fill_axes.argtypes = [P, i, P, P, P, P, P, P, P, P, P, P, P, i, i, i, i, P]
+    lib.pkv_copy_pages.argtypes = [P, P, P, P, P, P, i, P]
+    lib.pkv_compact_pages.argtypes = [P, P, P, P, P, P, i, P]
+    lib.pkv_sched_fork.argtypes = [P, i, i, i, SP, P, P, i, SP, SP]
+    lib.pkv_sched_release.argtypes = [P, i, i, i, SP]
+    lib.pkv_sched_compact.argtypes = [P, P, P, i, SP]
     lib.pkv_status_string.argtypes = [i]
     lib.pkv_status_string.restype = ctypes.c_char_p
     for name in EXPORTED[:-1]:
@@ -132,6 +151,16 @@ def load(path: str = None):
     if path == _build.LIBRARY:
         _lib = lib
     return lib
+
+
+_dtype_names = {}
+
+
+def _dtype_name(dtype):
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).removeprefix("torch.")
+    return name
 
 
 def _addr(x, dtype=None, what="tensor"):
@@ -145,7 +174,7 @@ def _addr(x, dtype=None, what="tensor"):
         return x
     if not x.is_contiguous():
         raise ValueError(f"{what}: the library takes contiguous tensors")
-    if dtype is not None and str(x.dtype) != "torch." + dtype:
+    if dtype is not None and _dtype_name(x.dtype) != dtype:
         raise ValueError(f"{what}: expected {dtype}, got {x.dtype}")
     return x.data_ptr()
 
@@ -158,7 +187,8 @@ def _i32(x, what):
 _DTYPES = {"q": "bfloat16", "k": "bfloat16", "v": "bfloat16", "k_pool": "bfloat16",
            "v_pool": "bfloat16", "block_tables": "int32", "positions": "int32",
            "seq_lens": "int32", "cu_tokens": "int32", "start_pos": "int32", "out": "float32",
-           "rope_cos": "float32", "rope_sin": "float32"}
+           "rope_cos": "float32", "rope_sin": "float32", "rope_positions": "int32",
+           "q_out": "bfloat16", "src": "int32", "dst": "int32", "tokens": "int32"}
 
 
 def _ptrs(**tensors):
@@ -183,9 +213,10 @@ def _check(status, call):
 class Pool:
     """Owns a pkv_pool_t handle (the split workspace and the error flag)."""
 
-    def __init__(self, handle, config, lib):
+    def __init__(self, handle, config, lib, device=None):
         self.handle = handle
         self.config = config
+        self.device = device     # CUDA device index, where known
         self._lib = lib
 
     def close(self):
@@ -207,7 +238,8 @@ def pkv_pool_create(num_layers, num_pages, max_batch, max_seq_len=MAX_SEQ_LEN, m
                      max_seq_len, max_batch, max_splits, flags)
     handle = ctypes.c_void_p()
     _check(lib.pkv_pool_create(ctypes.byref(cfg), ctypes.byref(handle)), "pkv_pool_create")
-    return Pool(handle.value, cfg, lib)
+    import torch
+    return Pool(handle.value, cfg, lib, torch.cuda.current_device())
 
 
 def pkv_pool_destroy(pool: Pool):
@@ -393,6 +425,174 @@ def pkv_prefill(pool: Pool, layer, q, k, v, k_pool, v_pool, block_tables, cu_tok
     _check(st, "pkv_prefill")
 
 
+# ---------------------------------------------------------------- window, axes, pages
+def _arg(pool, name, x, count=0):
+    """Address of a tensor argument: what _addr checks, and that the tensor lies
+    on the handle's device and holds at least `count` elements."""
+    if x is None or type(x) is int:
+        return x
+    address = _addr(x, _DTYPES[name], name)
+    if pool.device is not None and x.get_device() != pool.device:
+        raise ValueError(f"{name}: expected a tensor on cuda:{pool.device}, got {x.device}")
+    if x.numel() < count:
+        raise ValueError(f"{name}: expected at least {count} elements, got {x.numel()}")
+    return address
+
+
+def _table_entries(pool):
+    c = pool.config
+    return c.num_layers * c.max_batch * (c.max_seq_len // PAGE_SIZE) if c else 0
+
+
+def _pool_elements(pool):
+    return pool.config.num_pages * NUM_KV_HEADS * PAGE_SIZE * HEAD_DIM if pool.config else 0
+
+
+class AxesRope:
+    """Rotation by several position axes (include/pkv_axes.h): keeps the tables."""
+
+    def __init__(self, cos, sin, axis_of_pair):
+        pairs = HEAD_DIM // 2
+        axes = [int(a) for a in axis_of_pair]
+        if len(axes) != pairs or min(axes) < 0 or max(axes) >= PKV_MAX_AXES:
+            raise ValueError(f"axis_of_pair: expected {pairs} axes in 0 .. {PKV_MAX_AXES - 1}")
+        for name, t in (("rope_cos", cos), ("rope_sin", sin)):
+            if t.dim() != 2 or t.shape[1] != pairs or t.shape[0] < 1 or t.shape != cos.shape:
+                raise ValueError(f"{name}: expected [rows][{pairs}]")
+        self.tables = (cos, sin)
+        self.num_axes = max(axes) + 1
+        self.device = cos.get_device()
+        self.config = AxesRopeConfig(_addr(cos, "float32", "rope_cos"),
+                                     _addr(sin, "float32", "rope_sin"), int(cos.shape[0]),
+                                     self.num_axes, (ctypes.c_uint8 * pairs)(*axes))
+        self.address = ctypes.addressof(self.config)
+
+
+def pkv_axes_rope(cos, sin, axis_of_pair) -> AxesRope:
+    """cos, sin: fp32 [rows][32] on the device; axis_of_pair: the position axis of
+    each of the 32 rotary pairs. Keep it for as many calls as use the tables."""
+    return AxesRope(cos, sin, axis_of_pair)
+
+
+def _rope_args(pool, rope, positions, tokens):
+    """(rope, positions, stride) as the entry points take them; positions: int32
+    [axes][>= tokens]."""
+    if rope is None:
+        if positions is not None:
+            raise ValueError("rope_positions without rope")
+        return None, None, 0
+    if positions is None:
+        raise ValueError("rope_positions: missing")
+    if pool.device is not None and rope.device != pool.device:
+        raise ValueError(f"rope_cos: expected a tensor on cuda:{pool.device}")
+    if positions.dim() != 2 or positions.shape[0] < rope.num_axes or positions.shape[1] < tokens:
+        raise ValueError(f"rope_positions: expected [{rope.num_axes}][>= {tokens}], got "
+                         f"{tuple(positions.shape)}")
+    return rope.address, _arg(pool, "rope_positions", positions), int(positions.shape[1])
+
+
+def pkv_window_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, seq_lens, out, window,
+                         sinks=0, rope=None, rope_positions=None, batch=None, num_splits=0,
+                         stream=None):
+    """Decode attention over the last `window` tokens and the first `sinks` ones
+    (q bf16 [B][32][64], out fp32). rope: an AxesRope, with rope_positions
+    int32 [axes][B]: the queries are rotated first. seq_lens 0: a padding row."""
+    batch = _batch(seq_lens, batch)
+    rows = batch * NUM_Q_HEADS * HEAD_DIM
+    st = pool._lib.pkv_window_attention(
+        pool.handle, int(layer), _arg(pool, "q", q, rows),
+        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
+        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
+        int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
+        _stream(stream))
+    _check(st, "pkv_window_attention")
+
+
+def pkv_window_append_attend(pool: Pool, layer, q, k, v, k_pool, v_pool, block_tables, seq_lens,
+                             out, window, sinks=0, rope=None, rope_positions=None, batch=None,
+                             num_splits=0, stream=None):
+    """Append (at seq_lens - 1, the key rotated with rope) and pkv_window_attention
+    in one launch; k, v bf16 [B][8][64]."""
+    batch = _batch(seq_lens, batch)
+    rows, new = batch * NUM_Q_HEADS * HEAD_DIM, batch * NUM_KV_HEADS * HEAD_DIM
+    st = pool._lib.pkv_window_append_attend(
+        pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
+        _arg(pool, "v", v, new), _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
+        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
+        int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
+        _stream(stream))
+    _check(st, "pkv_window_append_attend")
+
+
+def pkv_window_prefill_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, cu_tokens,
+                                 start_pos, out, max_chunk_tokens, window, sinks=0, batch=None,
+                                 total_tokens=None, stream=None):
+    """pkv_prefill_attention behind a window: every chunk token attends to the last
+    `window` tokens up to itself and to the first `sinks` ones."""
+    batch = _batch(start_pos, batch)
+    total = int(q.shape[0]) if total_tokens is None else int(total_tokens)
+    rows = total * NUM_Q_HEADS * HEAD_DIM
+    st = pool._lib.pkv_window_prefill_attention(
+        pool.handle, int(layer), _arg(pool, "q", q, rows),
+        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
+        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
+        _arg(pool, "out", out, rows), int(window), int(sinks), batch, total,
+        int(max_chunk_tokens), _stream(stream))
+    _check(st, "pkv_window_prefill_attention")
+
+
+def pkv_prefill_fill_axes(pool: Pool, layer, q, k, v, q_out, k_pool, v_pool, block_tables,
+                          cu_tokens, start_pos, rope, rope_positions, max_chunk_tokens,
+                          batch=None, total_tokens=None, stream=None):
+    """Writes the chunk's rotated keys and its values into their pages and its
+    rotated queries into q_out (bf16; q itself, or None with q None).
+    rope_positions: int32 [axes][>= T]."""
+    if rope is None:
+        raise ValueError("rope: missing")
+    batch = _batch(start_pos, batch)
+    total = int(k.shape[0]) if total_tokens is None else int(total_tokens)
+    rows, new = total * NUM_Q_HEADS * HEAD_DIM, total * NUM_KV_HEADS * HEAD_DIM
+    st = pool._lib.pkv_prefill_fill_axes(
+        pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
+        _arg(pool, "v", v, new), _arg(pool, "q_out", q_out, rows),
+        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
+        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
+        *_rope_args(pool, rope, rope_positions, total), batch, total, int(max_chunk_tokens),
+        _stream(stream))
+    _check(st, "pkv_prefill_fill_axes")
+
+
+def pkv_copy_pages(pool: Pool, src, dst, k_pool, v_pool, tokens=None, n=None, stream=None):
+    """Copies page src[i] to page dst[i] in both pools: whole, or its first
+    tokens[i] tokens (int32 tensors on the device)."""
+    n = int(src.shape[0]) if n is None else int(n)
+    st = pool._lib.pkv_copy_pages(
+        pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
+        _arg(pool, "tokens", tokens, n), _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)), n, _stream(stream))
+    _check(st, "pkv_copy_pages")
+
+
+def pkv_compact_pages(pool: Pool, src, dst, k_pool, v_pool, block_tables, n=None, stream=None):
+    """Moves page src[i] to page dst[i] in both pools and rewrites the block
+    tables (all layers and rows) in place."""
+    n = int(src.shape[0]) if n is None else int(n)
+    st = pool._lib.pkv_compact_pages(
+        pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
+        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
+        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
+        _arg(pool, "block_tables", block_tables, _table_entries(pool)), n, _stream(stream))
+    _check(st, "pkv_compact_pages")
+
+
 # ---------------------------------------------------------------- admission scheduler (host)
 class Scheduler:
     """Owns a pkv_sched_t: admission credits and lazy page assignment for the
@@ -491,6 +691,47 @@ def pkv_sched_extend_batch(sched: Scheduler, ids, lengths):
 
 def pkv_sched_finish(sched: Scheduler, request_id):
     _check(sched._lib.pkv_sched_finish(sched.handle, int(request_id)), "pkv_sched_finish")
+
+
+def pkv_sched_fork(sched: Scheduler, request_id, length, max_new_tokens):
+    """Forks an active request after its first `length` tokens: (child id, src,
+    dst, tokens): the page copies (one per layer, or none) that the child needs
+    before it is used, the first `tokens` tokens of each; int32 arrays for
+    pkv_copy_pages. PkvError(PKV_ERR_REJECTED) when the free credits do not
+    cover the child."""
+    import numpy as np
+    layers = sched.config.num_layers
+    src, dst = np.empty(layers, np.intc), np.empty(layers, np.intc)
+    rid, count, tokens = ctypes.c_int(-1), ctypes.c_int(), ctypes.c_int()
+    _check(sched._lib.pkv_sched_fork(sched.handle, int(request_id), int(length),
+                                     int(max_new_tokens), ctypes.byref(rid), src.ctypes.data,
+                                     dst.ctypes.data, layers, ctypes.byref(count),
+                                     ctypes.byref(tokens)), "pkv_sched_fork")
+    n = count.value
+    return rid.value, src[:n], dst[:n], np.full(n, tokens.value, np.intc)
+
+
+def pkv_sched_release(sched: Scheduler, request_id, first_visible, sinks=0) -> int:
+    """Gives back the request's pages all of whose positions lie in
+    [sinks, first_visible); returns how many (over all layers)."""
+    count = ctypes.c_int()
+    _check(sched._lib.pkv_sched_release(sched.handle, int(request_id), int(first_visible),
+                                        int(sinks), ctypes.byref(count)), "pkv_sched_release")
+    return count.value
+
+
+def pkv_sched_compact(sched: Scheduler, max_moves=None):
+    """Renumbers pages so that those in use come first (at most max_moves of
+    them): (src, dst) int32 arrays for pkv_compact_pages, or for
+    pkv_copy_pages before tables of pkv_sched_block_tables are used."""
+    import numpy as np
+    cap = sched.config.num_pages if max_moves is None else int(max_moves)
+    cap = min(cap, sched.config.num_pages)
+    src, dst = np.empty(max(cap, 1), np.intc), np.empty(max(cap, 1), np.intc)
+    count = ctypes.c_int()
+    _check(sched._lib.pkv_sched_compact(sched.handle, src.ctypes.data, dst.ctypes.data, cap,
+                                        ctypes.byref(count)), "pkv_sched_compact")
+    return src[:count.value].copy(), dst[:count.value].copy()
 
 
 def pkv_sched_decode_batch(sched: Scheduler) -> list:

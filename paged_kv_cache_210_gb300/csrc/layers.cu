@@ -345,6 +345,7 @@ pkv_status launch_layers(pkv_pool_t pool, int layer_begin, int num_layers, const
       static_cast<long long>(layer_begin) + num_layers > c.num_layers || batch < 0 ||
       batch > c.max_batch)
     return PKV_ERR_INVALID_ARG;
+  if (!pkv_short_context(pool)) return PKV_ERR_UNSUPPORTED;
   if (batch == 0 || num_layers == 0) return PKV_OK;
   if (!q || !k || !v || !k_pool || !v_pool || !block_tables || !seq_lens || !out)
     return PKV_ERR_INVALID_ARG;

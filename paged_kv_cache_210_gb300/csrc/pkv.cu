@@ -712,6 +712,7 @@ pkv_status launch_decode(pkv_pool_t pool, int layer, const void* q, const void* 
   if (layer < 0 || layer >= c.num_layers || batch < 0 || batch > c.max_batch)
     return PKV_ERR_INVALID_ARG;
   if (num_splits < 0 || num_splits > c.max_splits) return PKV_ERR_INVALID_ARG;
+  if (!pkv_short_context(pool)) return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out) return PKV_ERR_INVALID_ARG;
   if (kFused && (!k || !v)) return PKV_ERR_INVALID_ARG;
@@ -948,8 +949,9 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
   if (c.page_size != kPage || c.num_q_heads != kHq || c.num_kv_heads != kHkv ||
       c.head_dim != kDim)
     return PKV_ERR_UNSUPPORTED;
+  const int longest = (c.flags & PKV_FLAG_LONG_CONTEXT) ? PKV_MAX_LONG_CONTEXT : kMaxSeqLen;
   if (c.num_layers < 1 || c.num_pages < 1 || c.max_batch < 1 || c.max_seq_len < kPage ||
-      c.max_seq_len > kMaxSeqLen || c.max_seq_len % kPage != 0 || c.max_splits < 0 ||
+      c.max_seq_len > longest || c.max_seq_len % kPage != 0 || c.max_splits < 0 ||
       c.max_splits > kMaxSplitsLimit || c.max_batch > 65535)
     return PKV_ERR_INVALID_ARG;
   if (c.max_splits == 0) c.max_splits = kDefaultMaxSplits;
@@ -970,6 +972,10 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
   ok = ok && cudaMalloc(&pool->err, sizeof(int)) == cudaSuccess;
   ok = ok && cudaMalloc(&pool->seq_done, static_cast<size_t>(c.max_batch) * sizeof(int)) ==
                  cudaSuccess;
+  ok = ok && cudaMalloc(&pool->page_marks, static_cast<size_t>(c.num_pages) *
+                                               (sizeof(unsigned long long) + sizeof(int))) ==
+                 cudaSuccess;
+  if (ok) pool->page_to = reinterpret_cast<int*>(pool->page_marks + c.num_pages);
 
   ok = ok && cudaMemset(pool->tickets, 0, 2 * static_cast<size_t>(c.max_batch) * kHkv * sizeof(int)) ==
                  cudaSuccess;
@@ -1016,6 +1022,7 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
     cudaGetLastError();   // a size the device refuses is not an error here
   }
   ok = ok && pkv_layers_setup(pool);
+  ok = ok && pkv_window_setup(pool);
   if (ok && pool->blocks_per_sm < 1) pool->blocks_per_sm = 1;
   if (ok && pool->cluster_blocks_per_sm < 1) pool->cluster_blocks_per_sm = 1;
   if (ok && pool->wide_blocks_per_sm < 1) pool->wide_blocks_per_sm = 1;
@@ -1037,6 +1044,7 @@ pkv_status pkv_pool_destroy(pkv_pool_t pool) {
   cudaFree(pool->tickets);
   cudaFree(pool->err);
   cudaFree(pool->seq_done);
+  cudaFree(pool->page_marks);
   delete pool;
   return st;
 }

@@ -22,6 +22,12 @@ struct pkv_pool {
   int* tickets;      // [2][max_batch][8]
   int* err;          // sticky error bits (PKV_DEV_ERR_*)
   int* seq_done;     // [max_batch]: layer completions per sequence (multi-layer launch)
+  unsigned long long* page_marks;   // [num_pages] how often the call's pairs name a page:
+                                    // low half as destination, high half as source
+  int* page_to;                     // [num_pages] 1 + where a page moves (0: it stays); follows
+                                    // page_marks in one allocation
+  int window_blocks_per_sm;         // resident blocks of the windowed decode's ticket shape
+  int window_cluster_blocks_per_sm; // ... and of its cluster shape
   int layer_clusters[5];   // resident clusters of the multi-layer kernel, S = 1, 2, 4, 8, 16
 };
 
@@ -41,6 +47,10 @@ inline pkv_status pkv_check_launch() {
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// Whether the handle is in the range of the entry points limited to
+// 2,048-token contexts (their kernels hold a whole block-table row).
+inline bool pkv_short_context(const pkv_pool* pool) { return pool->cfg.max_seq_len <= 2048; }
+
 // pkv.cu: a K or V pool of num_pages pages as the copy engine's 3-D tensor
 // map (dim, kv head x 16 + token, page), boxes of one (page, kv head) tile
 // with the 128-byte swizzle; false if the driver refuses it.
@@ -49,5 +59,8 @@ bool pkv_pool_tensor_map(const void* pool, int num_pages, CUtensorMap* map);
 // layers.cu: the multi-layer kernel's attributes and, per cluster size, how
 // many of its clusters the device holds at once (pool->layer_clusters).
 bool pkv_layers_setup(pkv_pool* pool);
+
+// window.cu: the windowed decode kernels' attributes and residency.
+bool pkv_window_setup(pkv_pool* pool);
 
 #endif  // PKV_POOL_INTERNAL_H

@@ -60,6 +60,7 @@ struct pkv_sched {
   std::unordered_map<int, Request> requests;
   int next_id = 0;
   pkv_sched_stats stats{};
+  std::vector<int32_t> owners;        // per page: how many requests hold it
 
   int64_t assigned() const { return cfg.num_pages - static_cast<int64_t>(free_heap.size()); }
 
@@ -67,10 +68,13 @@ struct pkv_sched {
     std::pop_heap(free_heap.begin(), free_heap.end(), std::greater<int32_t>());
     const int32_t p = free_heap.back();
     free_heap.pop_back();
+    owners[p] = 1;
     return p;
   }
 
+  // A request lets go of a page; the last owner frees it.
   void give_page(int32_t p) {
+    if (p < 0 || --owners[p] > 0) return;   // -1: given back before (pkv_sched_release)
     free_heap.push_back(p);
     std::push_heap(free_heap.begin(), free_heap.end(), std::greater<int32_t>());
   }
@@ -96,6 +100,7 @@ pkv_status pkv_sched_create(const pkv_sched_config* config, pkv_sched_t* out) {
   s->max_pages_per_seq = config->max_seq_len / config->page_size;
   s->free_heap.resize(static_cast<size_t>(config->num_pages));
   for (int i = 0; i < config->num_pages; ++i) s->free_heap[i] = i;   // sorted: a valid min-heap
+  s->owners.assign(static_cast<size_t>(config->num_pages), 0);
   s->credits = config->num_pages;
   s->stats.pool_pages = config->num_pages;
   *out = s;
@@ -209,6 +214,125 @@ pkv_status pkv_sched_finish(pkv_sched_t s, int request_id) {
   s->active.erase(std::find(s->active.begin(), s->active.end(), request_id));
   s->requests.erase(it);
   ++s->stats.finished;
+  return PKV_OK;
+}
+
+pkv_status pkv_sched_fork(pkv_sched_t s, int request_id, int length, int max_new_tokens,
+                          int* child_id, int32_t* src, int32_t* dst, int capacity, int* count,
+                          int* tokens) {
+  if (!s || !child_id || !src || !dst || !count || !tokens) return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> g(s->lock);
+  *child_id = -1;
+  *count = 0;
+  *tokens = 0;
+  if (capacity < s->cfg.num_layers) return PKV_ERR_INVALID_ARG;
+  auto it = s->requests.find(request_id);
+  if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
+  const int page = s->cfg.page_size;
+  if (length < 1 || length > static_cast<long long>(it->second.pages_per_layer) * page)
+    return PKV_ERR_INVALID_ARG;
+  Request r;
+  r.prompt_tokens = length;
+  if (budget_of(s->cfg, length, max_new_tokens, nullptr, &r.prefix, &r.budget) != PKV_OK)
+    return PKV_ERR_INVALID_ARG;
+  const int shared = length / page;
+  const bool partial = length % page != 0;
+  int64_t holes = 0;   // shared places whose page the parent gave back
+  for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
+    const int32_t* row = it->second.pages.data() + static_cast<size_t>(layer) * s->max_pages_per_seq;
+    holes += std::count(row, row + shared, -1);
+    // a partial page that the parent gave back cannot be copied
+    if (partial && row[shared] < 0) return PKV_ERR_INVALID_ARG;
+  }
+  r.budget -= holes;
+  if (r.budget > s->credits) return PKV_ERR_REJECTED;
+  r.active = true;
+  r.pages.assign(static_cast<size_t>(s->cfg.num_layers) * s->max_pages_per_seq, -1);
+  for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
+    const size_t row = static_cast<size_t>(layer) * s->max_pages_per_seq;
+    for (int i = 0; i < shared; ++i) {
+      const int32_t p = it->second.pages[row + i];
+      r.pages[row + i] = p;
+      if (p >= 0) ++s->owners[p];
+    }
+    if (partial) {
+      r.pages[row + shared] = s->take_page();
+      src[*count] = it->second.pages[row + shared];
+      dst[*count] = r.pages[row + shared];
+      ++*count;
+    }
+  }
+  if (partial) *tokens = length % page;
+  r.pages_per_layer = shared + (partial ? 1 : 0);
+  s->credits -= r.budget;
+  const int id = s->next_id++;
+  s->requests.emplace(id, std::move(r));
+  s->active.push_back(id);
+  ++s->stats.submitted;
+  ++s->stats.admitted;
+  s->stats.peak_active = std::max<int64_t>(s->stats.peak_active, s->active.size());
+  s->stats.peak_assigned_pages = std::max(s->stats.peak_assigned_pages, s->assigned());
+  *child_id = id;
+  return PKV_OK;
+}
+
+pkv_status pkv_sched_release(pkv_sched_t s, int request_id, int first_visible, int sinks,
+                             int* released) {
+  if (!s || first_visible < 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> g(s->lock);
+  if (released) *released = 0;
+  auto it = s->requests.find(request_id);
+  if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
+  Request& r = it->second;
+  const int page = s->cfg.page_size;
+  if (first_visible > static_cast<long long>(r.pages_per_layer) * page) return PKV_ERR_INVALID_ARG;
+  const int begin = sinks / page + (sinks % page != 0 ? 1 : 0);
+  const int end = first_visible / page;
+  int n = 0;
+  for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
+    for (int i = begin; i < end; ++i) {
+      int32_t& p = r.pages[static_cast<size_t>(layer) * s->max_pages_per_seq + i];
+      if (p < 0) continue;
+      s->give_page(p);
+      p = -1;
+      ++n;
+    }
+  }
+  r.budget -= n;
+  s->credits += n;
+  if (released) *released = n;
+  return PKV_OK;
+}
+
+pkv_status pkv_sched_compact(pkv_sched_t s, int32_t* src, int32_t* dst, int capacity,
+                             int* count) {
+  if (!s || !count || capacity < 0 || (capacity > 0 && (!src || !dst))) return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> g(s->lock);
+  *count = 0;
+  // the lowest free ids against the highest assigned ones, until they meet
+  std::sort(s->free_heap.begin(), s->free_heap.end());   // sorted: a valid min-heap
+  std::vector<int32_t> to(s->owners.size(), -1);
+  int n = 0;
+  int32_t high = static_cast<int32_t>(s->owners.size()) - 1;
+  while (n < capacity && n < static_cast<int>(s->free_heap.size())) {
+    while (high >= 0 && s->owners[high] == 0) --high;
+    const int32_t low = s->free_heap[n];
+    if (high < low) break;
+    src[n] = high;
+    dst[n] = low;
+    to[high] = low;
+    s->owners[low] = s->owners[high];
+    s->owners[high] = 0;
+    s->free_heap[n] = high;
+    ++n;
+    --high;
+  }
+  if (n == 0) return PKV_OK;
+  std::sort(s->free_heap.begin(), s->free_heap.end());
+  for (auto& entry : s->requests)
+    for (int32_t& p : entry.second.pages)
+      if (p >= 0 && to[p] >= 0) p = to[p];
+  *count = n;
   return PKV_OK;
 }
 
