@@ -49,6 +49,7 @@ typedef struct {
  * i.e. what pkv_prefill_attention and pkv_window_prefill_attention take.
  * rope_positions: device int32 [num_axes][position_stride], entry [a][i] the
  * position of packed row i on axis a; position_stride >= total_tokens.
+ * rope_positions, cu_tokens and start_pos need 4-byte alignment only.
  * q_out may be q itself (rotated in place) but not overlap it otherwise; q
  * and q_out may both be NULL (keys and values only). k and v must not
  * overlap the pools or q_out.

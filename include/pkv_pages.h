@@ -3,8 +3,8 @@
  * that forked sequences do not share (pkv_sched_fork) and the moves that
  * compact a pool (pkv_sched_compact).
  *
- * src, dst: device int32 [n] page ids (16-byte aligned, as every pointer here).
- * A page may be the source of several pairs. A destination must be named by
+ * src, dst: device int32 [n] page ids (4-byte aligned; the pools and tables 16,
+ * as everywhere). A page may be the source of several pairs. A destination must be named by
  * one pair only and be no pair's source: pairs that break this are skipped
  * and flagged (PKV_ERR_OUT_OF_RANGE from pkv_get_error), the others are
  * carried out, so the result never depends on the order of the copies. Pairs

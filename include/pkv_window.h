@@ -11,7 +11,8 @@
  *
  * Geometry, pools, block tables and dtypes are those of pkv.h and
  * pkv_prefill.h; a handle created with PKV_FLAG_LONG_CONTEXT raises
- * max_seq_len. Pages that hold no visible token are never read and their
+ * max_seq_len. Lists of int32 (seq_lens, cu_tokens, start_pos, rope_positions)
+ * need 4-byte alignment only. Pages that hold no visible token are never read and their
  * block-table entries may hold anything (-1 after pkv_sched_release). Inside
  * a page that is read, tokens that no query of the sequence sees may hold any
  * bits, NaN and infinities included; visible K and V are finite.

@@ -217,6 +217,10 @@ class Pool:
         self.handle = handle
         self.config = config
         self.device = device     # CUDA device index, where known
+        # elements of a pool tensor and entries of the block tables
+        self.elements = config.num_pages * NUM_KV_HEADS * PAGE_SIZE * HEAD_DIM if config else 0
+        self.entries = config.num_layers * config.max_batch * \
+            (config.max_seq_len // PAGE_SIZE) if config else 0
         self._lib = lib
 
     def close(self):
@@ -426,26 +430,32 @@ def pkv_prefill(pool: Pool, layer, q, k, v, k_pool, v_pool, block_tables, cu_tok
 
 
 # ---------------------------------------------------------------- window, axes, pages
+_torch_dtypes = {}
+
+
 def _arg(pool, name, x, count=0):
     """Address of a tensor argument: what _addr checks, and that the tensor lies
     on the handle's device and holds at least `count` elements."""
     if x is None or type(x) is int:
         return x
+    if x.dtype is _torch_dtypes.get(name) and x.get_device() == pool.device and \
+            x.numel() >= count and x.is_contiguous():
+        return x.data_ptr()
     address = _addr(x, _DTYPES[name], name)
     if pool.device is not None and x.get_device() != pool.device:
         raise ValueError(f"{name}: expected a tensor on cuda:{pool.device}, got {x.device}")
     if x.numel() < count:
         raise ValueError(f"{name}: expected at least {count} elements, got {x.numel()}")
+    _torch_dtypes[name] = x.dtype     # the one that _addr accepts
     return address
 
 
-def _table_entries(pool):
-    c = pool.config
-    return c.num_layers * c.max_batch * (c.max_seq_len // PAGE_SIZE) if c else 0
-
-
-def _pool_elements(pool):
-    return pool.config.num_pages * NUM_KV_HEADS * PAGE_SIZE * HEAD_DIM if pool.config else 0
+def _pool_stream(pool, stream):
+    """The stream's handle; by default the current stream of the handle's device."""
+    if stream is None and pool.device is not None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(pool.device)
+    return _stream(stream)
 
 
 class AxesRope:
@@ -501,12 +511,12 @@ def pkv_window_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, seq
     rows = batch * NUM_Q_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_attention(
         pool.handle, int(layer), _arg(pool, "q", q, rows),
-        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
-        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
         int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
-        _stream(stream))
+        _pool_stream(pool, stream))
     _check(st, "pkv_window_attention")
 
 
@@ -519,12 +529,12 @@ def pkv_window_append_attend(pool: Pool, layer, q, k, v, k_pool, v_pool, block_t
     rows, new = batch * NUM_Q_HEADS * HEAD_DIM, batch * NUM_KV_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_append_attend(
         pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
-        _arg(pool, "v", v, new), _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
-        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "v", v, new), _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
         int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
-        _stream(stream))
+        _pool_stream(pool, stream))
     _check(st, "pkv_window_append_attend")
 
 
@@ -538,12 +548,12 @@ def pkv_window_prefill_attention(pool: Pool, layer, q, k_pool, v_pool, block_tab
     rows = total * NUM_Q_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_prefill_attention(
         pool.handle, int(layer), _arg(pool, "q", q, rows),
-        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
-        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
         _arg(pool, "out", out, rows), int(window), int(sinks), batch, total,
-        int(max_chunk_tokens), _stream(stream))
+        int(max_chunk_tokens), _pool_stream(pool, stream))
     _check(st, "pkv_window_prefill_attention")
 
 
@@ -561,12 +571,12 @@ def pkv_prefill_fill_axes(pool: Pool, layer, q, k, v, q_out, k_pool, v_pool, blo
     st = pool._lib.pkv_prefill_fill_axes(
         pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
         _arg(pool, "v", v, new), _arg(pool, "q_out", q_out, rows),
-        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
-        _arg(pool, "block_tables", block_tables, _table_entries(pool)),
+        _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
         *_rope_args(pool, rope, rope_positions, total), batch, total, int(max_chunk_tokens),
-        _stream(stream))
+        _pool_stream(pool, stream))
     _check(st, "pkv_prefill_fill_axes")
 
 
@@ -576,8 +586,8 @@ def pkv_copy_pages(pool: Pool, src, dst, k_pool, v_pool, tokens=None, n=None, st
     n = int(src.shape[0]) if n is None else int(n)
     st = pool._lib.pkv_copy_pages(
         pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
-        _arg(pool, "tokens", tokens, n), _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)), n, _stream(stream))
+        _arg(pool, "tokens", tokens, n), _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements), n, _pool_stream(pool, stream))
     _check(st, "pkv_copy_pages")
 
 
@@ -587,9 +597,9 @@ def pkv_compact_pages(pool: Pool, src, dst, k_pool, v_pool, block_tables, n=None
     n = int(src.shape[0]) if n is None else int(n)
     st = pool._lib.pkv_compact_pages(
         pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
-        _arg(pool, "k_pool", k_pool, _pool_elements(pool)),
-        _arg(pool, "v_pool", v_pool, _pool_elements(pool)),
-        _arg(pool, "block_tables", block_tables, _table_entries(pool)), n, _stream(stream))
+        _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries), n, _pool_stream(pool, stream))
     _check(st, "pkv_compact_pages")
 
 

@@ -139,7 +139,7 @@ extern "C" pkv_status pkv_prefill_fill_axes(pkv_pool_t pool, int layer, const vo
     return PKV_ERR_INVALID_ARG;
   if (!pkv_aligned16(q) || !pkv_aligned16(k) || !pkv_aligned16(v) || !pkv_aligned16(q_out) ||
       !pkv_aligned16(k_pool) || !pkv_aligned16(v_pool) || !pkv_aligned16(block_tables) ||
-      !pkv_aligned16(cu_tokens) || !pkv_aligned16(start_pos))
+      !pkv_aligned4(cu_tokens) || !pkv_aligned4(start_pos))
     return PKV_ERR_INVALID_ARG;
   FillParams prm;
   const pkv_status st = make_axes_args(rope, rope_positions, position_stride, total_tokens,

@@ -33,7 +33,7 @@ inline pkv_status make_axes_args(const pkv_axes_rope* rope, const int32_t* posit
   if (!rope || !rope->cos || !rope->sin || !positions || rope->rows < 1 || rope->num_axes < 1 ||
       rope->num_axes > PKV_MAX_AXES || stride < tokens)
     return PKV_ERR_INVALID_ARG;
-  if (!pkv_aligned16(rope->cos) || !pkv_aligned16(rope->sin) || !pkv_aligned16(positions))
+  if (!pkv_aligned16(rope->cos) || !pkv_aligned16(rope->sin) || !pkv_aligned4(positions))
     return PKV_ERR_INVALID_ARG;
   unsigned long long axes = 0;
   for (int i = 0; i < kPairs; ++i) {

@@ -94,6 +94,35 @@ __device__ __forceinline__ uint32_t float2_to_bf16x2(float e0, float e1) {
   return w;
 }
 
+// x - (a BF16 half of the pair h), exact where h holds x truncated: one mixed
+// precision instruction on the FMA pipe, where masking h out of x and a
+// subtraction would load the busier ALU pipe.
+template <int kUpper>
+__device__ __forceinline__ float rest_of(float x, uint32_t h) {
+  float d;
+  if (kUpper)
+    asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %1;\n\tmov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, u, m, %2;\n\t}"
+        : "=f"(d)
+        : "r"(h), "f"(x));
+  else
+    asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %1;\n\tmov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, l, m, %2;\n\t}"
+        : "=f"(d)
+        : "r"(h), "f"(x));
+  return d;
+}
+
+// x = hi + mid + lo in BF16, 24 bits: hi and mid truncated (their differences
+// are exact), lo rounded; two values at a time, packed as BF16 pairs.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
+  hi = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+  const float r0 = rest_of<0>(x0, hi), r1 = rest_of<1>(x1, hi);
+  mid = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+  lo = float2_to_bf16x2(rest_of<0>(r0, mid), rest_of<1>(r1, mid));
+}
+
 }  // namespace pkv_dev
 
 #endif  // PKV_DEVICE_COMMON_CUH

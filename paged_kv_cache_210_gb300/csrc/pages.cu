@@ -119,7 +119,7 @@ pkv_status launch_copies(pkv_pool_t pool, const int32_t* src, const int32_t* dst
   if (n < 0 || n > c.num_pages) return PKV_ERR_INVALID_ARG;
   if (n == 0) return PKV_OK;
   if (!src || !dst || !k_pool || !v_pool || (compact && !tables)) return PKV_ERR_INVALID_ARG;
-  if (!pkv_aligned16(src) || !pkv_aligned16(dst) || !pkv_aligned16(tokens) ||
+  if (!pkv_aligned4(src) || !pkv_aligned4(dst) || !pkv_aligned4(tokens) ||
       !pkv_aligned16(k_pool) || !pkv_aligned16(v_pool) || !pkv_aligned16(tables))
     return PKV_ERR_INVALID_ARG;
   if (n > (1 << 30)) return PKV_ERR_INVALID_ARG;

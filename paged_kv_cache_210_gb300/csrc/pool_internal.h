@@ -43,6 +43,9 @@ enum : int {
 // Host helpers of the entry points.
 inline bool pkv_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Lists of int32 that the kernels read one by one.
+inline bool pkv_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline pkv_status pkv_check_launch() {
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

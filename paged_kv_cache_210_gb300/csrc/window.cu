@@ -35,6 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStagesW = 3;
 constexpr int kThreadsW = kWarps * 32;
+constexpr int kTries = 8;             // range sizes tried for a one-wave launch
+constexpr int kHeld = 3;              // sequences per thread whose page count is kept
 
 struct alignas(1024) WindowSmem {
   PageRing<kStagesW> warp[kWarps];
@@ -42,6 +44,14 @@ struct alignas(1024) WindowSmem {
   float m[kWarps][kGroup];
   float l[kWarps][kGroup];
   float acc[kWarps][kGroup][kDim];   // the warps' partial outputs (block merge)
+  struct {                           // unit search
+    float pages[kWarps];
+    int most[kWarps];
+    int full[kWarps];
+    uint32_t c12[kWarps], c34[kWarps];
+    int count[2][kWarps];
+    int seq, split;
+  } find;
   int last;
 };
 static_assert(4 * (sizeof(WindowSmem) + 1024 + 1024) <= kSmemPerSm, "4 ticket blocks per SM");
@@ -66,7 +76,11 @@ struct WindowParams {
   int table_stride;
   int max_seq_len;
   int max_splits;
-  int num_splits;             // ranges per sequence (and gridDim.x)
+  int num_splits;             // > 0: ranges per sequence (and gridDim.x); 0: units (below)
+  int batch;
+  int wave_units;             // units: > 0: batch <= 32 kHeld, try to keep to this many
+  int range_div;              // units: ranges of about (the batch's pages) / range_div pages
+  int least_pages;            // ranges have at least this many pages
   int window;                 // 1 .. max_seq_len
   int sinks;                  // 0 .. max_seq_len
   AxesArgs rope;
@@ -86,20 +100,6 @@ __device__ __forceinline__ void mma_rows16(float (&d)[4], uint32_t a0, uint32_t 
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// x = hi + mid + lo with hi and mid truncated to BF16 (exact differences) and
-// lo rounded: two values at a time, packed as BF16 pairs.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid,
-                                       uint32_t& lo) {
-  const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
-  hi = __byte_perm(b0, b1, 0x7632);
-  const float r0 = x0 - __uint_as_float(b0 & 0xffff0000u);
-  const float r1 = x1 - __uint_as_float(b1 & 0xffff0000u);
-  const uint32_t c0 = __float_as_uint(r0), c1 = __float_as_uint(r1);
-  mid = __byte_perm(c0, c1, 0x7632);
-  lo = float2_to_bf16x2(r0 - __uint_as_float(c0 & 0xffff0000u),
-                        r1 - __uint_as_float(c1 & 0xffff0000u));
 }
 
 // The queries as A fragments: lane L serves head (L / 4) % 4, dims 16 (L % 4)
@@ -141,6 +141,17 @@ __device__ __forceinline__ void load_queries(const uint16_t* qrow, int lane, flo
   }
 }
 
+// A warp's running softmax state: o[j] holds dims 8 j + 2 q, + 1 (q = lane % 4)
+// of its row's part. A page's products start from zero and are added here: a
+// tensor-core sum drops the bits below its accumulator's last one, always
+// downwards, which over a long context adds up (1.8e-6 of the output after
+// 131,072 tokens with the accumulator kept in the product, against 3e-7).
+struct PageState {
+  float o[8][2];
+  float m_run;     // base-2 max the exponentials of the head are taken against
+  float l_run;     // this lane's share of the head's sum
+};
+
 // One page: K tile kt and V tile vt (swizzled, in shared memory), bit t of
 // `seen` = token t counts (at least one does). The scores of the others are
 // dropped by select; their V rows must hold finite values. Lanes L and L + 16
@@ -148,7 +159,7 @@ __device__ __forceinline__ void load_queries(const uint16_t* qrow, int lane, flo
 template <bool kRope>
 __device__ __forceinline__ void attend_page(const uint8_t* kt, const uint8_t* vt, uint32_t seen,
                                             int lane, const uint32_t (&qa)[8],
-                                            const uint32_t (&ql)[8], MmaState& st) {
+                                            const uint32_t (&ql)[8], PageState& st) {
   const int g8 = lane >> 2;
   const int qq = lane & 3;
   float s[4];
@@ -188,13 +199,10 @@ __device__ __forceinline__ void attend_page(const uint8_t* kt, const uint8_t* vt
     const float alpha = grow ? fast_exp2(st.m_run - pm) : 1.f;   // 0 on the first page
     if (grow) st.m_run = pm;
     st.l_run *= alpha;
-    // the accumulators' rows belong to the same head in every lane
     #pragma unroll
     for (int j = 0; j < 8; ++j) {
       st.o[j][0] *= alpha;
       st.o[j][1] *= alpha;
-      st.o[j][2] *= alpha;
-      st.o[j][3] *= alpha;
     }
   }
   const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
@@ -220,14 +228,223 @@ __device__ __forceinline__ void attend_page(const uint8_t* kt, const uint8_t* vt
   for (int jj = 0; jj < 4; ++jj) {
     uint32_t bv[4];
     ldsm_x4_trans(bv, vrow + (((2 * jj + (mat >> 1)) ^ mrow) << 4));
-    mma_rows16(st.o[2 * jj], pa[0], pl[0], pa[1], pl[1], bv[0], bv[1]);
-    mma_rows16(st.o[2 * jj + 1], pa[0], pl[0], pa[1], pl[1], bv[2], bv[3]);
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_rows16(d, pa[0], pl[0], pa[1], pl[1], bv[2 * h], bv[2 * h + 1]);
+      // rows g (high or middle parts) and g + 8 (low parts) of the same head
+      st.o[2 * jj + h][0] += d[0] + d[2];
+      st.o[2 * jj + h][1] += d[1] + d[3];
+    }
   }
 }
 
 // The lowest n bits (n clamped to 0 .. 16).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= kPage ? 0xffffu : (1u << n) - 1u;
+}
+
+// The visible pages of a sequence: the sink pages [0, sinks) and the window's
+// [window, window + count - sinks), `count` in all.
+struct SeenPages {
+  int sinks, window, count, first_token;
+  __device__ SeenPages(int len, const WindowParams& prm) {
+    first_token = max(len - prm.window, 0);
+    window = first_token / kPage;
+    sinks = min((prm.sinks + kPage - 1) / kPage, window);
+    count = sinks + (len + kPage - 1) / kPage - window;
+  }
+};
+
+// ---------------------------------------------------------------- units
+// Larger batches launch a grid of (sequence, range) units instead of a fixed
+// number of splits per sequence, whose blocks would be idle for short
+// sequences and uneven for long ones. The range size comes from the lengths
+// the launch finds; a sequence of p visible pages has ceil(p / range) units,
+// the last of which may be short. With T the batch's visible pages:
+//  * a batch that may fit one wave of resident blocks (wave_units > 0) takes
+//    the smallest range of r0 (8 + k) / 8, r0 = T / wave_units, k < 8, whose
+//    units fit it: a second wave of full ranges costs more than longer ranges
+//    (32 sequences at a 1,024-token window: 15.2 us in one wave, 19.7 in two);
+//  * others take T / range_div, but at least least_pages.
+// So there are fewer than batch + range_div units, or at most wave_units.
+// They are handed out largest first (all full ranges, then the short ones by
+// quarters of a range), so what does not fit the first wave is short (256
+// ragged sequences behind 4,096 tokens: 105.9 us, in batch order 124.2). Each
+// block finds its own unit: sums over the batch, the class of size the unit
+// falls into, and a prefix sum within it. Padding rows have no units; a
+// length out of range has one, which reports it.
+//
+// kBlock: the block's threads share the batch, kHeld sequences each kept in
+// registers, the rest read again; otherwise (batch <= 32 kHeld) every warp
+// does it all without a barrier, which a small batch's latency would show.
+// Called by every thread of the block; false past the last unit.
+template <bool kBlock>
+__device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, WindowSmem& sm, int& b,
+                                          int& split, int& range) {
+  constexpr int kGroupSize = kBlock ? kThreadsW : 32;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int me = kBlock ? static_cast<int>(threadIdx.x) : lane;
+  auto pages_of = [&](int s) {
+    if (s >= prm.batch) return 0;
+    const int len = prm.seq_lens[s];
+    if (len == 0) return 0;
+    return len < 0 || len > prm.max_seq_len ? 1 : SeenPages(len, prm).count;
+  };
+  // fn(e, pages) for every sequence of this thread; e: its register, or -1
+  int held[kHeld];
+  #pragma unroll
+  for (int e = 0; e < kHeld; ++e) held[e] = pages_of(me + e * kGroupSize);
+  auto each = [&](auto fn) {
+    #pragma unroll
+    for (int e = 0; e < kHeld; ++e) fn(held[e]);
+    if (kBlock)
+      for (int s = me + kHeld * kGroupSize; s < prm.batch; s += kGroupSize) fn(pages_of(s));
+  };
+  // exact quotients of p <= 65,538 pages by r: the reciprocal's error stays
+  // below the half added
+  auto ceil_of = [](int p, float r, float inv) {
+    return static_cast<int>((static_cast<float>(p) + r - 0.5f) * inv);
+  };
+  float sum = 0.f;                            // pages: exact to 2^24, then to 2^-22 of itself
+  int most = 0;
+  each([&](int p) {
+    sum += static_cast<float>(p);
+    most = max(most, p);
+  });
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (kBlock) {
+    if (lane == 0) {
+      sm.find.pages[warp] = sum;
+      sm.find.most[warp] = most;
+    }
+    __syncthreads();
+    sum = 0.f;
+    #pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sum += sm.find.pages[w];
+      most = max(most, sm.find.most[w]);
+    }
+  }
+  // T / by, rounded up past the float error (ranges stay below 2^17 pages)
+  auto share = [&](int by) {
+    return static_cast<int>(fminf(__fdividef(sum, static_cast<float>(by)), 131072.f)) + 1;
+  };
+  range = max(prm.least_pages, share(prm.range_div));
+  if (!kBlock) {
+    const int r0 = max(prm.least_pages, share(prm.wave_units));
+    #pragma unroll
+    for (int k = kTries - 1; k >= 0; --k) {
+      const int r = (r0 * (kTries + k) + kTries - 1) / kTries;
+      const float fr = static_cast<float>(r), inv = __frcp_rn(fr);
+      int units = 0;
+      #pragma unroll
+      for (int e = 0; e < kHeld; ++e) units += ceil_of(held[e], fr, inv);
+      if (static_cast<int>(__reduce_add_sync(0xffffffffu, units)) <= prm.wave_units) range = r;
+    }
+  }
+  range = min(range, max(most, 1));
+  const float f_range = static_cast<float>(range), inv_range = __frcp_rn(f_range);
+  // a sequence's full ranges and the class of what is left: 1 (longest) .. 4, 0: nothing
+  auto classify = [&](int p, int& full) {
+    full = ceil_of(p + 1, f_range, inv_range) - 1;
+    const int rest = p - full * range;
+    return rest > 0 ? 4 - static_cast<int>((4.f * rest - 0.5f) * inv_range) : 0;
+  };
+  int full = 0;
+  uint32_t c12 = 0, c34 = 0;                 // two 16-bit counts each (batch <= 65535)
+  each([&](int p) {
+    int f;
+    const int c = classify(p, f);
+    full += f;
+    c12 += c == 1 ? 1u : c == 2 ? 0x10000u : 0u;
+    c34 += c == 3 ? 1u : c == 4 ? 0x10000u : 0u;
+  });
+  full = __reduce_add_sync(0xffffffffu, full);
+  c12 = __reduce_add_sync(0xffffffffu, c12);
+  c34 = __reduce_add_sync(0xffffffffu, c34);
+  if (kBlock) {
+    if (lane == 0) {
+      sm.find.full[warp] = full;
+      sm.find.c12[warp] = c12;
+      sm.find.c34[warp] = c34;
+    }
+    __syncthreads();
+    full = 0;
+    c12 = c34 = 0;
+    #pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      full += sm.find.full[w];
+      c12 += sm.find.c12[w];
+      c34 += sm.find.c34[w];
+    }
+  }
+  const int sizes[5] = {full, static_cast<int>(c12 & 0xffffu), static_cast<int>(c12 >> 16),
+                        static_cast<int>(c34 & 0xffffu), static_cast<int>(c34 >> 16)};
+  int cls = -1;
+  #pragma unroll
+  for (int c = 0; c < 5; ++c) {
+    if (cls < 0) {
+      if (u < sizes[c]) {
+        cls = c;
+      } else {
+        u -= sizes[c];
+      }
+    }
+  }
+  if (cls < 0) return false;                 // the same decision in every thread
+  int before = 0;
+  for (int base = 0, turn = 0; base < prm.batch; base += kGroupSize, turn ^= 1) {
+    const int e = base / kGroupSize;
+    int pages = held[0];
+    #pragma unroll
+    for (int h = 1; h < kHeld; ++h) pages = e == h ? held[h] : pages;
+    if (kBlock && e >= kHeld) pages = pages_of(base + me);
+    int f;
+    const int c = classify(pages, f);
+    const int units = cls == 0 ? f : c == cls ? 1 : 0;
+    int incl = units;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    int total = __shfl_sync(0xffffffffu, incl, 31), excl = before + incl - units;
+    if (kBlock) {
+      if (lane == 0) sm.find.count[turn][warp] = total;
+      __syncthreads();
+      total = 0;
+      #pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int cw = sm.find.count[turn][w];
+        excl += w < warp ? cw : 0;
+        total += cw;
+      }
+    }
+    if (u < before + total) {                // the same decision in every thread
+      const bool mine = u >= excl && u < excl + units;
+      const int at = cls == 0 ? u - excl : f;
+      if (kBlock) {
+        if (mine) {
+          sm.find.seq = base + me;
+          sm.find.split = at;
+        }
+        __syncthreads();
+        b = sm.find.seq;
+        split = sm.find.split;
+      } else {
+        const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        b = base + from;
+        split = __shfl_sync(0xffffffffu, at, from);
+      }
+      return true;
+    }
+    before += total;
+  }
+  return false;
 }
 
 // ---------------------------------------------------------------- decode
@@ -242,15 +459,23 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   WindowSmem& sm = *reinterpret_cast<WindowSmem*>(smem_base);
   AsyncInbox& inbox = *reinterpret_cast<AsyncInbox*>(smem_base + sizeof(WindowSmem));
 
-  const int split = blockIdx.x;
-  const int kvh = blockIdx.y;
-  const int b = blockIdx.z;
+  const bool units = !kCluster && prm.num_splits == 0;   // grid (units x kv heads)
+  int split = blockIdx.x;
+  const int kvh = units ? blockIdx.x % kHkv : blockIdx.y;
+  int b = blockIdx.z;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   // Before the wait (programmatic dependent launch) this block reads only
   // seq_lens, the block table, the rotary inputs and pool rows below the
   // appended position.
+  int range = 0;
+  if (units) {
+    const int u = static_cast<int>(blockIdx.x) / kHkv;
+    if (!(prm.wave_units > 0 ? find_unit<false>(u, prm, sm, b, split, range)
+                             : find_unit<true>(u, prm, sm, b, split, range)))
+      return;
+  }
   const int len = prm.seq_lens[b];
   if (len == 0) return;                                  // a padding row
   if (len < 0 || len > prm.max_seq_len) {
@@ -262,12 +487,12 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrPosition);
     return;                                              // every block of the sequence
   }
-  const int n_pages = (len + kPage - 1) / kPage;
-  const int win_lo = max(len - prm.window, 0);           // first token of the window
-  const int win_page = win_lo / kPage;
-  const int sink_pages = min((prm.sinks + kPage - 1) / kPage, win_page);
-  const int n_seen = sink_pages + n_pages - win_page;    // visible pages, >= 1
-  const int chunk = (n_seen + prm.num_splits - 1) / prm.num_splits;
+  const SeenPages see(len, prm);
+  const int sink_pages = see.sinks;
+  const int win_page = see.window;
+  const int win_lo = see.first_token;
+  const int n_seen = see.count;                          // >= 1
+  const int chunk = prm.num_splits > 0 ? (n_seen + prm.num_splits - 1) / prm.num_splits : range;
   const int n_splits = (n_seen + chunk - 1) / chunk;     // non-empty splits of this sequence
   if (kCluster) {
     if (n_splits == 1 && split > 0) return;   // the same decision in every block of the cluster
@@ -394,8 +619,11 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   load_queries<kRope>(prm.q + (static_cast<size_t>(b) * kHq + kvh * kGroup) * kDim, lane, ang_c,
                       ang_s, qa, ql);
 
-  MmaState st;
-  st.reset();
+  PageState st;
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) st.o[j][0] = st.o[j][1] = 0.f;
+  st.m_run = -INFINITY;
+  st.l_run = 0.f;
   int issued = n_prefetch;
   int consumed = 0;
   bool timed_out = false;
@@ -456,18 +684,21 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     st.l_run = 0.f;
   }
 
-  // the three parts' accumulators of a head: rows g, g + 4 (lane + 16), g + 8
+  // lanes L and L + 16 hold the parts of the same head
+  MmaState total;
   #pragma unroll
   for (int j = 0; j < 8; ++j) {
     #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float o = st.o[j][e] + st.o[j][e + 2];
-      st.o[j][e] = o + __shfl_xor_sync(0xffffffffu, o, 16);
+      total.o[j][e] = st.o[j][e] + __shfl_xor_sync(0xffffffffu, st.o[j][e], 16);
+      total.o[j][e + 2] = 0.f;
     }
   }
+  total.m_run = st.m_run;
+  total.l_run = st.l_run;
   float M, L;
   float2 O;
-  block_merge_mma<kWarps>(sm, st, warp, lane, M, L, O);
+  block_merge_mma<kWarps>(sm, total, warp, lane, M, L, O);
   float* out_kv = prm.out + (static_cast<size_t>(b) * kHq + kvh * kGroup) * kDim;
   if (kCluster && n_splits > 1) {
     cluster_merge_async(inbox, M, L, O, warp, lane, out_kv, prm.err);
@@ -497,21 +728,53 @@ WindowKernel window_kernel(bool fused, bool rope) {
                        : window_decode_kernel<false, kCluster, false>);
 }
 
-// Splits per sequence and whether they form a cluster. Enough blocks for one
-// wave of resident ones, but at least 4 pages (one per warp) per block.
-void plan_window(const pkv_pool* pool, int batch, int window, int sinks, int num_splits,
-                 int* splits, bool* cluster) {
+// The launch: splits per sequence (a cluster, or a ticket), or units.
+struct WindowPlan {
+  int num_splits;   // 0: units
+  bool cluster;
+  int units;        // units in the grid
+  int wave_units;
+  int range_div;
+  int least_pages;
+};
+
+// Small batches take a cluster per (sequence, kv head): its merge is shorter
+// than the ticket's (us, one 2,048-token sequence: cluster of 12 5.8, units
+// 6.8; 4 sequences at a 1,024-token window: 6.0 and 6.9), as long as all blocks
+// are resident at once (4 sequences, cluster of 16: 9.4) and either fill half
+// of the slots or have few pages (one 131,072-token sequence: cluster of 12
+// 120.6, units 48.0). Everything else takes units.
+constexpr int kMostCluster = 12;
+
+WindowPlan plan_window(const pkv_pool* pool, int batch, int window, int sinks, int num_splits) {
   const pkv_pool_config& c = pool->cfg;
   const int max_pages = c.max_seq_len / kPage;
+  // the most pages a sequence can see
   const int seen = std::min(max_pages, (sinks + kPage - 1) / kPage + (window - 1) / kPage + 2);
-  int s = num_splits;
-  if (s == 0) {
-    const int rows = batch * kHkv;
-    const int fill = std::max(1, pool->window_blocks_per_sm * pool->num_sms / rows);
-    s = std::max(1, std::min({fill, (seen + kWarps - 1) / kWarps, c.max_splits}));
+  WindowPlan p = {};
+  if (num_splits > 0) {
+    p.num_splits = num_splits;
+    p.cluster = num_splits >= 2 && num_splits <= pool->max_cluster;
+    return p;
   }
-  *splits = s;
-  *cluster = s >= 2 && s <= pool->max_cluster;
+  const long long rows = static_cast<long long>(batch) * kHkv;
+  const long long cluster_slots =
+      static_cast<long long>(pool->window_cluster_blocks_per_sm) * pool->num_sms;
+  const int s = std::min({kMostCluster, pool->max_cluster, c.max_splits,
+                          (seen + kWarps - 1) / kWarps});
+  if (s >= 2 && rows * s <= cluster_slots &&
+      (seen <= 4 * kWarps * s || 2 * rows * s >= cluster_slots)) {
+    p.num_splits = s;
+    p.cluster = true;
+    return p;
+  }
+  const int wave = std::max(1, pool->window_blocks_per_sm * pool->num_sms / kHkv);
+  const int fewest = (seen + c.max_splits - 1) / c.max_splits;   // keeps to max_splits ranges
+  if (batch <= std::min(wave, 32 * kHeld)) p.wave_units = wave;
+  p.range_div = std::max(1, 3 * wave / 5);
+  p.least_pages = std::max(2 * kWarps, fewest);
+  p.units = std::max(p.wave_units, batch + p.range_div);
+  return p;
 }
 
 template <bool kFused>
@@ -530,7 +793,7 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
   if (!q || !k_pool || !v_pool || !block_tables || !seq_lens || !out || (kFused && (!k || !v)))
     return PKV_ERR_INVALID_ARG;
   if (!pkv_aligned16(q) || !pkv_aligned16(k) || !pkv_aligned16(v) || !pkv_aligned16(k_pool) ||
-      !pkv_aligned16(v_pool) || !pkv_aligned16(block_tables) || !pkv_aligned16(seq_lens) ||
+      !pkv_aligned16(v_pool) || !pkv_aligned16(block_tables) || !pkv_aligned4(seq_lens) ||
       !pkv_aligned16(out))
     return PKV_ERR_INVALID_ARG;
   WindowParams prm = {};
@@ -561,11 +824,17 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
   prm.max_splits = c.max_splits;
   prm.window = std::min(window, c.max_seq_len);
   prm.sinks = std::min(sinks, c.max_seq_len);
-  bool cluster = false;
-  plan_window(pool, batch, prm.window, prm.sinks, num_splits, &prm.num_splits, &cluster);
+  const WindowPlan plan = plan_window(pool, batch, prm.window, prm.sinks, num_splits);
+  const bool cluster = plan.cluster;
+  prm.num_splits = plan.num_splits;
+  prm.batch = batch;
+  prm.wave_units = plan.wave_units;
+  prm.range_div = plan.range_div;
+  prm.least_pages = plan.least_pages;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(prm.num_splits, kHkv, batch);
+  cfg.gridDim = plan.num_splits > 0 ? dim3(plan.num_splits, kHkv, batch)
+                                    : dim3(plan.units * kHkv, 1, 1);
   cfg.blockDim = dim3(kThreadsW, 1, 1);
   cfg.dynamicSmemBytes = cluster ? kClusterSmemBytes : kTicketSmemBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);

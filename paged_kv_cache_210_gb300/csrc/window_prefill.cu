@@ -6,24 +6,43 @@
 // the tokens visible from position p_i: one pass per 64-token query tile
 // with a running maximum m_i and sum per row.
 //
-// Like the full-context kernel (prefill.cu) one CTA takes a (sequence, kv
-// head, 64-token tile): 256 rows (token x 4 heads) in two halves of 128, K and
-// V steps of 64 keys (4 pages) brought by two loader warps, scores and
-// values on tcgen05 with accumulators in tensor memory, and eight softmax
-// warps with one row per thread. What the window changes:
+// Like the full-context kernel (prefill.cu) a CTA takes the rows (token x 4
+// heads) of a query tile of one (sequence, kv head), K and V come in steps of
+// 64 keys (4 pages) by two loader warps, scores and values run on tcgen05 with
+// accumulators in tensor memory, and the softmax warps hold one row per
+// thread. What is different, and why:
 //  * the steps of a tile are those that hold a visible key: the sink steps and
 //    the window's steps. Pages in them without a visible token, or with an
 //    invalid id, are read as a page past the pool's end, which the copy
 //    engine fills with zeros, so every step moves the same bytes;
-//  * page ids come straight from the block table, one step ahead, so the
-//    context's length does not appear in shared memory;
-//  * a step's row masks are 64-bit words, built only in steps on an edge (the
-//    diagonal, the window's start, the sinks' end) or with an invalid page;
-//  * probabilities enter the value product as three BF16 terms (24 bits): a
-//    score tile of 64 columns becomes 96 columns of P, so two tiles per row
-//    half are held (2 x 2 x 96 columns, and 2 x 64 for O, fill the 512). A
-//    tile is free again once its value product is done, which takes less
-//    than the softmax of the other tile.
+//  * page ids come straight from the block table, eight steps at a time, so
+//    the context's length does not appear in shared memory;
+//  * a tile has 32 tokens (128 rows) and two CTAs share an SM: behind a window
+//    a tile is a few steps long, and one CTA's start and end run under the
+//    other's steps;
+//  * probabilities enter the value product as three BF16 terms (24 bits) in
+//    columns of their own (S 64, P 96 and O 64 of the CTA's 256), so the next
+//    step's scores are computed as soon as this step's are in registers;
+//  * O leaves tensor memory every kSegment steps and is added up in FP32 in
+//    registers: a tensor-core sum drops the bits below its accumulator's last
+//    one, always downwards, 12 times a step, which over a 4,096-token window
+//    came to 1.5e-5 of the output (1e-6 with segments).
+//
+// What bounds it: the softmax warps, two per scheduler. A step's arithmetic
+// (maximum, exponentials, sums, the split into three terms) takes two warps
+// 1,200 cycles by itself, measured alone; with the hand-offs it is about 2,000,
+// against 1,024 of the tensor pipe (two CTAs' 16 products of 32 cycles). Two
+// 4,096-token chunks behind a 4,096-token window: 520 us (530 TFLOP/s of score
+// and value products counted once); eight prompts of up to 2,048 tokens behind
+// 512: 159 us, of which a third is the start and end of the 8-step tiles. What
+// was measured on the way to the first of these: 718 us as a plain port of the
+// step loop; 696 with the products issued by a converged warp (one thread in a
+// divergent branch takes 55 cycles an issue for its operands); 654 with the
+// split's subtractions in mixed precision; 613 with O summed in registers
+// (192 a thread, setmaxnreg) instead of shared memory; 534 with one
+// hand-over of P per step, one flag instead of a step's edge tests and
+// failure paths placed out of line; 520 with page ids fetched ahead. Two
+// threads per row (16 warps) took 10 % longer than one at the same stage.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -44,43 +63,50 @@ using namespace pkv_prefill_dev;
 
 namespace {
 
-constexpr int kRowHalves = 2;                        // MMAs of M = 128 rows per CTA
-constexpr int kHalfRows = 128;
-constexpr int kRows = kRowHalves * kHalfRows;        // 256 rows: token x head
-constexpr int kTileTokens = kRows / kGroup;          // 64 query tokens per CTA
+constexpr int kRows = 128;                           // an MMA's M: token x head
+constexpr int kTileTokens = kRows / kGroup;          // 32 query tokens per CTA
 constexpr int kStepKeys = 64;                        // keys per step: the S MMA's N
 constexpr int kStepPages = kStepKeys / kPage;        // 4
-constexpr int kSoftmaxWarps = 4 * kRowHalves;        // one per (lane quarter, row half)
-constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kLoadWarp = kSoftmaxWarps;             // Q and K copies, then V (+ 1)
-constexpr int kScoreWarp = kSoftmaxWarps + 2;
-constexpr int kValueWarp0 = kSoftmaxWarps + 3;       // one per row half
-constexpr int kThreads = kSoftmaxThreads + 96 + 32 * kRowHalves;
-constexpr int kKStages = 6;
-constexpr int kVStages = 5;
-constexpr int kSTiles = 2;                           // score (then P) tiles per row half
-constexpr int kTileCols = 96;                        // S: 64 columns; P: 3 parts x 32 columns
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = kSTiles * kRowHalves * kTileCols;   // O of row half h at + 64 h
-static_assert(kTmemO + kRowHalves * kDim == kTmemCols, "tensor memory is filled exactly");
+constexpr int kHalfKeys = kStepKeys / 2;             // keys of one P hand-over
+constexpr int kSoftmaxThreads = kRows;
+constexpr int kSoftmaxWarps = 4;                     // one per tensor-memory lane quarter
+constexpr int kLoadWarp = 4;                         // Q and K copies, then V (+ 1)
+constexpr int kScoreWarp = 6;                        // S products; then the value products (+ 1)
+constexpr int kThreads = 8 * 32;
+constexpr int kKStages = 4;
+constexpr int kVStages = 3;
+constexpr int kCtasPerSm = 2;                        // they share an SM's 512 columns
+constexpr uint32_t kTmemCols = 512 / kCtasPerSm;
+constexpr uint32_t kTmemP = kStepKeys;               // after S: two halves of P ...
+constexpr uint32_t kPartCols = kHalfKeys / 2;        // ... of three parts, two keys per column
+constexpr uint32_t kTmemO = kTmemP + 2 * 3 * kPartCols;
+static_assert(kTmemO + kDim <= kTmemCols, "S, P and O fit the CTA's tensor memory");
 constexpr float kRescaleLog2 = 8.f;                  // lazy max: p <= 2^8
+constexpr int kSegment = 4;                          // steps whose O stays in tensor memory
+// Registers a thread, once the roles are taken: 128 at launch, shared by the
+// CTA's two warpgroups.
+constexpr int kSoftmaxRegs = 192;
+constexpr int kOtherRegs = 64;
+static_assert(kSoftmaxRegs + kOtherRegs <= 2 * 128, "the launch's registers are split");
 constexpr uint32_t kStepBytes = kStepKeys * kRowBytes;
 
 struct WindowPrefillSmem {                           // every tile 1024-byte aligned
-  uint8_t q[kRows * kRowBytes];                      // 32 KiB
-  uint8_t k[kKStages][kStepBytes];                   // 6 x 8 KiB
-  uint8_t v[kVStages][kStepBytes];                   // 5 x 8 KiB
-  unsigned long long bar_q, bar_k[kKStages], bar_v[kVStages], bar_s[kSTiles], bar_p[kSTiles];
-  unsigned long long bar_o[kSTiles];                 // P(j) V(j) done, per tile
-  unsigned long long k_free[kKStages], v_free[kVStages];
+  uint8_t q[kRows * kRowBytes];                      // 16 KiB
+  uint8_t k[kKStages][kStepBytes];                   // 4 x 8 KiB
+  uint8_t v[kVStages][kStepBytes];                   // 3 x 8 KiB
+  unsigned long long bar_q, bar_k[kKStages], bar_v[kVStages];   // copies landed
+  unsigned long long k_free[kKStages], v_free[kVStages];        // stage read by its products
+  unsigned long long bar_s, s_free;                  // S(j) computed; in registers
+  unsigned long long bar_p, p_done;                  // P(j) written; multiplied
   uint32_t tmem_base;
   int abort_flag;
+  int bad_page;
 };
 static_assert(offsetof(WindowPrefillSmem, k) % 1024 == 0 &&
                   offsetof(WindowPrefillSmem, v) % 1024 == 0,
               "swizzled tiles start on 1024-byte boundaries");
 constexpr size_t kSmemBytes = sizeof(WindowPrefillSmem) + 1024;   // + room to align the base
-static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "kCtasPerSm CTAs per SM");
 
 struct WindowPrefillParams {
   const int32_t* table;       // this layer's block tables [max_batch][table_stride]
@@ -97,9 +123,88 @@ struct WindowPrefillParams {
   int sinks;                  // 0 .. max_seq_len
 };
 
-// The lowest n bits of 64 (n clamped to 0 .. 64).
-__device__ __forceinline__ unsigned long long low_bits64(int n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+// Whether `x` holds, which is rare: the code under it is placed out of the
+// step loop's way.
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
+
+// The rest of a bounded wait on an mbarrier phase that has not come yet; gives
+// up when the CTA does.
+__device__ __noinline__ bool wait_longer(unsigned long long* bar, uint32_t parity,
+                                         volatile int* abort_flag) {
+  const long long start = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || clock64() - start > kWaitCycles) return false;
+  return true;
+}
+
+// One verdict per warp (what follows is warp-wide).
+__device__ __forceinline__ bool wait_phase(unsigned long long* bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) done = wait_longer(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, done);
+}
+
+// V rows that no row of the tile sees (past its last key, or between the sinks
+// and the window) set to zero, so that p = 0 times them stays 0.
+__device__ __noinline__ void zero_rows(uint8_t* stage, int key0, int n_keys, int sinks, int lo) {
+  for (int idx = threadIdx.x; idx < kStepKeys * 8; idx += kSoftmaxThreads) {
+    const int key = key0 + (idx >> 3);
+    if (key >= n_keys || (key >= sinks && key < lo))
+      *reinterpret_cast<uint4*>(stage + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+}
+
+// One lane of a converged warp, always the same. The issuing warps run their
+// loops whole and only the tcgen05 instructions under this predicate, so the
+// operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The largest of three (the last two given as bits).
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  return max3(__uint_as_float(a), b, c);
+}
+
+// 64 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  #pragma unroll
+  for (int h = 0; h < 4; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[16 * h]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]),
+          "=r"(r[16 * h + 4]), "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]),
+          "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]), "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]),
+          "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]), "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+        : "r"(taddr + 16 * h));
+  // the registers are written once the wait returns: it takes them as operands
+  #pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t* x = r + 16 * h;
+    if (h == 0)
+      asm volatile("tcgen05.wait::ld.sync.aligned;"
+                   : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                     "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                     "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+    else
+      asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                        "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                        "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+  }
 }
 
 // What the tile (and each of its steps) sees of the sequence.
@@ -111,6 +216,7 @@ struct TileView {
   int win_step;          // the window's first step
   int n_steps;
   int sinks;
+  int plain_from, plain_to;   // steps whose keys every row sees
 
   __device__ TileView(int first, int count, int window, int sinks_) {
     p_first = first;
@@ -121,6 +227,9 @@ struct TileView {
     win_step = lo / kStepKeys;
     sink_steps = min((sinks + kStepKeys - 1) / kStepKeys, win_step);
     n_steps = sink_steps + (n_keys + kStepKeys - 1) / kStepKeys - win_step;
+    const int hidden = p_last - window;        // the last key outside some row's window
+    plain_from = sink_steps + (hidden < 0 ? 0 : hidden / kStepKeys + 1 - win_step);
+    plain_to = sink_steps + (p_first + 1) / kStepKeys - win_step;
   }
   __device__ int step(int j) const { return j < sink_steps ? j : j - sink_steps + win_step; }
   // whether logical page lp holds a key that some row sees
@@ -129,7 +238,7 @@ struct TileView {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
     const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
     const __grid_constant__ CUtensorMap tmap_v, const WindowPrefillParams prm) {
   extern __shared__ uint8_t smem_raw[];
@@ -142,6 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
 
+  // the descriptors into the cache ahead of their first copies
+  if (tid < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(
+                     tid == 0 ? &tmap_q : tid == 1 ? &tmap_k : &tmap_v))
+                 : "memory");
   const int row0 = prm.cu_tokens[b];
   const int n = prm.cu_tokens[b + 1] - row0;
   const int start = prm.start_pos[b];
@@ -161,341 +275,363 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(
   const int n_steps = view.n_steps;
   const int32_t* trow = prm.table + static_cast<size_t>(b) * prm.table_stride;
 
-  // invalid ids among the pages that count are flagged once, here
-  bool bad_page = false;
-  for (int i = tid; i < n_steps * kStepPages; i += kThreads) {
-    const int lp = view.step(i / kStepPages) * kStepPages + i % kStepPages;
-    if (!view.wants(lp)) continue;
-    const int id = __ldg(trow + lp);
-    bad_page |= id < 0 || id >= prm.num_pages;
-  }
-  if (bad_page) set_error(prm.err, PKV_DEV_ERR_PAGE);
-
-  if (tid == 0) {
+  if (warp == kLoadWarp && lane_of(tid) == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int i = 0; i < kKStages; ++i) mbar_init(&sm.bar_k[i], 1);
     for (int i = 0; i < kVStages; ++i) mbar_init(&sm.bar_v[i], 1);
-    for (int i = 0; i < kSTiles; ++i) mbar_init(&sm.bar_s[i], 1);
-    for (int i = 0; i < kSTiles; ++i) mbar_init(&sm.bar_p[i], kSoftmaxThreads);
-    // the value barriers complete once both row halves' issuers committed
-    for (int i = 0; i < kSTiles; ++i) mbar_init(&sm.bar_o[i], kRowHalves);
     for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_free[i], 1);
-    for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_free[i], kRowHalves);
+    for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_free[i], 1);
+    mbar_init(&sm.bar_s, 1);
+    mbar_init(&sm.s_free, kSoftmaxWarps);
+    mbar_init(&sm.bar_p, kSoftmaxWarps);
+    mbar_init(&sm.p_done, 1);
     sm.abort_flag = 0;
+    sm.bad_page = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&sm.tmem_base, kTmemCols);
   tc_fence_before();
-  const bool any_bad_page = __syncthreads_or(bad_page);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
 
-  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    // ------------------------------------------------------------ copy engine
-    // Lanes 0..3 copy the step's 4 pages in one instruction once lane 0 saw
-    // the stage free. A page that does not count is copied from past the
-    // pool's end: zeros.
-    const int lane = lane_of(tid);
-    const bool is_v = warp != kLoadWarp;
-    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-    const int stages = is_v ? kVStages : kKStages;
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-      if (!is_v) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q))
-                     : "memory");
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kScoreWarp) {
+      // ------------------------------------------------------------ copy engine
+      // Lanes 0..3 copy the step's 4 pages in one instruction once lane 0 saw
+      // the stage free. A page that does not count is copied from past the
+      // pool's end: zeros.
+      const int lane = lane_of(tid);
+      const bool is_v = warp != kLoadWarp;
+      const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+      const int stages = is_v ? kVStages : kKStages;
+      auto page_of = [&](int j, int e) {        // the e-th page of step j, past the end if none
+        int id = prm.num_pages;
+        if (j < n_steps) {
+          const int lp = view.step(j) * kStepPages + e;
+          if (view.wants(lp)) id = __ldg(trow + lp);
+          if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
+        }
+        return id;
+      };
+      // lane 4 s + e holds the e-th page of the s-th of 8 steps; the next 8 steps'
+      // are fetched while these are in use
+      int ids = page_of(lane / kStepPages, lane % kStepPages);
+      int ids_next = page_of(8 + lane / kStepPages, lane % kStepPages);
+      if (!is_v && lane == 0) {
         mbar_arrive_expect_tx(&sm.bar_q, kRows * kRowBytes);
         tma_load_3d(sm.q, &tmap_q, 0, g * kGroup, row0 + tile * kTileTokens, &sm.bar_q);
       }
-    }
-    auto page_of = [&](int j) {
-      int id = prm.num_pages;
-      if (j < n_steps && lane < kStepPages) {
-        const int lp = view.step(j) * kStepPages + lane;
-        if (view.wants(lp)) id = __ldg(trow + lp);
-        if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
-      }
-      return id;
-    };
-    int page = page_of(0);
-    int issued = 0;
-    bool ok = true;
-    for (int j = 0; j < n_steps; ++j) {
-      const int st = j % stages;
-      unsigned long long* full = is_v ? &sm.bar_v[st] : &sm.bar_k[st];
-      const int next_page = page_of(j + 1);
-      bool good = true;
-      if (lane == 0) {
-        good = *abort_flag == 0;
-        if (good && j >= stages)
-          good = mbar_wait(is_v ? &sm.v_free[st] : &sm.k_free[st], ((j - stages) / stages) & 1);
-        if (good) mbar_arrive_expect_tx(full, kStepBytes);
-      }
-      if (!__shfl_sync(0xffffffffu, good ? 1 : 0, 0)) {
-        ok = false;
-        break;
-      }
-      if (lane < kStepPages)
-        tma_load_3d((is_v ? sm.v[st] : sm.k[st]) + lane * kPage * kRowBytes, map, 0, g * kPage,
-                    page, full);
-      __syncwarp();
-      page = next_page;
-      ++issued;
-    }
-    if (lane == 0) {
-      if (!ok) {
-        *abort_flag = 1;
-        set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
-      }
-      // every copy issued lands before the CTA frees its memory (bounded waits)
-      if (!is_v) mbar_wait(&sm.bar_q, 0);
-      for (int s = 0; s < stages; ++s) {
-        const int uses = (issued - s + stages - 1) / stages;
-        if (uses > 0) mbar_wait(is_v ? &sm.bar_v[s] : &sm.bar_k[s], (uses - 1) & 1);
-      }
-    }
-  } else if (warp >= kScoreWarp) {
-    // ------------------------------------------------------------ tensor cores
-    // One issuing thread for the scores, one per row half for the values.
-    if (lane_of(tid) == 0) {
-      const bool scores = warp == kScoreWarp;
-      const int half = warp - kValueWarp0;
       int issued = 0;
       bool ok = true;
-      if (scores) {
-        const uint32_t idesc_s = instr_desc(kHalfRows, kStepKeys, false);
+      for (int j = 0; j < n_steps; ++j) {
+        const int st = j % stages;
+        unsigned long long* full = is_v ? &sm.bar_v[st] : &sm.bar_k[st];
+        if ((j & 7) == 0 && j > 0) {
+          ids = ids_next;
+          ids_next = page_of(j + 8 + lane / kStepPages, lane % kStepPages);
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, (j & 7) * kStepPages + lane % kStepPages);
+        bool good = true;
+        if (lane == 0) {
+          good = *abort_flag == 0;
+          if (good && j >= stages)
+            good = mbar_wait(is_v ? &sm.v_free[st] : &sm.k_free[st], ((j - stages) / stages) & 1);
+          if (good) mbar_arrive_expect_tx(full, kStepBytes);
+        }
+        if (!__shfl_sync(0xffffffffu, good ? 1 : 0, 0)) {
+          ok = false;
+          break;
+        }
+        if (lane < kStepPages)
+          tma_load_3d((is_v ? sm.v[st] : sm.k[st]) + lane * kPage * kRowBytes, map, 0, g * kPage,
+                      page, full);
+        __syncwarp();
+        ++issued;
+      }
+      if (lane == 0) {
+        if (!ok) {
+          *abort_flag = 1;
+          set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
+        }
+        // every copy issued lands before the CTA frees its memory (bounded waits)
+        if (!is_v) mbar_wait(&sm.bar_q, 0);
+        for (int s = 0; s < stages; ++s) {
+          const int uses = (issued - s + stages - 1) / stages;
+          if (uses > 0) mbar_wait(is_v ? &sm.bar_v[s] : &sm.bar_k[s], (uses - 1) & 1);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ tensor cores
+      // One issuing warp for the scores and one for the values.
+      int issued = 0;
+      bool ok = true;
+      if (warp == kScoreWarp) {
+        const uint32_t idesc_s = instr_desc(kRows, kStepKeys, false);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
-        ok = mbar_wait(&sm.bar_q, 0);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_q, 0));
         for (int j = 0; ok && j < n_steps; ++j) {
-          // S(j) = Q K(j)^T into tile j % 2, once K(j) landed and P(j - 2) V(j - 2),
-          // which reads that tile, is done
-          if (*abort_flag || !mbar_wait(&sm.bar_k[j % kKStages], (j / kKStages) & 1) ||
-              (j >= kSTiles &&
-               !mbar_wait(&sm.bar_o[j % kSTiles], ((j - kSTiles) / kSTiles) & 1))) {
+          // S(j) = Q K(j)^T, once K(j) landed and S(j - 1) is in registers
+          if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
+                                           mbar_wait(&sm.bar_k[j % kKStages], (j / kKStages) & 1) &&
+                                           (j == 0 || mbar_wait(&sm.s_free, (j - 1) & 1)))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[j % kKStages]), 16, 1024);
-          #pragma unroll
-          for (int kk = 0; kk < kDim / 16; ++kk) {
+          if (elect_one()) {
             #pragma unroll
-            for (int h = 0; h < kRowHalves; ++h)
-              mma_bf16(tmem + ((j % kSTiles) * kRowHalves + h) * kTileCols,
-                       q_desc + h * (kHalfRows * kRowBytes >> 4) + kk * 2, k_desc + kk * 2,
-                       idesc_s, kk > 0);
+            for (int kk = 0; kk < kDim / 16; ++kk)
+              mma_bf16(tmem, q_desc + kk * 2, k_desc + kk * 2, idesc_s, kk > 0);
+            mma_commit(&sm.bar_s);
+            mma_commit(&sm.k_free[j % kKStages]);
           }
-          mma_commit(&sm.bar_s[j % kSTiles]);
-          mma_commit(&sm.k_free[j % kKStages]);
+          __syncwarp();
           ++issued;
         }
+        // every product issued completes before the CTA frees its memory
+        if (issued > 0) mbar_wait(&sm.bar_s, (issued - 1) & 1);
       } else {
-        const uint32_t idesc_o = instr_desc(kHalfRows, kDim, true);
+        const uint32_t idesc_o = instr_desc(kRows, kDim, true);
         for (int j = 0; ok && j < n_steps; ++j) {
-          // O += P(j) V(j), P's three parts 32 columns apart, 16 keys per 8 columns
-          if (*abort_flag || !mbar_wait(&sm.bar_p[j % kSTiles], (j / kSTiles) & 1) ||
-              !mbar_wait(&sm.bar_v[j % kVStages], (j / kVStages) & 1)) {
+          // O += P(j) V(j): 16 keys per product, P's three parts kPartCols
+          // columns apart in each half
+          if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
+                                           mbar_wait(&sm.bar_v[j % kVStages], (j / kVStages) & 1) &&
+                                           mbar_wait(&sm.bar_p, j & 1))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[j % kVStages]), 8192, 1024);
-          const uint32_t p_tile = tmem + ((j % kSTiles) * kRowHalves + half) * kTileCols;
-          const uint32_t o_tile = tmem + kTmemO + half * kDim;
-          #pragma unroll
-          for (int part = 0; part < 3; ++part) {
+          if (elect_one()) {
             #pragma unroll
-            for (int kk = 0; kk < kStepKeys / 16; ++kk)
-              mma_bf16_tmem_a(o_tile, p_tile + part * 32 + kk * 8,
-                              v_desc + kk * (16 * kRowBytes >> 4), idesc_o,
-                              (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kStepKeys / 16; ++kk) {
+              #pragma unroll
+              for (int part = 0; part < 3; ++part)
+                mma_bf16_tmem_a(tmem + kTmemO,
+                                tmem + kTmemP + (3 * (kk / 2) + part) * kPartCols + (kk % 2) * 8,
+                                v_desc + kk * (16 * kRowBytes >> 4), idesc_o,
+                                (j % kSegment > 0 || kk > 0 || part > 0) ? 1u : 0u);
+            }
+            mma_commit(&sm.p_done);
+            mma_commit(&sm.v_free[j % kVStages]);
           }
-          mma_commit(&sm.bar_o[j % kSTiles]);
-          mma_commit(&sm.v_free[j % kVStages]);
+          __syncwarp();
           ++issued;
         }
+        if (issued > 0) mbar_wait(&sm.p_done, (issued - 1) & 1);
       }
-      if (!ok) {
+      if (!ok && lane_of(tid) == 0) {
         *abort_flag = 1;
         set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
       }
-      // every product this thread issued completes before the CTA frees its memory
-      if (scores) {
-        for (int t = 0; t < kSTiles; ++t) {
-          const int uses = (issued - t + kSTiles - 1) / kSTiles;
-          if (uses > 0) mbar_wait(&sm.bar_s[t], (uses - 1) & 1);
-        }
-      } else if (issued > 0) {
-        mbar_wait(&sm.bar_o[(issued - 1) % kSTiles], ((issued - 1) / kSTiles) & 1);
-      }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax warps
-    const int rh = warp >> 2;                           // row half
-    const int r = (warp & 3) * 32 + (tid & 31);         // its MMA row = tensor-memory lane
-    const int tok = (rh * kHalfRows + r) >> 2;          // token of the tile, head r & 3
-    const uint32_t o_col = kTmemO + rh * kDim;
+    const int r = tid;                                  // its MMA row = tensor-memory lane
+    const int tok = r >> 2;                             // token of the tile, head r & 3
     const int pos = view.p_first + min(tok, t_valid - 1);   // rows past the chunk mirror its last
     const float c = 1.4426950408889634f * 0.125f;       // log2(e) / sqrt(64)
-    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
     float m_run = -INFINITY, l_run = 0.f;
+    float m_sum = -INFINITY;                            // the max that o_sum is taken against
+    float2 o_sum[kDim / 2];                             // earlier segments' O
+    #pragma unroll
+    for (int d = 0; d < kDim / 2; ++d) o_sum[d] = make_float2(0.f, 0.f);
     bool ok = true;
+    // invalid ids among the pages that count: flagged here, under the first copies
+    bool bad_page = false;
+    for (int i = tid; i < n_steps * kStepPages; i += kRows) {
+      const int lp = view.step(i / kStepPages) * kStepPages + i % kStepPages;
+      if (!view.wants(lp)) continue;
+      const int id = __ldg(trow + lp);
+      bad_page |= id < 0 || id >= prm.num_pages;
+    }
+    if (bad_page) {
+      set_error(prm.err, PKV_DEV_ERR_PAGE);
+      sm.bad_page = 1;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");       // the 4 softmax warps
+    const bool any_bad_page = *static_cast<volatile int*>(&sm.bad_page) != 0;
+    const int plain_from = any_bad_page ? n_steps : view.plain_from;
+    const int plain_count = any_bad_page ? 0 : max(view.plain_to - view.plain_from, 0);
+    int segment = 0;                                    // j % kSegment
     for (int j = 0; j < n_steps; ++j) {
-      // one verdict per warp (the tensor-memory accesses below are warp-wide)
-      if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
-                                       mbar_wait(&sm.bar_s[j % kSTiles], (j / kSTiles) & 1))) {
+      if (!wait_phase(&sm.bar_s, j & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t st_tile = tmem + lane_addr + ((j % kSTiles) * kRowHalves + rh) * kTileCols;
       uint32_t sv[64];                                   // the row's 64 keys of the step
-      {
-        uint32_t (&a)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
-        uint32_t (&b2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[32]);
-        tmem_ld32(st_tile, a);
-        tmem_ld32(st_tile + 32, b2);
-      }
-      const int key0 = view.step(j) * kStepKeys;
-      // some key of the step is hidden from some row
-      const bool edge = key0 + kStepKeys - 1 > view.p_first ||
-                        (key0 <= view.p_last - prm.window && key0 + kStepKeys > view.sinks);
-      if (edge || any_bad_page) {
-        unsigned long long seen =
-            low_bits64(pos + 1 - key0) &
-            (low_bits64(view.sinks - key0) | ~low_bits64(pos - prm.window + 1 - key0));
+      tmem_ld64(tmem + lane_addr, sv);
+      tc_fence_before();
+      __syncwarp();
+      if (lane_of(tid) == 0) mbar_arrive(&sm.s_free);
+      const bool plain = static_cast<unsigned>(j - plain_from) < static_cast<unsigned>(plain_count);
+      if (rarely(!plain)) {
+        const int key0 = view.step(j) * kStepKeys;
+        const int last = pos - key0;                     // the row's last key, first windowed key
+        const int first = last - prm.window + 1;         // and sinks, within the step
+        const int sinks = view.sinks - key0;
+        if (key0 + kStepKeys - 1 > view.p_first) {
+          #pragma unroll
+          for (int i = 0; i < kStepKeys; ++i)
+            if (i > last) sv[i] = __float_as_uint(-INFINITY);
+        }
+        if (key0 <= view.p_last - prm.window && sinks < kStepKeys) {
+          if (sinks <= 0) {
+            #pragma unroll
+            for (int i = 0; i < kStepKeys; ++i)
+              if (i < first) sv[i] = __float_as_uint(-INFINITY);
+          } else {
+            #pragma unroll
+            for (int i = 0; i < kStepKeys; ++i)
+              if (i < first && i >= sinks) sv[i] = __float_as_uint(-INFINITY);
+          }
+        }
         if (any_bad_page) {
+          #pragma unroll
           for (int e = 0; e < kStepPages; ++e) {
             const int lp = key0 / kPage + e;
             const int id = view.wants(lp) ? __ldg(trow + lp) : -1;
-            if (id < 0 || id >= prm.num_pages) seen &= ~(0xffffull << (16 * e));
+            if (id < 0 || id >= prm.num_pages) {
+              #pragma unroll
+              for (int i = 0; i < kPage; ++i) sv[e * kPage + i] = __float_as_uint(-INFINITY);
+            }
           }
         }
-        const uint32_t w0 = static_cast<uint32_t>(seen), w1 = static_cast<uint32_t>(seen >> 32);
-        #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (!((w0 >> i) & 1u)) sv[i] = __float_as_uint(-INFINITY);
-          if (!((w1 >> i) & 1u)) sv[i + 32] = __float_as_uint(-INFINITY);
+        // V rows that no row of the tile sees, in pages that were read: past
+        // the last key, or between the sinks and the window
+        if (key0 + kStepKeys > view.n_keys ||
+            max(key0, view.sinks) < min(key0 + kStepKeys, view.lo)) {
+          if (!wait_phase(&sm.bar_v[j % kVStages], (j / kVStages) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          zero_rows(sm.v[j % kVStages], key0, view.n_keys, view.sinks, view.lo);
         }
       }
-      float mx8[8];
+      float mx[4];
       #pragma unroll
-      for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(sv[e]);
+      for (int e = 0; e < 4; ++e) mx[e] = max3(sv[e], sv[e + 4], sv[e + 8]);
       #pragma unroll
-      for (int i = 8; i < 64; ++i) mx8[i & 7] = fmaxf(mx8[i & 7], __uint_as_float(sv[i]));
-      const float m_step = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * c;
-      float alpha = 1.f;
+      for (int i = 12; i < 60; i += 8) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[i + e], sv[i + e + 4]);
+      }
+      #pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[60 + e]));
+      const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
       const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
-      if (grow) {
-        alpha = fast_exp2(m_run - m_step);
-        m_run = m_step;
-        l_run *= alpha;
-      }
-      {
-        const float mu = m_run == -INFINITY ? 0.f : m_run;
-        const float2 c2 = make_float2(c, c);
-        const float2 nm2 = make_float2(-mu, -mu);
-        const float2 neg1 = make_float2(-1.f, -1.f);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                         make_float2(0.f, 0.f)};
-        #pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-          uint32_t hi[16], mid[16], lo[16];
-          #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const int k = kh * 32 + i;
-            const float2 x = __ffma2_rn(
-                make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, nm2);
-            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], pp);
-            // p = hi + mid + lo: two truncated parts, the rest rounded
-            const uint32_t b0 = __float_as_uint(pp.x), b1 = __float_as_uint(pp.y);
-            hi[i / 2] = __byte_perm(b0, b1, 0x7632);
-            const float2 r1 = __ffma2_rn(make_float2(__uint_as_float(b0 & 0xffff0000u),
-                                                     __uint_as_float(b1 & 0xffff0000u)),
-                                         neg1, pp);
-            const uint32_t c0 = __float_as_uint(r1.x), c1 = __float_as_uint(r1.y);
-            mid[i / 2] = __byte_perm(c0, c1, 0x7632);
-            const float2 r2 = __ffma2_rn(make_float2(__uint_as_float(c0 & 0xffff0000u),
-                                                     __uint_as_float(c1 & 0xffff0000u)),
-                                         neg1, r1);
-            lo[i / 2] = float2_to_bf16x2(r2.x, r2.y);
-          }
-          // the scores of both halves are in registers already: P may overwrite them
-          tmem_st16(st_tile + kh * 16, hi);
-          tmem_st16(st_tile + 32 + kh * 16, mid);
-          tmem_st16(st_tile + 64 + kh * 16, lo);
+      // Once P(j - 1) V(j - 1) is done (P(j) V(j) cannot start before this
+      // thread hands over P(j)): after a segment O joins the sum, and
+      // elsewhere a row that grew its max rescales its O.
+      const bool join = segment == kSegment;
+      if (rarely(__any_sync(0xffffffffu, grow || join))) {
+        float alpha = 1.f;
+        if (grow) {
+          alpha = fast_exp2(m_run - m_step);
+          m_run = m_step;
+          l_run *= alpha;
         }
-        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        l_run += a.x + a.y;
-      }
-
-      // a row that grew its max rescales its O, once P(j - 1) V(j - 1) is done
-      bool failed = false;
-      if (j > 0 && __any_sync(0xffffffffu, grow)) {
-        failed = !__all_sync(0xffffffffu,
-                             mbar_wait(&sm.bar_o[(j - 1) % kSTiles], ((j - 1) / kSTiles) & 1));
-        tc_fence_after();
-        if (!failed) {
+        if (j > 0) {
+          if (!wait_phase(&sm.p_done, (j - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
+          const float2 a2 = make_float2(alpha, alpha), b2 = make_float2(beta, beta);
           #pragma unroll
           for (int dh = 0; dh < 2; ++dh) {
             uint32_t ov[32];
-            tmem_ld32(tmem + lane_addr + o_col + dh * 32, ov);
-            #pragma unroll
-            for (int d = 0; d < 32; ++d) ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
-            tmem_st32(tmem + lane_addr + o_col + dh * 32, ov);
+            tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
+            if (join) {
+              #pragma unroll
+              for (int d = 0; d < 16; ++d) {
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(ov[2 * d]),
+                                                        __uint_as_float(ov[2 * d + 1])), a2);
+                o_sum[dh * 16 + d] = __ffma2_rn(o_sum[dh * 16 + d], b2, x);
+              }
+            } else {
+              #pragma unroll
+              for (int d = 0; d < 32; ++d) ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
+              tmem_st32(tmem + lane_addr + kTmemO + dh * 32, ov);
+            }
+          }
+          if (join) {
+            m_sum = m_run;
+            segment = 0;
           }
         }
       }
-      // V rows that no row of the tile sees, in pages that were read (zero, so
-      // that p = 0 times them stays 0): past the last key, or between the
-      // sinks and the window
-      const bool dead_tail = key0 + kStepKeys > view.n_keys;
-      const bool dead_gap = max(key0, view.sinks) < min(key0 + kStepKeys, view.lo);
-      if (!failed && (dead_tail || dead_gap)) {
-        if (__all_sync(0xffffffffu, mbar_wait(&sm.bar_v[j % kVStages], (j / kVStages) & 1))) {
-          for (int idx = tid; idx < kStepKeys * 8; idx += kSoftmaxThreads) {
-            const int key = key0 + (idx >> 3);
-            if (key >= view.n_keys || (key >= view.sinks && key < view.lo))
-              *reinterpret_cast<uint4*>(sm.v[j % kVStages] + idx * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        } else {
-          failed = true;
+      ++segment;
+      // the probabilities, their sum and their three BF16 parts, 32 keys at a
+      // time; into tensor memory once the last step's product has read its P
+      const float mu = m_run == -INFINITY ? 0.f : m_run;
+      const float2 c2 = make_float2(c, c);
+      const float2 nm2 = make_float2(-mu, -mu);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t hi[16], mid[16], lo[16];
+        #pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const int k = h * 32 + i;
+          const float2 x = __ffma2_rn(
+              make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, nm2);
+          const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], pp);
+          split3(pp.x, pp.y, hi[i / 2], mid[i / 2], lo[i / 2]);
         }
+        if (h == 0 && j > 0) {
+          if (!wait_phase(&sm.p_done, (j - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        const uint32_t p_half = tmem + lane_addr + kTmemP + 3 * h * kPartCols;
+        tmem_st16(p_half, hi);
+        tmem_st16(p_half + kPartCols, mid);
+        tmem_st16(p_half + 2 * kPartCols, lo);
       }
-      if (failed) {
-        ok = false;
-        break;
-      }
+      if (rarely(!ok)) break;
+      const float2 a = __fadd2_rn(acc[0], acc[1]);
+      l_run += a.x + a.y;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sm.bar_p[j % kSTiles]);
+      __syncwarp();
+      if (lane_of(tid) == 0) mbar_arrive(&sm.bar_p);
     }
     if (!ok) {
       *abort_flag = 1;
       set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
     }
-    const bool done = ok && !*abort_flag &&
-                      mbar_wait(&sm.bar_o[(n_steps - 1) % kSTiles], ((n_steps - 1) / kSTiles) & 1);
-    if (__all_sync(0xffffffffu, done)) {
+    if (ok && wait_phase(&sm.p_done, (n_steps - 1) & 1, abort_flag)) {
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
       float* dst = prm.out + ((static_cast<size_t>(row0) + tile * kTileTokens + tok) * kHq +
                               g * kGroup + (r & 3)) * kDim;
       #pragma unroll
       for (int dh = 0; dh < 2; ++dh) {
         uint32_t ov[32];
-        tmem_ld32(tmem + lane_addr + o_col + dh * 32, ov);
-        if (tok < t_valid) {
-          #pragma unroll
-          for (int d = 0; d < 32; d += 4)
-            *reinterpret_cast<float4*>(dst + dh * 32 + d) =
-                make_float4(__uint_as_float(ov[d]) * inv, __uint_as_float(ov[d + 1]) * inv,
-                            __uint_as_float(ov[d + 2]) * inv, __uint_as_float(ov[d + 3]) * inv);
+        tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
+        #pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const float2 was0 = o_sum[dh * 16 + 2 * d], was1 = o_sum[dh * 16 + 2 * d + 1];
+          if (tok < t_valid)
+            *reinterpret_cast<float4*>(dst + dh * 32 + 4 * d) =
+                make_float4(fmaf(was0.x, beta, __uint_as_float(ov[4 * d])) * inv,
+                            fmaf(was0.y, beta, __uint_as_float(ov[4 * d + 1])) * inv,
+                            fmaf(was1.x, beta, __uint_as_float(ov[4 * d + 2])) * inv,
+                            fmaf(was1.y, beta, __uint_as_float(ov[4 * d + 3])) * inv);
         }
       }
     }
@@ -539,7 +675,7 @@ extern "C" pkv_status pkv_window_prefill_attention(
   if (max_chunk_tokens < 1 || max_chunk_tokens > c.max_seq_len) return PKV_ERR_INVALID_ARG;
   if (!q || !k_pool || !v_pool || !block_tables || !cu_tokens || !start_pos || !out ||
       !pkv_aligned16(q) || !pkv_aligned16(k_pool) || !pkv_aligned16(v_pool) ||
-      !pkv_aligned16(block_tables) || !pkv_aligned16(cu_tokens) || !pkv_aligned16(start_pos) ||
+      !pkv_aligned16(block_tables) || !pkv_aligned4(cu_tokens) || !pkv_aligned4(start_pos) ||
       !pkv_aligned16(out))
     return PKV_ERR_INVALID_ARG;
   int dev = -1;

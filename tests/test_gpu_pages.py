@@ -154,6 +154,20 @@ def test_captured_and_replayed_with_other_lists():
     pool.close()
 
 
+def test_lists_that_start_anywhere():
+    """Slices of a longer list: int32 alignment is enough."""
+    kp, vp = _pools(64)
+    want = kp.clone()
+    ids = _i32(range(64))
+    tok = _i32([16] * 64)
+    pool = pkv.pkv_pool_create(1, 64, 1)
+    _bits(want)[33:36] = _bits(want)[5:8]
+    pkv.pkv_copy_pages(pool, ids[5:8], ids[33:36], kp, vp, tokens=tok[1:4])
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    assert torch.equal(_bits(kp), _bits(want))
+    pool.close()
+
+
 def test_refusals():
     kp, vp = _pools(10)
     pool = pkv.pkv_pool_create(1, 10, 1, max_seq_len=256)

@@ -140,6 +140,29 @@ def test_second_layer_and_wider_tables():
     _decode([300, 40], 100, 4, fused=True, num_layers=3, layer=2, max_batch=5)
 
 
+def test_lists_that_start_anywhere():
+    """seq_lens, positions, cu_tokens and start_pos taken as slices."""
+    c = W.Cache([40, 33])
+    kp, vp = c.pools(lambda b: np.ones(c.lens[b], bool), 0.0)
+    pool = _pool(c)
+    q = torch.randn(2, 32, 64, device="cuda").bfloat16()
+    lens = torch.tensor([7, 40, 33], dtype=torch.int32, device="cuda")[1:]
+    flat = torch.zeros(5, dtype=torch.int32, device="cuda")[1:]
+    cos, sin = W.angles(4)
+    rope = pkv.pkv_axes_rope(cos, sin, SECTIONS[2])
+    a, b = torch.zeros(2, 32, 64, device="cuda"), torch.zeros(2, 32, 64, device="cuda")
+    pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, lens, a, 16, rope=rope,
+                             rope_positions=flat.view(2, 2))
+    pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, c.lens_tensor(), b, 16)
+    assert torch.equal(a, b)            # angle 0 leaves the queries as they are
+    cu = torch.tensor([9, 0, 1, 2], dtype=torch.int32, device="cuda")[1:]
+    start = torch.tensor([9, 39, 32], dtype=torch.int32, device="cuda")[1:]
+    pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, cu, start, a, 1, 16)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    assert (a - b).abs().max().item() <= 2e-5 * b.abs().max().item()
+    pool.close()
+
+
 def test_other_stream():
     s = torch.cuda.Stream()
     _decode([300, 40, 2048], 100, 4, fused=True, stream=s)
