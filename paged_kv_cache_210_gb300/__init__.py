@@ -436,11 +436,13 @@ _torch_dtypes = {}
 def _arg(pool, name, x, count=0):
     """Address of a tensor argument: what _addr checks, and that the tensor lies
     on the handle's device and holds at least `count` elements."""
-    if x is None or type(x) is int:
-        return x
-    if x.dtype is _torch_dtypes.get(name) and x.get_device() == pool.device and \
-            x.numel() >= count and x.is_contiguous():
-        return x.data_ptr()
+    try:      # the common case in as few steps as a small call's latency wants
+        if x.dtype is _torch_dtypes[name] and x.get_device() == pool.device and \
+                x.numel() >= count and x.is_contiguous():
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        if x is None or isinstance(x, int):
+            return x
     address = _addr(x, _DTYPES[name], name)
     if pool.device is not None and x.get_device() != pool.device:
         raise ValueError(f"{name}: expected a tensor on cuda:{pool.device}, got {x.device}")

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kFillWarps * 32) fill_axes_kernel(const FillPa
   }
   const long long row = static_cast<long long>(row0) + i;
   float c, s;
-  if (!load_pair_angle(prm.rope, row, lane, c, s)) {
+  if (!load_pair_angle(prm.rope, pair_position(prm.rope, row, lane), lane, c, s)) {
     if (lane == 0) set_error(prm.err, PKV_DEV_ERR_POSITION);
     return;
   }

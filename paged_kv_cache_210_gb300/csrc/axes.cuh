@@ -44,14 +44,17 @@ inline pkv_status make_axes_args(const pkv_axes_rope* rope, const int32_t* posit
   return PKV_OK;
 }
 
-// Lane i's angle of pair i for token `token`; false (in every lane) if the
-// token has a position outside the tables. Called by a whole warp.
-__device__ __forceinline__ bool load_pair_angle(const AxesArgs& rope, long long token, int lane,
-                                                float& c, float& s) {
+// Lane i's position for pair i of token `token` (to be checked by its user).
+__device__ __forceinline__ int pair_position(const AxesArgs& rope, long long token, int lane) {
   const int axis = static_cast<int>(rope.axes >> (2 * lane)) & 3;
-  const int p = __ldg(rope.positions + axis * rope.stride + token);
-  const bool ok = p >= 0 && p < rope.rows;
-  if (!__all_sync(0xffffffffu, ok)) return false;
+  return __ldg(rope.positions + axis * rope.stride + token);
+}
+
+// Lane i's angle of pair i at its position p; false (in every lane) if a lane's
+// position is outside the tables. Called by a whole warp.
+__device__ __forceinline__ bool load_pair_angle(const AxesArgs& rope, int p, int lane, float& c,
+                                                float& s) {
+  if (!__all_sync(0xffffffffu, p >= 0 && p < rope.rows)) return false;
   const size_t at = static_cast<size_t>(p) * kPairs + lane;
   c = __ldg(rope.cos + at);
   s = __ldg(rope.sin + at);

@@ -50,7 +50,7 @@ struct alignas(1024) WindowSmem {
     int full[kWarps];
     uint32_t c12[kWarps], c34[kWarps];
     int count[2][kWarps];
-    int seq, split;
+    int seq, split, len;
   } find;
   int last;
 };
@@ -281,42 +281,50 @@ struct SeenPages {
 // Called by every thread of the block; false past the last unit.
 template <bool kBlock>
 __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, WindowSmem& sm, int& b,
-                                          int& split, int& range) {
+                                          int& split, int& range, int& len) {
   constexpr int kGroupSize = kBlock ? kThreadsW : 32;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int me = kBlock ? static_cast<int>(threadIdx.x) : lane;
-  auto pages_of = [&](int s) {
-    if (s >= prm.batch) return 0;
-    const int len = prm.seq_lens[s];
-    if (len == 0) return 0;
-    return len < 0 || len > prm.max_seq_len ? 1 : SeenPages(len, prm).count;
+  auto pages_of = [&](int len) {
+    return len == 0 ? 0 : len < 0 || len > prm.max_seq_len ? 1 : SeenPages(len, prm).count;
   };
-  // fn(e, pages) for every sequence of this thread; e: its register, or -1
-  int held[kHeld];
+  auto len_of = [&](int s) { return s < prm.batch ? prm.seq_lens[s] : 0; };
+  int held_len[kHeld], held[kHeld];
   #pragma unroll
-  for (int e = 0; e < kHeld; ++e) held[e] = pages_of(me + e * kGroupSize);
-  auto each = [&](auto fn) {
+  for (int e = 0; e < kHeld; ++e) held_len[e] = len_of(me + e * kGroupSize);
+  #pragma unroll
+  for (int e = 0; e < kHeld; ++e) held[e] = pages_of(held_len[e]);
+  auto each = [&](auto fn) {                  // for every sequence of this thread
     #pragma unroll
     for (int e = 0; e < kHeld; ++e) fn(held[e]);
     if (kBlock)
-      for (int s = me + kHeld * kGroupSize; s < prm.batch; s += kGroupSize) fn(pages_of(s));
+      for (int s = me + kHeld * kGroupSize; s < prm.batch; s += kGroupSize) fn(pages_of(len_of(s)));
   };
-  // exact quotients of p <= 65,538 pages by r: the reciprocal's error stays
-  // below the half added
+  // ceil(p / r) by r's reciprocal, exact for p, r < 2^17 (the quotient of p + r -
+  // 1/2 stays 1 / (2 r) away from integers, the errors are below 2^-22 of it);
+  // adding 2^23 - 1/2 rounds it down into the low bits, without a conversion.
   auto ceil_of = [](int p, float r, float inv) {
-    return static_cast<int>((static_cast<float>(p) + r - 0.5f) * inv);
+    return __float_as_int(fmaf(static_cast<float>(p) + (r - 0.5f), inv, 8388607.5f)) - 0x4b000000;
   };
   float sum = 0.f;                            // pages: exact to 2^24, then to 2^-22 of itself
   int most = 0;
-  each([&](int p) {
-    sum += static_cast<float>(p);
-    most = max(most, p);
-  });
-  #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (kBlock) {
+  if (!kBlock) {
+    int pages = 0;
+    each([&](int p) {
+      pages += p;
+      most = max(most, p);
+    });
+    sum = static_cast<float>(static_cast<int>(__reduce_add_sync(0xffffffffu, pages)));
+    most = __reduce_max_sync(0xffffffffu, most);
+  } else {
+    each([&](int p) {
+      sum += static_cast<float>(p);
+      most = max(most, p);
+    });
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) {
       sm.find.pages[warp] = sum;
       sm.find.most[warp] = most;
@@ -331,14 +339,14 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
   }
   // T / by, rounded up past the float error (ranges stay below 2^17 pages)
   auto share = [&](int by) {
-    return static_cast<int>(fminf(__fdividef(sum, static_cast<float>(by)), 131072.f)) + 1;
+    return static_cast<int>(fminf(__fdividef(sum, static_cast<float>(by)), 131070.f)) + 1;
   };
   range = max(prm.least_pages, share(prm.range_div));
   if (!kBlock) {
     const int r0 = max(prm.least_pages, share(prm.wave_units));
     #pragma unroll
     for (int k = kTries - 1; k >= 0; --k) {
-      const int r = (r0 * (kTries + k) + kTries - 1) / kTries;
+      const int r = min((r0 * (kTries + k) + kTries - 1) / kTries, 131071);
       const float fr = static_cast<float>(r), inv = __frcp_rn(fr);
       int units = 0;
       #pragma unroll
@@ -352,7 +360,7 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
   auto classify = [&](int p, int& full) {
     full = ceil_of(p + 1, f_range, inv_range) - 1;
     const int rest = p - full * range;
-    return rest > 0 ? 4 - static_cast<int>((4.f * rest - 0.5f) * inv_range) : 0;
+    return rest > 0 ? 5 - ceil_of(4 * rest, f_range, inv_range) : 0;
   };
   int full = 0;
   uint32_t c12 = 0, c34 = 0;                 // two 16-bit counts each (batch <= 65535)
@@ -399,20 +407,34 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
   int before = 0;
   for (int base = 0, turn = 0; base < prm.batch; base += kGroupSize, turn ^= 1) {
     const int e = base / kGroupSize;
-    int pages = held[0];
+    int pages = held[0], own_len = held_len[0];
     #pragma unroll
-    for (int h = 1; h < kHeld; ++h) pages = e == h ? held[h] : pages;
-    if (kBlock && e >= kHeld) pages = pages_of(base + me);
+    for (int h = 1; h < kHeld; ++h) {
+      pages = e == h ? held[h] : pages;
+      own_len = e == h ? held_len[h] : own_len;
+    }
+    if (kBlock && e >= kHeld) {
+      own_len = len_of(base + me);
+      pages = pages_of(own_len);
+    }
     int f;
     const int c = classify(pages, f);
     const int units = cls == 0 ? f : c == cls ? 1 : 0;
-    int incl = units;
-    #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+    int excl, total;                         // over the warp
+    if (cls == 0) {
+      int incl = units;
+      #pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      excl = before + incl - units;
+    } else {
+      const uint32_t some = __ballot_sync(0xffffffffu, units != 0);
+      total = __popc(some);
+      excl = before + __popc(some & ((1u << lane) - 1u));
     }
-    int total = __shfl_sync(0xffffffffu, incl, 31), excl = before + incl - units;
     if (kBlock) {
       if (lane == 0) sm.find.count[turn][warp] = total;
       __syncthreads();
@@ -431,14 +453,17 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
         if (mine) {
           sm.find.seq = base + me;
           sm.find.split = at;
+          sm.find.len = own_len;
         }
         __syncthreads();
         b = sm.find.seq;
         split = sm.find.split;
+        len = sm.find.len;
       } else {
         const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         b = base + from;
         split = __shfl_sync(0xffffffffu, at, from);
+        len = __shfl_sync(0xffffffffu, own_len, from);
       }
       return true;
     }
@@ -470,23 +495,22 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // seq_lens, the block table, the rotary inputs and pool rows below the
   // appended position.
   int range = 0;
+  int len;
   if (units) {
     const int u = static_cast<int>(blockIdx.x) / kHkv;
-    if (!(prm.wave_units > 0 ? find_unit<false>(u, prm, sm, b, split, range)
-                             : find_unit<true>(u, prm, sm, b, split, range)))
+    if (!(prm.wave_units > 0 ? find_unit<false>(u, prm, sm, b, split, range, len)
+                             : find_unit<true>(u, prm, sm, b, split, range, len)))
       return;
+  } else {
+    len = prm.seq_lens[b];
   }
-  const int len = prm.seq_lens[b];
   if (len == 0) return;                                  // a padding row
   if (len < 0 || len > prm.max_seq_len) {
     if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrSeqLen);
     return;
   }
-  float ang_c = 1.f, ang_s = 0.f;                        // the angle of pair `lane`
-  if (kRope && !load_pair_angle(prm.rope, b, lane, ang_c, ang_s)) {
-    if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrPosition);
-    return;                                              // every block of the sequence
-  }
+  int rope_pos = 0;
+  if (kRope) rope_pos = pair_position(prm.rope, b, lane);   // arrives with the page ids
   const SeenPages see(len, prm);
   const int sink_pages = see.sinks;
   const int win_page = see.window;
@@ -525,6 +549,11 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   int ids = fetch_ids(0);
   int ids_next = mine > 32 ? fetch_ids(32) : -1;
   auto good_id = [&](int phys) { return phys >= 0 && phys < prm.num_pages; };
+  float ang_c = 1.f, ang_s = 0.f;                        // the angle of pair `lane`
+  if (kRope && !load_pair_angle(prm.rope, rope_pos, lane, ang_c, ang_s)) {
+    if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrPosition);
+    return;                                              // every block of the sequence
+  }
 
   PageRing<kStagesW>& ws = sm.warp[warp];
   unsigned long long* bars = sm.bar[warp];
@@ -559,14 +588,17 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   };
   // Fused: the appended row, one 16-byte chunk per lane (K in lanes 0..7, V
   // in 8..15), rotated, into the pool; kept to patch into the stage.
-  uint4 new_val = make_uint4(0u, 0u, 0u, 0u);
-  auto write_new_row = [&](int phys) {
-    const int c = lane & 7;
+  auto load_new_row = [&]() {
     uint4 val = make_uint4(0u, 0u, 0u, 0u);
     if (lane < 16)
       val = __ldg(reinterpret_cast<const uint4*>(
           (lane >= 8 ? prm.v_new : prm.k_new) +
-          (static_cast<size_t>(b) * kHkv + kvh) * kDim + c * 8));
+          (static_cast<size_t>(b) * kHkv + kvh) * kDim + (lane & 7) * 8));
+    return val;
+  };
+  uint4 new_val = make_uint4(0u, 0u, 0u, 0u);
+  auto write_new_row = [&](int phys, uint4 val) {
+    const int c = lane & 7;
     if (kRope) {
       const uint4 partner = shfl_xor_uint4(val, 4);
       float cs[8], sn[8];
@@ -613,11 +645,14 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   pdl_wait();
   pdl_launch_dependents();
   if (deferred) issue_copy(j_new, j_new, __shfl_sync(0xffffffffu, ids, j_new));
-  if (kFused && j_new >= 0 && j_new < n_prefetch)
-    write_new_row(__shfl_sync(0xffffffffu, ids, j_new));
+  // the new row's load goes out before the queries', so their latencies overlap
+  const bool new_early = kFused && j_new >= 0 && j_new < n_prefetch;
+  uint4 early = make_uint4(0u, 0u, 0u, 0u);
+  if (new_early) early = load_new_row();
   uint32_t qa[8], ql[8];
   load_queries<kRope>(prm.q + (static_cast<size_t>(b) * kHq + kvh * kGroup) * kDim, lane, ang_c,
                       ang_s, qa, ql);
+  if (new_early) write_new_row(__shfl_sync(0xffffffffu, ids, j_new), early);
 
   PageState st;
   #pragma unroll
@@ -668,7 +703,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
       }
       const int phys = __shfl_sync(0xffffffffu, ids, next & 31);
       issue_copy(next, stage, phys);
-      if (kFused && next == j_new) write_new_row(phys);
+      if (kFused && next == j_new) write_new_row(phys, load_new_row());
       issued = next + 1;
     }
     if (++stage == kStagesW) {

@@ -186,32 +186,38 @@ def test_flags_bad_data_and_recovers():
                                      sinks=4, rope=rope, rope_positions=pos_)
         return out, pkv.pkv_get_error(pool)
 
+    def right(out, rows, sinks=4):
+        """The split of a sequence depends on the batch, so its last bits may."""
+        keys = W.rotate(k, cos, sin, pos, SECTIONS[2], torch.float32).bfloat16()
+        q64 = W.rotate(q, cos, sin, pos, SECTIONS[2], torch.float64)
+        for b in rows:
+            kk, vv = c.k[b].double().clone(), c.v[b].double().clone()
+            kk[39], vv[39] = keys[b].double(), k[b].double()
+            ref, tol = W.attend(q64[b:b + 1], kk, vv, torch.tensor([39], device="cuda"), 16, sinks)
+            W.check(out[b:b + 1], ref, tol, f"sequence {b}")
+
     good, st = run(lens)
     assert st == pkv.PKV_OK
+    right(good, range(5))
     for bad in (2049, -1, 2 ** 31 - 1, -2 ** 31):
         out, st = run([40, bad, 40, 40, 40])
-        assert st == pkv.PKV_ERR_OUT_OF_RANGE
-        assert (out[1] == 7.5).all() and torch.equal(out[[0, 2, 3, 4]], good[[0, 2, 3, 4]])
+        assert st == pkv.PKV_ERR_OUT_OF_RANGE and (out[1] == 7.5).all()
+        right(out, [0, 2, 3, 4])
     for bad in (-1, 100, 2 ** 31 - 1):
         p = pos.clone()
         p[1, 3] = bad
         was = kp.clone()
         out, st = run(lens, p)
-        assert st == pkv.PKV_ERR_OUT_OF_RANGE
-        assert (out[3] == 7.5).all() and torch.equal(out[[0, 1, 2, 4]], good[[0, 1, 2, 4]])
+        assert st == pkv.PKV_ERR_OUT_OF_RANGE and (out[3] == 7.5).all()
+        right(out, [0, 1, 2, 4])
         assert torch.equal(was.view(torch.int16), kp.view(torch.int16))
     for bad in (-1, c.num_pages, 2 ** 31 - 1):
         t = c.tables.clone()
         t[0, 2, 0] = bad                   # the sinks' page: its tokens are skipped
         out, st = run(lens, tables=t)
         assert st == pkv.PKV_ERR_OUT_OF_RANGE
-        keys = W.rotate(k[2:3], cos, sin, pos[:, 2:3], SECTIONS[2], torch.float32).bfloat16()
-        kk, vv = c.k[2].double().clone(), c.v[2].double().clone()
-        kk[39], vv[39] = keys[0].double(), k[2].double()
-        q64 = W.rotate(q[2:3], cos, sin, pos[:, 2:3], SECTIONS[2], torch.float64)
-        ref, tol = W.attend(q64, kk, vv, torch.tensor([39], device="cuda"), 16, 0)
-        W.check(out[2:3], ref, tol, "without the sinks")
-        assert torch.equal(out[[0, 1, 3, 4]], good[[0, 1, 3, 4]])
+        right(out, [2], sinks=0)
+        right(out, [0, 1, 3, 4])
     t = c.tables.clone()
     t[0, 2] = -1
     out, st = run(lens, tables=t)
@@ -219,6 +225,48 @@ def test_flags_bad_data_and_recovers():
     out, st = run(lens)
     assert st == pkv.PKV_OK and torch.equal(out, good)
     pool.close()
+
+
+@pytest.mark.parametrize("batch", [90, 100, 400])
+def test_bad_lengths_and_padding_inside_shares(batch):
+    """Sequences that are skipped, padding rows and good ones packed into the
+    same blocks; every good row right, every other left alone."""
+    rng = np.random.RandomState(batch)
+    lens = rng.randint(1, 400, batch)
+    lens[rng.rand(batch) < 0.2] = 0
+    bad = (rng.rand(batch) < 0.1) & (lens > 0)
+    c = W.Cache(lens.tolist(), seed=batch)
+    kp, vp = c.pools(lambda b: np.ones(lens[b], bool), float("nan"))
+    pool = _pool(c)
+    q = torch.randn(batch, 32, 64, generator=c.gen, device="cuda").bfloat16()
+    given = torch.tensor(np.where(bad, 5000, lens), dtype=torch.int32, device="cuda")
+    out = torch.full((batch, 32, 64), 7.5, device="cuda")
+    pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, given, out, 200, sinks=4)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_ERR_OUT_OF_RANGE
+    for b in range(batch):
+        if bad[b] or lens[b] == 0:
+            assert (out[b] == 7.5).all()
+        else:
+            ref, tol = W.attend(q[b:b + 1].double(), c.k[b].double(), c.v[b].double(),
+                                torch.tensor([lens[b] - 1], device="cuda"), 200, 4)
+            W.check(out[b:b + 1], ref, tol, f"sequence {b}")
+    # the tickets are whole again: a clean call on the same handle is right
+    given = c.lens_tensor()
+    pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, given, out, 200, sinks=4)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    for b in np.flatnonzero(lens):
+        ref, tol = W.attend(q[b:b + 1].double(), c.k[b].double(), c.v[b].double(),
+                            torch.tensor([lens[b] - 1], device="cuda"), 200, 4)
+        W.check(out[b:b + 1], ref, tol, f"sequence {b} again")
+    pool.close()
+
+
+def test_few_splits_allowed():
+    """max_splits of 1, 2 and 3 bound the ranges of a sequence."""
+    for max_splits in (1, 2, 3):
+        lens = [2048, 5, 1000, 700, 0, 2048] * 15
+        c = W.Cache(lens, seed=max_splits)
+        _decode(lens, 2048, 0, fused=True, seed=max_splits, pool=_pool(c, max_splits=max_splits))
 
 
 def test_captured_and_replayed_with_changing_lengths():
