@@ -117,7 +117,7 @@ pkv_status pkv_sched_finish(pkv_sched_t sched, int request_id);
  * can always finish whoever ends first. A fork extends work that was admitted,
  * so it does not queue: PKV_ERR_REJECTED, changing nothing, if the free credits
  * do not cover it now. Shared pages are freed when their last owner gives
- * them back.
+ * them back. In the counters a fork is a submission that was admitted.
  *
  * *count (0, or num_layers when length is not a whole number of pages) page
  * copies are due before the child is used: the first *tokens tokens of src[i] to

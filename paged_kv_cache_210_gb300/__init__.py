@@ -488,7 +488,7 @@ def pkv_axes_rope(cos, sin, axis_of_pair) -> AxesRope:
 
 def _rope_args(pool, rope, positions, tokens):
     """(rope, positions, stride) as the entry points take them; positions: int32
-    [axes][>= tokens]."""
+    [axes][>= tokens], or the address of [axes][tokens]."""
     if rope is None:
         if positions is not None:
             raise ValueError("rope_positions without rope")
@@ -497,6 +497,8 @@ def _rope_args(pool, rope, positions, tokens):
         raise ValueError("rope_positions: missing")
     if pool.device is not None and rope.device != pool.device:
         raise ValueError(f"rope_cos: expected a tensor on cuda:{pool.device}")
+    if isinstance(positions, int):       # a raw address: rows of `tokens` entries
+        return rope.address, positions, tokens
     if positions.dim() != 2 or positions.shape[0] < rope.num_axes or positions.shape[1] < tokens:
         raise ValueError(f"rope_positions: expected [{rope.num_axes}][>= {tokens}], got "
                          f"{tuple(positions.shape)}")

@@ -3,7 +3,9 @@
 // share, and the moves and block-table rewrites that compact a pool.
 //
 // The work is memory traffic alone: 64 KiB per whole page pair (K and V, read
-// and written), so HBM bounds it; small calls are bound by their launches.
+// and written), so HBM bounds it: 16,384 moves with their tables take 167 us
+// (6.4 TB/s, 96 % of the measured copy rate); small calls are bound by their
+// launch (128 pairs 2.5 us).
 // Whether a pair may be carried out depends on the whole list (a destination
 // must be named once and be nobody's source), so that is settled before any
 // byte moves: no order of the blocks can change the result.
@@ -24,8 +26,9 @@ constexpr int kCopyThreads = 128;
 constexpr int kPageVecs = kHkv * kPage * kRowBytes / 16;     // 16-byte vectors of a page: 1024
 constexpr int kVecsPerThread = kPageVecs / kCopyThreads;     // 8
 
-// Lists of up to this many pairs are checked by every copy block for itself
-// (one launch); longer ones are counted per page first.
+// Lists of up to this many pairs are checked by every copy block for itself,
+// in one launch (256 pairs 3.4 us); longer ones are counted per page first, in
+// two launches more (257 pairs 5.4 us), since the checks grow with n^2.
 constexpr int kScanPairs = 256;
 
 // How often each page is named: destinations in the low half of a page's

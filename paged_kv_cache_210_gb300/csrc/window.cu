@@ -494,19 +494,27 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // Before the wait (programmatic dependent launch) this block reads only
   // seq_lens, the block table, the rotary inputs and pool rows below the
   // appended position.
+  // A block without work leaves at once, but the first one waits all the same:
+  // a launch must not complete before the one ahead of it does, even if none
+  // of its rows has work (the launch after it waits for this one alone).
+  auto leave = [&]() {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
+  };
   int range = 0;
   int len;
   if (units) {
     const int u = static_cast<int>(blockIdx.x) / kHkv;
     if (!(prm.wave_units > 0 ? find_unit<false>(u, prm, sm, b, split, range, len)
-                             : find_unit<true>(u, prm, sm, b, split, range, len)))
+                             : find_unit<true>(u, prm, sm, b, split, range, len))) {
+      leave();
       return;
+    }
   } else {
     len = prm.seq_lens[b];
   }
-  if (len == 0) return;                                  // a padding row
-  if (len < 0 || len > prm.max_seq_len) {
-    if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrSeqLen);
+  if (len <= 0 || len > prm.max_seq_len) {               // a padding row (0), or a bad length
+    if (len != 0 && split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrSeqLen);
+    leave();
     return;
   }
   int rope_pos = 0;
@@ -552,6 +560,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   float ang_c = 1.f, ang_s = 0.f;                        // the angle of pair `lane`
   if (kRope && !load_pair_angle(prm.rope, rope_pos, lane, ang_c, ang_s)) {
     if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrPosition);
+    leave();
     return;                                              // every block of the sequence
   }
 
