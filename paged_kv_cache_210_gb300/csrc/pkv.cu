@@ -975,6 +975,8 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
   ok = ok && cudaMalloc(&pool->page_marks, static_cast<size_t>(c.num_pages) *
                                                (sizeof(unsigned long long) + sizeof(int))) ==
                  cudaSuccess;
+  ok = ok && cudaMalloc(&pool->prefill_next, 2 * sizeof(unsigned long long)) == cudaSuccess &&
+       cudaMemset(pool->prefill_next, 0, 2 * sizeof(unsigned long long)) == cudaSuccess;
   if (ok) pool->page_to = reinterpret_cast<int*>(pool->page_marks + c.num_pages);
 
   ok = ok && cudaMemset(pool->tickets, 0, 2 * static_cast<size_t>(c.max_batch) * kHkv * sizeof(int)) ==
@@ -1045,6 +1047,7 @@ pkv_status pkv_pool_destroy(pkv_pool_t pool) {
   cudaFree(pool->err);
   cudaFree(pool->seq_done);
   cudaFree(pool->page_marks);
+  cudaFree(pool->prefill_next);
   delete pool;
   return st;
 }

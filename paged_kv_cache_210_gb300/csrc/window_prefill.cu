@@ -17,32 +17,40 @@
 //    engine fills with zeros, so every step moves the same bytes;
 //  * page ids come straight from the block table, eight steps at a time, so
 //    the context's length does not appear in shared memory;
-//  * a tile has 32 tokens (128 rows) and two CTAs share an SM: behind a window
-//    a tile is a few steps long, and one CTA's start and end run under the
-//    other's steps;
+//  * a tile has 32 tokens (128 rows), two CTAs share an SM, and the CTAs of one
+//    wave draw their tiles from a counter: behind a window a tile is a few
+//    steps long, so the next tile's copies and scores run under the last one's
+//    end, and each CTA's start and end under the other's steps;
+//  * rows of V that no row of the tile sees are cleared by the V loader before
+//    it completes a stage, and a step's row masks are two 32-bit words, built
+//    only in steps on an edge (the diagonal, the window's start, the sinks'
+//    end) or with an invalid page;
 //  * probabilities enter the value product as three BF16 terms (24 bits) in
 //    columns of their own (S 64, P 96 and O 64 of the CTA's 256), so the next
 //    step's scores are computed as soon as this step's are in registers;
 //  * O leaves tensor memory every kSegment steps and is added up in FP32 in
 //    registers: a tensor-core sum drops the bits below its accumulator's last
 //    one, always downwards, 12 times a step, which over a 4,096-token window
-//    came to 1.5e-5 of the output (1e-6 with segments).
+//    came to 1.5e-5 of the output (1.1e-6 with segments).
 //
 // What bounds it: the softmax warps, two per scheduler. A step's arithmetic
 // (maximum, exponentials, sums, the split into three terms) takes two warps
 // 1,200 cycles by itself, measured alone; with the hand-offs it is about 2,000,
-// against 1,024 of the tensor pipe (two CTAs' 16 products of 32 cycles). Two
-// 4,096-token chunks behind a 4,096-token window: 520 us (530 TFLOP/s of score
-// and value products counted once); eight prompts of up to 2,048 tokens behind
-// 512: 159 us, of which a third is the start and end of the 8-step tiles. What
-// was measured on the way to the first of these: 718 us as a plain port of the
-// step loop; 696 with the products issued by a converged warp (one thread in a
-// divergent branch takes 55 cycles an issue for its operands); 654 with the
-// split's subtractions in mixed precision; 613 with O summed in registers
-// (192 a thread, setmaxnreg) instead of shared memory; 534 with one
-// hand-over of P per step, one flag instead of a step's edge tests and
-// failure paths placed out of line; 520 with page ids fetched ahead. Two
-// threads per row (16 warps) took 10 % longer than one at the same stage.
+// against 1,024 of the tensor pipe (two CTAs' 16 products of 32 cycles); a
+// tile's start and end cost it some 4,000 more. Two 4,096-token chunks behind a
+// 4,096-token window: 525 us (526 TFLOP/s of score and value products counted
+// once); eight prompts of up to 2,048 tokens behind 512: 123 us; sixteen of 512
+// tokens behind 128: 46 us. What was measured on the way, the first of these:
+// 718 us as a plain port of the step loop; 696 with the products issued by a
+// converged warp (one thread in a divergent branch takes 55 cycles an issue
+// for its operands); 654 with the split's subtractions in mixed precision; 613
+// with O summed in registers (192 a thread, setmaxnreg) instead of shared
+// memory; 534 with one hand-over of P per step, one flag instead of a step's
+// edge tests and failure paths placed out of line; 520 with page ids fetched
+// ahead. The second: 159 us up to there, one CTA per tile; 134 with tiles drawn
+// by resident CTAs, V cleared by its loader and results written through shared
+// memory; 123 with word masks. Two threads per row (16 softmax warps per SM)
+// took 10 % longer than one at the same stage.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -68,11 +76,12 @@ constexpr int kTileTokens = kRows / kGroup;          // 32 query tokens per CTA
 constexpr int kStepKeys = 64;                        // keys per step: the S MMA's N
 constexpr int kStepPages = kStepKeys / kPage;        // 4
 constexpr int kHalfKeys = kStepKeys / 2;             // keys of one P hand-over
-constexpr int kSoftmaxThreads = kRows;
 constexpr int kSoftmaxWarps = 4;                     // one per tensor-memory lane quarter
 constexpr int kLoadWarp = 4;                         // Q and K copies, then V (+ 1)
 constexpr int kScoreWarp = 6;                        // S products; then the value products (+ 1)
 constexpr int kThreads = 8 * 32;
+constexpr int kQBuffers = 2;
+constexpr int kWorkSlots = 4;                        // tiles the loaders may be ahead by
 constexpr int kKStages = 4;
 constexpr int kVStages = 3;
 constexpr int kCtasPerSm = 2;                        // they share an SM's 512 columns
@@ -90,17 +99,32 @@ constexpr int kOtherRegs = 64;
 static_assert(kSoftmaxRegs + kOtherRegs <= 2 * 128, "the launch's registers are split");
 constexpr uint32_t kStepBytes = kStepKeys * kRowBytes;
 
+// One tile of work, as the K loader hands it to the other warps; count 0: the end.
+struct TileWork {
+  int b;          // sequence
+  int g;          // KV head
+  int row;        // its first row of q and out
+  int p_first;    // position of that row
+  int count;      // rows, 1 .. 32
+  int bad_page;   // some page that counts has an invalid id
+};
+
 struct WindowPrefillSmem {                           // every tile 1024-byte aligned
-  uint8_t q[kRows * kRowBytes];                      // 16 KiB
+  uint8_t q[kQBuffers][kRows * kRowBytes];           // 2 x 16 KiB
   uint8_t k[kKStages][kStepBytes];                   // 4 x 8 KiB
   uint8_t v[kVStages][kStepBytes];                   // 3 x 8 KiB
-  unsigned long long bar_q, bar_k[kKStages], bar_v[kVStages];   // copies landed
-  unsigned long long k_free[kKStages], v_free[kVStages];        // stage read by its products
-  unsigned long long bar_s, s_free;                  // S(j) computed; in registers
-  unsigned long long bar_p, p_done;                  // P(j) written; multiplied
+  float4 stage[kRows][kDim / 8];                     // half of the rows' results, on their way out
+  unsigned long long bar_q[kQBuffers], bar_k[kKStages];   // copies landed
+  unsigned long long bar_v[kVStages];                // ... and rows no one sees cleared
+  unsigned long long q_free[kQBuffers];              // read by its tile's last scores
+  unsigned long long k_free[kKStages], v_free[kVStages];   // stage read by its products
+  unsigned long long work_full[kWorkSlots], work_free[kWorkSlots];
+  unsigned long long bar_edge;                       // V of an edge step landed
+  unsigned long long bar_s, s_free;                  // S of a step computed; in registers
+  unsigned long long bar_p, p_done;                  // P of a step written; multiplied
+  TileWork work[kWorkSlots];
   uint32_t tmem_base;
   int abort_flag;
-  int bad_page;
 };
 static_assert(offsetof(WindowPrefillSmem, k) % 1024 == 0 &&
                   offsetof(WindowPrefillSmem, v) % 1024 == 0,
@@ -114,14 +138,22 @@ struct WindowPrefillParams {
   const int32_t* start_pos;   // [batch]
   float* out;                 // [total][32][64]
   int* err;
+  unsigned long long* next_tile;   // shared by the launch's CTAs; zero before and after it
+  unsigned int* ctas_done;         // the same
   int num_pages;
   int table_stride;
   int max_seq_len;
-  int tiles_max;              // gridDim.y: tiles per sequence the launch covers
+  int batch;
+  int tiles_max;              // tiles per sequence the launch covers
   int total_tokens;
   int window;                 // 1 .. max_seq_len
   int sinks;                  // 0 .. max_seq_len
 };
+
+// The lowest n bits of 32 (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits32(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
 
 // Whether `x` holds, which is rare: the code under it is placed out of the
 // step loop's way.
@@ -145,17 +177,6 @@ __device__ __forceinline__ bool wait_phase(unsigned long long* bar, uint32_t par
   return __all_sync(0xffffffffu, done);
 }
 
-// V rows that no row of the tile sees (past its last key, or between the sinks
-// and the window) set to zero, so that p = 0 times them stays 0.
-__device__ __noinline__ void zero_rows(uint8_t* stage, int key0, int n_keys, int sinks, int lo) {
-  for (int idx = threadIdx.x; idx < kStepKeys * 8; idx += kSoftmaxThreads) {
-    const int key = key0 + (idx >> 3);
-    if (key >= n_keys || (key >= sinks && key < lo))
-      *reinterpret_cast<uint4*>(stage + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
-}
-
 // One lane of a converged warp, always the same. The issuing warps run their
 // loops whole and only the tcgen05 instructions under this predicate, so the
 // operands stay in uniform registers.
@@ -172,7 +193,9 @@ __device__ __forceinline__ bool elect_one() {
 // The largest of three (the last two given as bits).
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  asm("max.f32 %0, %1, %2, %3;"
+      : "=f"(d)
+      : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
   return d;
 }
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
@@ -232,9 +255,39 @@ struct TileView {
     plain_to = sink_steps + (p_first + 1) / kStepKeys - win_step;
   }
   __device__ int step(int j) const { return j < sink_steps ? j : j - sink_steps + win_step; }
+  // whether a step whose first key is key0 has keys that no row sees
+  __device__ bool has_dead(int key0) const {
+    return key0 + kStepKeys > n_keys || max(key0, sinks) < min(key0 + kStepKeys, lo);
+  }
   // whether logical page lp holds a key that some row sees
   __device__ bool wants(int lp) const {
     return lp * kPage < n_keys && ((lp + 1) * kPage > lo || lp * kPage < sinks);
+  }
+};
+
+// V rows that no row of the tile sees (past its last key, or between the sinks
+// and the window) set to zero, so that p = 0 times them stays 0. By one warp.
+__device__ __forceinline__ void zero_rows(uint8_t* stage, int key0, const TileView& view,
+                                          int lane) {
+  #pragma unroll 4
+  for (int idx = lane; idx < kStepKeys * 8; idx += 32) {
+    const int key = key0 + (idx >> 3);
+    if (key >= view.n_keys || (key >= view.sinks && key < view.lo))
+      *reinterpret_cast<uint4*>(stage + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+}
+
+// A step's place in a ring of stages, and how often the ring has gone round.
+template <int kStages>
+struct RingAt {
+  int stage = 0;
+  uint32_t round = 0;      // parity of the phase that the stage's barriers complete next
+  __device__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      round ^= 1u;
+    }
   }
 };
 
@@ -245,48 +298,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   WindowPrefillSmem& sm = *reinterpret_cast<WindowPrefillSmem*>(smem_raw + pad);
 
-  const int tile = prm.tiles_max - 1 - static_cast<int>(blockIdx.y);   // heaviest first
-  const int g = blockIdx.x;
-  const int b = blockIdx.z;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
+  const int lane = lane_of(tid);
 
   // the descriptors into the cache ahead of their first copies
   if (tid < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(
                      tid == 0 ? &tmap_q : tid == 1 ? &tmap_k : &tmap_v))
                  : "memory");
-  const int row0 = prm.cu_tokens[b];
-  const int n = prm.cu_tokens[b + 1] - row0;
-  const int start = prm.start_pos[b];
-  if (row0 < 0 || n < 0 || n > prm.total_tokens - row0) {   // rows outside the caller's buffers
-    if (blockIdx.y == 0 && g == 0 && tid == 0) set_error(prm.err, PKV_DEV_ERR_SEQ_LEN);
-    return;
-  }
-  if (blockIdx.y == 0 && g == 0 && tid == 0 && n > prm.tiles_max * kTileTokens)
-    set_error(prm.err, PKV_DEV_ERR_SEQ_LEN);
-  if (tile * kTileTokens >= n) return;                 // the whole CTA, before any allocation
-  if (start < 0 || start > prm.max_seq_len || n > prm.max_seq_len - start) {
-    if (tid == 0) set_error(prm.err, PKV_DEV_ERR_POSITION);
-    return;
-  }
-  const int t_valid = min(kTileTokens, n - tile * kTileTokens);
-  const TileView view(start + tile * kTileTokens, t_valid, prm.window, prm.sinks);
-  const int n_steps = view.n_steps;
-  const int32_t* trow = prm.table + static_cast<size_t>(b) * prm.table_stride;
-
-  if (warp == kLoadWarp && lane_of(tid) == 0) {
-    mbar_init(&sm.bar_q, 1);
+  if (warp == kLoadWarp && lane == 0) {
+    for (int i = 0; i < kQBuffers; ++i) mbar_init(&sm.bar_q[i], 1);
+    for (int i = 0; i < kQBuffers; ++i) mbar_init(&sm.q_free[i], 1);
     for (int i = 0; i < kKStages; ++i) mbar_init(&sm.bar_k[i], 1);
     for (int i = 0; i < kVStages; ++i) mbar_init(&sm.bar_v[i], 1);
     for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_free[i], 1);
     for (int i = 0; i < kVStages; ++i) mbar_init(&sm.v_free[i], 1);
+    for (int i = 0; i < kWorkSlots; ++i) mbar_init(&sm.work_full[i], 1);
+    // read by the V loader, the two issuing warps and the softmax warps
+    for (int i = 0; i < kWorkSlots; ++i) mbar_init(&sm.work_free[i], 3 + kSoftmaxWarps);
+    mbar_init(&sm.bar_edge, 1);
     mbar_init(&sm.bar_s, 1);
     mbar_init(&sm.s_free, kSoftmaxWarps);
     mbar_init(&sm.bar_p, kSoftmaxWarps);
     mbar_init(&sm.p_done, 1);
     sm.abort_flag = 0;
-    sm.bad_page = 0;
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -296,329 +332,462 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
 
+  // The n-th tile of this CTA, handed over by the K loader. One verdict per
+  // warp: false if it never comes.
+  auto next_work = [&](int n, TileWork& work) {
+    const int slot = n % kWorkSlots;
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm.work_full[slot], (n / kWorkSlots) & 1)))
+      return false;
+    work = sm.work[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.work_free[slot]);
+    return true;
+  };
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
+  };
+
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp < kScoreWarp) {
-      // ------------------------------------------------------------ copy engine
-      // Lanes 0..3 copy the step's 4 pages in one instruction once lane 0 saw
+      // ---------------------------------------------------------- copy engine
+      // Lanes 0..3 copy a step's 4 pages in one instruction once lane 0 saw
       // the stage free. A page that does not count is copied from past the
       // pool's end: zeros.
-      const int lane = lane_of(tid);
-      const bool is_v = warp != kLoadWarp;
-      const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-      const int stages = is_v ? kVStages : kKStages;
-      auto page_of = [&](int j, int e) {        // the e-th page of step j, past the end if none
-        int id = prm.num_pages;
-        if (j < n_steps) {
-          const int lp = view.step(j) * kStepPages + e;
-          if (view.wants(lp)) id = __ldg(trow + lp);
-          if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
+      // lane 4 s + e holds the e-th page of the s-th of 8 steps; the next 8
+      // steps' are fetched while these are in use
+      // V only: a step with rows that no one sees lands on a barrier of its
+      // own; the loader clears those rows and then completes the stage.
+      int edges = 0;
+      auto load_tile = [&](const TileView& view, const TileWork& work, const CUtensorMap* map,
+                           uint8_t* ring, unsigned long long* full, unsigned long long* free,
+                           auto& at, int& issued, int stages, bool is_v) {
+        const int32_t* trow = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
+        auto page_of = [&](int j, int e) {      // the e-th page of step j, past the end if none
+          int id = prm.num_pages;
+          if (j < view.n_steps) {
+            const int lp = view.step(j) * kStepPages + e;
+            if (view.wants(lp)) id = __ldg(trow + lp);
+            if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
+          }
+          return id;
+        };
+        int ids = page_of(lane / kStepPages, lane % kStepPages);
+        int ids_next = page_of(8 + lane / kStepPages, lane % kStepPages);
+        for (int j = 0; j < view.n_steps; ++j) {
+          if ((j & 7) == 0 && j > 0) {
+            ids = ids_next;
+            ids_next = page_of(j + 8 + lane / kStepPages, lane % kStepPages);
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, (j & 7) * kStepPages + lane % kStepPages);
+          const int key0 = view.step(j) * kStepKeys;
+          const bool edge = is_v && view.has_dead(key0);
+          unsigned long long* landed = edge ? &sm.bar_edge : &full[at.stage];
+          uint8_t* to = ring + at.stage * kStepBytes;
+          bool good = true;
+          if (lane == 0) {
+            good = *abort_flag == 0;
+            if (good && issued >= stages) good = mbar_wait(&free[at.stage], at.round ^ 1u);
+            if (good) mbar_arrive_expect_tx(landed, kStepBytes);
+          }
+          if (!__shfl_sync(0xffffffffu, good ? 1 : 0, 0)) return false;
+          if (lane < kStepPages)
+            tma_load_3d(to + lane * kPage * kRowBytes, map, 0, work.g * kPage, page, landed);
+          __syncwarp();
+          if (edge) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.bar_edge, edges & 1))) return false;
+            ++edges;
+            zero_rows(to, key0, view, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[at.stage]);
+          }
+          at.next();
+          ++issued;
         }
-        return id;
+        return true;
       };
-      // lane 4 s + e holds the e-th page of the s-th of 8 steps; the next 8 steps'
-      // are fetched while these are in use
-      int ids = page_of(lane / kStepPages, lane % kStepPages);
-      int ids_next = page_of(8 + lane / kStepPages, lane % kStepPages);
-      if (!is_v && lane == 0) {
-        mbar_arrive_expect_tx(&sm.bar_q, kRows * kRowBytes);
-        tma_load_3d(sm.q, &tmap_q, 0, g * kGroup, row0 + tile * kTileTokens, &sm.bar_q);
-      }
-      int issued = 0;
+      // every copy issued lands before the CTA frees its memory (bounded waits)
+      auto drain = [&](unsigned long long* full, int issued, int stages) {
+        if (lane == 0)
+          for (int s = 0; s < stages; ++s) {
+            const int uses = (issued - s + stages - 1) / stages;
+            if (uses > 0) mbar_wait(&full[s], (uses - 1) & 1);
+          }
+      };
       bool ok = true;
-      for (int j = 0; j < n_steps; ++j) {
-        const int st = j % stages;
-        unsigned long long* full = is_v ? &sm.bar_v[st] : &sm.bar_k[st];
-        if ((j & 7) == 0 && j > 0) {
-          ids = ids_next;
-          ids_next = page_of(j + 8 + lane / kStepPages, lane % kStepPages);
+      int issued = 0;
+      if (warp == kLoadWarp) {
+        // K, Q and the tiles themselves: the launch's CTAs draw them from one
+        // counter, heaviest first (the last tile of every sequence, then the
+        // one before it, ...), the 8 KV heads of a tile in a row
+        RingAt<kKStages> at;
+        int n = 0;                              // tiles handed over
+        auto hand_over = [&](const TileWork& work) {
+          const int slot = n % kWorkSlots;
+          bool good = true;
+          if (lane == 0) {
+            if (n >= kWorkSlots)
+              good = mbar_wait(&sm.work_free[slot], (n / kWorkSlots - 1) & 1);
+            if (good) {
+              sm.work[slot] = work;
+              mbar_arrive(&sm.work_full[slot]);
+            }
+          }
+          return __shfl_sync(0xffffffffu, good ? 1 : 0, 0) != 0;
+        };
+        const unsigned long long total =
+            static_cast<unsigned long long>(prm.tiles_max) * prm.batch * kHkv;
+        for (;;) {
+          // drawn once the last tile's copies are all on their way, a few
+          // steps before they are used up: any earlier, and a CTA would hold a
+          // tile back from those that run out of work
+          unsigned long long index = 0;
+          if (lane == 0) index = atomicAdd(prm.next_tile, 1ull);
+          index = __shfl_sync(0xffffffffu, index, 0);
+          if (index >= total) break;
+          const int g = static_cast<int>(index % kHkv);
+          const unsigned long long pair = index / kHkv;
+          const int ty = static_cast<int>(pair / static_cast<unsigned>(prm.batch));
+          const int b = static_cast<int>(pair % static_cast<unsigned>(prm.batch));
+          const int tile = prm.tiles_max - 1 - ty;
+          const int row0 = prm.cu_tokens[b];
+          const int rows = prm.cu_tokens[b + 1] - row0;
+          const int start = prm.start_pos[b];
+          // rows outside the caller's buffers
+          const bool bad_rows = row0 < 0 || rows < 0 || rows > prm.total_tokens - row0;
+          if (ty == 0 && g == 0 && lane == 0 && (bad_rows || rows > prm.tiles_max * kTileTokens))
+            set_error(prm.err, PKV_DEV_ERR_SEQ_LEN);
+          if (bad_rows || tile * kTileTokens >= rows) continue;
+          if (start < 0 || start > prm.max_seq_len || rows > prm.max_seq_len - start) {
+            if (lane == 0) set_error(prm.err, PKV_DEV_ERR_POSITION);
+            continue;
+          }
+          TileWork work;
+          work.b = b;
+          work.g = g;
+          work.row = row0 + tile * kTileTokens;
+          work.p_first = start + tile * kTileTokens;
+          work.count = min(kTileTokens, rows - tile * kTileTokens);
+          const TileView view(work.p_first, work.count, prm.window, prm.sinks);
+          const int32_t* trow = prm.table + static_cast<size_t>(b) * prm.table_stride;
+          // invalid ids among the pages that count
+          bool bad = false;
+          for (int i = lane; i < view.n_steps * kStepPages; i += 32) {
+            const int lp = view.step(i / kStepPages) * kStepPages + i % kStepPages;
+            if (!view.wants(lp)) continue;
+            const int id = __ldg(trow + lp);
+            bad |= id < 0 || id >= prm.num_pages;
+          }
+          work.bad_page = __any_sync(0xffffffffu, bad);
+          if (work.bad_page && lane == 0) set_error(prm.err, PKV_DEV_ERR_PAGE);
+          ok = hand_over(work);
+          if (ok) {
+            const int buffer = n % kQBuffers;
+            if (lane == 0) {
+              if (n >= kQBuffers)
+                ok = mbar_wait(&sm.q_free[buffer], (n / kQBuffers - 1) & 1);
+              if (ok) {
+                mbar_arrive_expect_tx(&sm.bar_q[buffer], kRows * kRowBytes);
+                tma_load_3d(sm.q[buffer], &tmap_q, 0, g * kGroup, work.row, &sm.bar_q[buffer]);
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          }
+          if (!ok) break;
+          ++n;
+          ok = load_tile(view, work, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued, kKStages,
+                         false);
+          if (!ok) break;
         }
-        const int page = __shfl_sync(0xffffffffu, ids, (j & 7) * kStepPages + lane % kStepPages);
-        bool good = true;
+        if (ok) {
+          TileWork end = {};
+          ok = hand_over(end);
+        }
+        if (!ok && lane == 0) give_up();
+        drain(sm.bar_k, issued, kKStages);
+        drain(sm.bar_q, n, kQBuffers);
+        // the last CTA to stop drawing leaves the counters at zero
         if (lane == 0) {
-          good = *abort_flag == 0;
-          if (good && j >= stages)
-            good = mbar_wait(is_v ? &sm.v_free[st] : &sm.k_free[st], ((j - stages) / stages) & 1);
-          if (good) mbar_arrive_expect_tx(full, kStepBytes);
+          __threadfence();
+          if (atomicAdd(prm.ctas_done, 1u) == gridDim.x - 1) {
+            *prm.next_tile = 0;
+            *prm.ctas_done = 0;
+          }
         }
-        if (!__shfl_sync(0xffffffffu, good ? 1 : 0, 0)) {
-          ok = false;
-          break;
+      } else {
+        RingAt<kVStages> at;
+        for (int n = 0;; ++n) {
+          TileWork work;
+          ok = next_work(n, work);
+          if (!ok || work.count == 0) break;
+          const TileView view(work.p_first, work.count, prm.window, prm.sinks);
+          ok = load_tile(view, work, &tmap_v, sm.v[0], sm.bar_v, sm.v_free, at, issued, kVStages,
+                         true);
+          if (!ok) break;
         }
-        if (lane < kStepPages)
-          tma_load_3d((is_v ? sm.v[st] : sm.k[st]) + lane * kPage * kRowBytes, map, 0, g * kPage,
-                      page, full);
-        __syncwarp();
-        ++issued;
-      }
-      if (lane == 0) {
-        if (!ok) {
-          *abort_flag = 1;
-          set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
-        }
-        // every copy issued lands before the CTA frees its memory (bounded waits)
-        if (!is_v) mbar_wait(&sm.bar_q, 0);
-        for (int s = 0; s < stages; ++s) {
-          const int uses = (issued - s + stages - 1) / stages;
-          if (uses > 0) mbar_wait(is_v ? &sm.bar_v[s] : &sm.bar_k[s], (uses - 1) & 1);
-        }
+        if (!ok && lane == 0) give_up();
+        drain(sm.bar_v, issued, kVStages);
       }
     } else {
-      // ------------------------------------------------------------ tensor cores
+      // ---------------------------------------------------------- tensor cores
       // One issuing warp for the scores and one for the values.
-      int issued = 0;
       bool ok = true;
+      uint32_t steps = 0;                       // of all tiles so far
       if (warp == kScoreWarp) {
         const uint32_t idesc_s = instr_desc(kRows, kStepKeys, false);
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q), 16, 1024);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_q, 0));
-        for (int j = 0; ok && j < n_steps; ++j) {
-          // S(j) = Q K(j)^T, once K(j) landed and S(j - 1) is in registers
-          if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
-                                           mbar_wait(&sm.bar_k[j % kKStages], (j / kKStages) & 1) &&
-                                           (j == 0 || mbar_wait(&sm.s_free, (j - 1) & 1)))) {
-            ok = false;
-            break;
+        RingAt<kKStages> at;
+        for (int n = 0; ok; ++n) {
+          TileWork work;
+          ok = next_work(n, work);
+          if (!ok || work.count == 0) break;
+          const TileView view(work.p_first, work.count, prm.window, prm.sinks);
+          const int buffer = n % kQBuffers;
+          const uint64_t q_desc = smem_desc_sw128(smem_u32(sm.q[buffer]), 16, 1024);
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_q[buffer], (n / kQBuffers) & 1));
+          for (int j = 0; ok && j < view.n_steps; ++j) {
+            // S = Q K^T, once K landed and the last step's S is in registers
+            const bool ready = *abort_flag == 0 && mbar_wait(&sm.bar_k[at.stage], at.round) &&
+                               (steps == 0 || mbar_wait(&sm.s_free, (steps - 1) & 1));
+            if (!__all_sync(0xffffffffu, ready)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[at.stage]), 16, 1024);
+            if (elect_one()) {
+              #pragma unroll
+              for (int kk = 0; kk < kDim / 16; ++kk)
+                mma_bf16(tmem, q_desc + kk * 2, k_desc + kk * 2, idesc_s, kk > 0);
+              mma_commit(&sm.bar_s);
+              mma_commit(&sm.k_free[at.stage]);
+              if (j == view.n_steps - 1) mma_commit(&sm.q_free[buffer]);
+            }
+            __syncwarp();
+            at.next();
+            ++steps;
           }
-          tc_fence_after();
-          const uint64_t k_desc = smem_desc_sw128(smem_u32(sm.k[j % kKStages]), 16, 1024);
-          if (elect_one()) {
-            #pragma unroll
-            for (int kk = 0; kk < kDim / 16; ++kk)
-              mma_bf16(tmem, q_desc + kk * 2, k_desc + kk * 2, idesc_s, kk > 0);
-            mma_commit(&sm.bar_s);
-            mma_commit(&sm.k_free[j % kKStages]);
-          }
-          __syncwarp();
-          ++issued;
         }
         // every product issued completes before the CTA frees its memory
-        if (issued > 0) mbar_wait(&sm.bar_s, (issued - 1) & 1);
+        if (steps > 0) mbar_wait(&sm.bar_s, (steps - 1) & 1);
       } else {
         const uint32_t idesc_o = instr_desc(kRows, kDim, true);
-        for (int j = 0; ok && j < n_steps; ++j) {
-          // O += P(j) V(j): 16 keys per product, P's three parts kPartCols
-          // columns apart in each half
-          if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
-                                           mbar_wait(&sm.bar_v[j % kVStages], (j / kVStages) & 1) &&
-                                           mbar_wait(&sm.bar_p, j & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[j % kVStages]), 8192, 1024);
-          if (elect_one()) {
-            #pragma unroll
-            for (int kk = 0; kk < kStepKeys / 16; ++kk) {
-              #pragma unroll
-              for (int part = 0; part < 3; ++part)
-                mma_bf16_tmem_a(tmem + kTmemO,
-                                tmem + kTmemP + (3 * (kk / 2) + part) * kPartCols + (kk % 2) * 8,
-                                v_desc + kk * (16 * kRowBytes >> 4), idesc_o,
-                                (j % kSegment > 0 || kk > 0 || part > 0) ? 1u : 0u);
+        RingAt<kVStages> at;
+        for (int n = 0; ok; ++n) {
+          TileWork work;
+          ok = next_work(n, work);
+          if (!ok || work.count == 0) break;
+          const TileView view(work.p_first, work.count, prm.window, prm.sinks);
+          for (int j = 0; j < view.n_steps; ++j) {
+            // O += P V: 16 keys per product, P's three parts kPartCols columns
+            // apart in each half
+            if (!__all_sync(0xffffffffu, *abort_flag == 0 &&
+                                             mbar_wait(&sm.bar_v[at.stage], at.round) &&
+                                             mbar_wait(&sm.bar_p, steps & 1))) {
+              ok = false;
+              break;
             }
-            mma_commit(&sm.p_done);
-            mma_commit(&sm.v_free[j % kVStages]);
+            tc_fence_after();
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[at.stage]), 8192, 1024);
+            if (elect_one()) {
+              #pragma unroll
+              for (int kk = 0; kk < kStepKeys / 16; ++kk) {
+                #pragma unroll
+                for (int part = 0; part < 3; ++part)
+                  mma_bf16_tmem_a(tmem + kTmemO,
+                                  tmem + kTmemP + (3 * (kk / 2) + part) * kPartCols + (kk % 2) * 8,
+                                  v_desc + kk * (16 * kRowBytes >> 4), idesc_o,
+                                  (j % kSegment > 0 || kk > 0 || part > 0) ? 1u : 0u);
+              }
+              mma_commit(&sm.p_done);
+              mma_commit(&sm.v_free[at.stage]);
+            }
+            __syncwarp();
+            at.next();
+            ++steps;
           }
-          __syncwarp();
-          ++issued;
         }
-        if (issued > 0) mbar_wait(&sm.p_done, (issued - 1) & 1);
+        if (steps > 0) mbar_wait(&sm.p_done, (steps - 1) & 1);
       }
-      if (!ok && lane_of(tid) == 0) {
-        *abort_flag = 1;
-        set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
-      }
+      if (!ok && lane == 0) give_up();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------ softmax warps
     const int r = tid;                                  // its MMA row = tensor-memory lane
     const int tok = r >> 2;                             // token of the tile, head r & 3
-    const int pos = view.p_first + min(tok, t_valid - 1);   // rows past the chunk mirror its last
     const float c = 1.4426950408889634f * 0.125f;       // log2(e) / sqrt(64)
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    float m_run = -INFINITY, l_run = 0.f;
-    float m_sum = -INFINITY;                            // the max that o_sum is taken against
-    float2 o_sum[kDim / 2];                             // earlier segments' O
-    #pragma unroll
-    for (int d = 0; d < kDim / 2; ++d) o_sum[d] = make_float2(0.f, 0.f);
     bool ok = true;
-    // invalid ids among the pages that count: flagged here, under the first copies
-    bool bad_page = false;
-    for (int i = tid; i < n_steps * kStepPages; i += kRows) {
-      const int lp = view.step(i / kStepPages) * kStepPages + i % kStepPages;
-      if (!view.wants(lp)) continue;
-      const int id = __ldg(trow + lp);
-      bad_page |= id < 0 || id >= prm.num_pages;
-    }
-    if (bad_page) {
-      set_error(prm.err, PKV_DEV_ERR_PAGE);
-      sm.bad_page = 1;
-    }
-    asm volatile("bar.sync 1, 128;" ::: "memory");       // the 4 softmax warps
-    const bool any_bad_page = *static_cast<volatile int*>(&sm.bad_page) != 0;
-    const int plain_from = any_bad_page ? n_steps : view.plain_from;
-    const int plain_count = any_bad_page ? 0 : max(view.plain_to - view.plain_from, 0);
-    int segment = 0;                                    // j % kSegment
-    for (int j = 0; j < n_steps; ++j) {
-      if (!wait_phase(&sm.bar_s, j & 1, abort_flag)) {
+    uint32_t steps = 0;                                 // of all tiles so far
+    for (int n = 0; ok; ++n) {
+      TileWork work;
+      ok = next_work(n, work);
+      if (!ok || work.count == 0) break;
+      const TileView view(work.p_first, work.count, prm.window, prm.sinks);
+      const int n_steps = view.n_steps;
+      const bool any_bad_page = work.bad_page != 0;
+      const int pos = view.p_first + min(tok, work.count - 1);  // rows past the end mirror the last
+      float m_run = -INFINITY, l_run = 0.f;
+      float m_sum = -INFINITY;                          // the max that o_sum is taken against
+      float2 o_sum[kDim / 2];                           // earlier segments' O
+      #pragma unroll
+      for (int d = 0; d < kDim / 2; ++d) o_sum[d] = make_float2(0.f, 0.f);
+      const int plain_from = any_bad_page ? n_steps : view.plain_from;
+      const int plain_count = any_bad_page ? 0 : max(view.plain_to - view.plain_from, 0);
+      int segment = 0;                                  // j % kSegment, kSegment before a join
+      for (int j = 0; j < n_steps; ++j, ++steps) {
+        if (!wait_phase(&sm.bar_s, steps & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[64];                                   // the row's 64 keys of the step
+        tmem_ld64(tmem + lane_addr, sv);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free);
+        const bool plain =
+            static_cast<unsigned>(j - plain_from) < static_cast<unsigned>(plain_count);
+        if (rarely(!plain)) {
+          const int key0 = view.step(j) * kStepKeys;
+          // bit i of seen[w]: key 32 w + i of the step is visible (one word test
+          // and one select per key: the code of an edge step is fetched anew
+          // each time, and a compare per condition and key made it 1,600
+          // cycles)
+          uint32_t seen[2];
+          #pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int base = key0 + 32 * w;
+            seen[w] = low_bits32(pos + 1 - base) &
+                      (low_bits32(view.sinks - base) | ~low_bits32(pos - prm.window + 1 - base));
+          }
+          if (any_bad_page) {
+            for (int e = 0; e < kStepPages; ++e) {
+              const int lp = key0 / kPage + e;
+              const int id = view.wants(lp) ? __ldg(prm.table + static_cast<size_t>(work.b) *
+                                                                    prm.table_stride + lp)
+                                            : -1;
+              if (id < 0 || id >= prm.num_pages) {
+                if (e < 2) {
+                  seen[0] &= ~(0xffffu << (16 * e));
+                } else {
+                  seen[1] &= ~(0xffffu << (16 * (e - 2)));
+                }
+              }
+            }
+          }
+          #pragma unroll
+          for (int i = 0; i < kStepKeys; ++i)
+            if (!((seen[i / 32] >> (i % 32)) & 1u)) sv[i] = __float_as_uint(-INFINITY);
+        }
+        float mx[4];
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(sv[e], sv[e + 4], sv[e + 8]);
+        #pragma unroll
+        for (int i = 12; i < 60; i += 8) {
+          #pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[i + e], sv[i + e + 4]);
+        }
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[60 + e]));
+        const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
+        // Once P(j - 1) V(j - 1) is done (P(j) V(j) cannot start before this
+        // thread hands over P(j)): after a segment O joins the sum, and
+        // elsewhere a row that grew its max rescales its O.
+        const bool join = segment == kSegment;
+        if (rarely(__any_sync(0xffffffffu, grow || join))) {
+          float alpha = 1.f;
+          if (grow) {
+            alpha = fast_exp2(m_run - m_step);
+            m_run = m_step;
+            l_run *= alpha;
+          }
+          if (j > 0) {
+            if (!wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
+            const float2 a2 = make_float2(alpha, alpha), b2 = make_float2(beta, beta);
+            #pragma unroll
+            for (int dh = 0; dh < 2; ++dh) {
+              uint32_t ov[32];
+              tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
+              if (join) {
+                #pragma unroll
+                for (int d = 0; d < 16; ++d) {
+                  const float2 x = __fmul2_rn(make_float2(__uint_as_float(ov[2 * d]),
+                                                          __uint_as_float(ov[2 * d + 1])), a2);
+                  o_sum[dh * 16 + d] = __ffma2_rn(o_sum[dh * 16 + d], b2, x);
+                }
+              } else {
+                #pragma unroll
+                for (int d = 0; d < 32; ++d)
+                  ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
+                tmem_st32(tmem + lane_addr + kTmemO + dh * 32, ov);
+              }
+            }
+            if (join) {
+              m_sum = m_run;
+              segment = 0;
+            }
+          }
+        }
+        ++segment;
+        // the probabilities, their sum and their three BF16 parts, 32 keys at a
+        // time; into tensor memory once the last step's product has read its P
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        const float2 c2 = make_float2(c, c);
+        const float2 nm2 = make_float2(-mu, -mu);
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[16], mid[16], lo[16];
+          #pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const int k = h * 32 + i;
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, nm2);
+            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], pp);
+            split3(pp.x, pp.y, hi[i / 2], mid[i / 2], lo[i / 2]);
+          }
+          if (h == 0 && steps > 0) {
+            if (!wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          const uint32_t p_half = tmem + lane_addr + kTmemP + 3 * h * kPartCols;
+          tmem_st16(p_half, hi);
+          tmem_st16(p_half + kPartCols, mid);
+          tmem_st16(p_half + 2 * kPartCols, lo);
+        }
+        if (rarely(!ok)) break;
+        const float2 a = __fadd2_rn(acc[0], acc[1]);
+        l_run += a.x + a.y;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.bar_p);
+      }
+      if (!ok || !wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t sv[64];                                   // the row's 64 keys of the step
-      tmem_ld64(tmem + lane_addr, sv);
-      tc_fence_before();
-      __syncwarp();
-      if (lane_of(tid) == 0) mbar_arrive(&sm.s_free);
-      const bool plain = static_cast<unsigned>(j - plain_from) < static_cast<unsigned>(plain_count);
-      if (rarely(!plain)) {
-        const int key0 = view.step(j) * kStepKeys;
-        const int last = pos - key0;                     // the row's last key, first windowed key
-        const int first = last - prm.window + 1;         // and sinks, within the step
-        const int sinks = view.sinks - key0;
-        if (key0 + kStepKeys - 1 > view.p_first) {
-          #pragma unroll
-          for (int i = 0; i < kStepKeys; ++i)
-            if (i > last) sv[i] = __float_as_uint(-INFINITY);
-        }
-        if (key0 <= view.p_last - prm.window && sinks < kStepKeys) {
-          if (sinks <= 0) {
-            #pragma unroll
-            for (int i = 0; i < kStepKeys; ++i)
-              if (i < first) sv[i] = __float_as_uint(-INFINITY);
-          } else {
-            #pragma unroll
-            for (int i = 0; i < kStepKeys; ++i)
-              if (i < first && i >= sinks) sv[i] = __float_as_uint(-INFINITY);
-          }
-        }
-        if (any_bad_page) {
-          #pragma unroll
-          for (int e = 0; e < kStepPages; ++e) {
-            const int lp = key0 / kPage + e;
-            const int id = view.wants(lp) ? __ldg(trow + lp) : -1;
-            if (id < 0 || id >= prm.num_pages) {
-              #pragma unroll
-              for (int i = 0; i < kPage; ++i) sv[e * kPage + i] = __float_as_uint(-INFINITY);
-            }
-          }
-        }
-        // V rows that no row of the tile sees, in pages that were read: past
-        // the last key, or between the sinks and the window
-        if (key0 + kStepKeys > view.n_keys ||
-            max(key0, view.sinks) < min(key0 + kStepKeys, view.lo)) {
-          if (!wait_phase(&sm.bar_v[j % kVStages], (j / kVStages) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          zero_rows(sm.v[j % kVStages], key0, view.n_keys, view.sinks, view.lo);
-        }
-      }
-      float mx[4];
-      #pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = max3(sv[e], sv[e + 4], sv[e + 8]);
-      #pragma unroll
-      for (int i = 12; i < 60; i += 8) {
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], sv[i + e], sv[i + e + 4]);
-      }
-      #pragma unroll
-      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[60 + e]));
-      const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
-      // Once P(j - 1) V(j - 1) is done (P(j) V(j) cannot start before this
-      // thread hands over P(j)): after a segment O joins the sum, and
-      // elsewhere a row that grew its max rescales its O.
-      const bool join = segment == kSegment;
-      if (rarely(__any_sync(0xffffffffu, grow || join))) {
-        float alpha = 1.f;
-        if (grow) {
-          alpha = fast_exp2(m_run - m_step);
-          m_run = m_step;
-          l_run *= alpha;
-        }
-        if (j > 0) {
-          if (!wait_phase(&sm.p_done, (j - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
-          const float2 a2 = make_float2(alpha, alpha), b2 = make_float2(beta, beta);
-          #pragma unroll
-          for (int dh = 0; dh < 2; ++dh) {
-            uint32_t ov[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
-            if (join) {
-              #pragma unroll
-              for (int d = 0; d < 16; ++d) {
-                const float2 x = __fmul2_rn(make_float2(__uint_as_float(ov[2 * d]),
-                                                        __uint_as_float(ov[2 * d + 1])), a2);
-                o_sum[dh * 16 + d] = __ffma2_rn(o_sum[dh * 16 + d], b2, x);
-              }
-            } else {
-              #pragma unroll
-              for (int d = 0; d < 32; ++d) ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
-              tmem_st32(tmem + lane_addr + kTmemO + dh * 32, ov);
-            }
-          }
-          if (join) {
-            m_sum = m_run;
-            segment = 0;
-          }
-        }
-      }
-      ++segment;
-      // the probabilities, their sum and their three BF16 parts, 32 keys at a
-      // time; into tensor memory once the last step's product has read its P
-      const float mu = m_run == -INFINITY ? 0.f : m_run;
-      const float2 c2 = make_float2(c, c);
-      const float2 nm2 = make_float2(-mu, -mu);
-      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t hi[16], mid[16], lo[16];
-        #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int k = h * 32 + i;
-          const float2 x = __ffma2_rn(
-              make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2, nm2);
-          const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], pp);
-          split3(pp.x, pp.y, hi[i / 2], mid[i / 2], lo[i / 2]);
-        }
-        if (h == 0 && j > 0) {
-          if (!wait_phase(&sm.p_done, (j - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-        }
-        const uint32_t p_half = tmem + lane_addr + kTmemP + 3 * h * kPartCols;
-        tmem_st16(p_half, hi);
-        tmem_st16(p_half + kPartCols, mid);
-        tmem_st16(p_half + 2 * kPartCols, lo);
-      }
-      if (rarely(!ok)) break;
-      const float2 a = __fadd2_rn(acc[0], acc[1]);
-      l_run += a.x + a.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane_of(tid) == 0) mbar_arrive(&sm.bar_p);
-    }
-    if (!ok) {
-      *abort_flag = 1;
-      set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
-    }
-    if (ok && wait_phase(&sm.p_done, (n_steps - 1) & 1, abort_flag)) {
-      tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
       const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
-      float* dst = prm.out + ((static_cast<size_t>(row0) + tile * kTileTokens + tok) * kHq +
-                              g * kGroup + (r & 3)) * kDim;
+      // Half a row at a time through shared memory, so that 8 lanes write 128
+      // contiguous bytes (a row per lane writes 32 half sectors at once: the
+      // four warps' stores then took 2,000 cycles a tile). Row r's chunk c is
+      // kept at c ^ (r % 8), different banks for 8 rows.
+      float4* rows_out = reinterpret_cast<float4*>(
+          prm.out + ((static_cast<size_t>(work.row) + warp * 8) * kHq + work.g * kGroup) * kDim);
       #pragma unroll
       for (int dh = 0; dh < 2; ++dh) {
         uint32_t ov[32];
@@ -626,15 +795,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         #pragma unroll
         for (int d = 0; d < 8; ++d) {
           const float2 was0 = o_sum[dh * 16 + 2 * d], was1 = o_sum[dh * 16 + 2 * d + 1];
-          if (tok < t_valid)
-            *reinterpret_cast<float4*>(dst + dh * 32 + 4 * d) =
-                make_float4(fmaf(was0.x, beta, __uint_as_float(ov[4 * d])) * inv,
-                            fmaf(was0.y, beta, __uint_as_float(ov[4 * d + 1])) * inv,
-                            fmaf(was1.x, beta, __uint_as_float(ov[4 * d + 2])) * inv,
-                            fmaf(was1.y, beta, __uint_as_float(ov[4 * d + 3])) * inv);
+          sm.stage[r][d ^ (r & 7)] =
+              make_float4(fmaf(was0.x, beta, __uint_as_float(ov[4 * d])) * inv,
+                          fmaf(was0.y, beta, __uint_as_float(ov[4 * d + 1])) * inv,
+                          fmaf(was1.x, beta, __uint_as_float(ov[4 * d + 2])) * inv,
+                          fmaf(was1.y, beta, __uint_as_float(ov[4 * d + 3])) * inv);
         }
+        __syncwarp();
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {           // token e of the warp's 8, its head lane / 8
+          const int row = 4 * e + (lane >> 3);
+          const float4 x = sm.stage[warp * 32 + row][(lane & 7) ^ (row & 7)];
+          if (warp * 8 + e < work.count)
+            rows_out[(e * kHq + (lane >> 3)) * (kDim / 4) + dh * 8 + (lane & 7)] = x;
+        }
+        __syncwarp();
       }
+      // O is in registers before the next tile's first P is handed over
+      tc_fence_before();
     }
+    if (!ok) give_up();
   }
   tc_fence_before();
   __syncthreads();
@@ -704,7 +884,13 @@ extern "C" pkv_status pkv_window_prefill_attention(
   prm.total_tokens = total_tokens;
   prm.window = std::min(window, c.max_seq_len);
   prm.sinks = std::min(sinks, c.max_seq_len);
-  window_prefill_kernel<<<dim3(kHkv, prm.tiles_max, batch), kThreads, kSmemBytes,
-                          static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, prm);
+  prm.batch = batch;
+  // every CTA of a wave takes tiles until none is left
+  prm.next_tile = pool->prefill_next;
+  prm.ctas_done = reinterpret_cast<unsigned int*>(pool->prefill_next + 1);
+  const long long tiles = static_cast<long long>(prm.tiles_max) * batch * kHkv;
+  const int ctas = static_cast<int>(std::min<long long>(tiles, kCtasPerSm * pool->num_sms));
+  window_prefill_kernel<<<ctas, kThreads, kSmemBytes, static_cast<cudaStream_t>(stream)>>>(
+      tq, tk, tv, prm);
   return pkv_check_launch();
 }
