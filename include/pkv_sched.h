@@ -109,7 +109,8 @@ pkv_status pkv_sched_extend_batch(pkv_sched_t sched, const int* ids, const int* 
 pkv_status pkv_sched_finish(pkv_sched_t sched, int request_id);
 
 /* Forks an active request after its first `length` tokens (1 <= length, at
- * most what pkv_sched_extend has made addressable): a new active request, last
+ * most the largest length pkv_sched_extend was given for it; their K/V are in
+ * the pages by the time the copies run): a new active request, last
  * in admission order, that shares the parent's pages of positions below
  * floor(length / page_size) * page_size and owns a page per layer for the rest.
  * Its budget is that of a submission with `length` prompt tokens and
@@ -133,7 +134,8 @@ pkv_status pkv_sched_fork(pkv_sched_t sched, int request_id, int length, int max
  * first_visible with `sinks` first tokens never reads again (pkv_window.h).
  * Their block-table entries become -1 and their credits return to the pool.
  * *released (may be NULL) is the number of pages. INVALID_ARG for an inactive
- * request, negative arguments or first_visible beyond the addressable length. */
+ * request, negative arguments or first_visible beyond the largest length
+ * pkv_sched_extend was given for it. */
 pkv_status pkv_sched_release(pkv_sched_t sched, int request_id, int first_visible, int sinks,
                              int* released);
 

@@ -452,6 +452,20 @@ def _arg(pool, name, x, count=0):
     return address
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _length(x):
+    """A window or sink count as the C int it becomes: any beyond an int means
+    the whole context, any negative one is refused."""
+    return x if 0 <= x <= _INT_MAX else _INT_MAX if x > 0 else -1
+
+
+def _int(x):
+    """A C int; a value outside its range becomes one that every call refuses."""
+    return x if -1 <= x <= _INT_MAX else -1
+
+
 def _pool_stream(pool, stream):
     """The stream's handle; by default the current stream of the handle's device."""
     if stream is None and pool.device is not None:
@@ -511,15 +525,15 @@ def pkv_window_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, seq
     """Decode attention over the last `window` tokens and the first `sinks` ones
     (q bf16 [B][32][64], out fp32). rope: an AxesRope, with rope_positions
     int32 [axes][B]: the queries are rotated first. seq_lens 0: a padding row."""
-    batch = _batch(seq_lens, batch)
+    batch = _int(_batch(seq_lens, batch))
     rows = batch * NUM_Q_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_attention(
-        pool.handle, int(layer), _arg(pool, "q", q, rows),
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows),
         _arg(pool, "k_pool", k_pool, pool.elements),
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
-        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
-        int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch, _int(int(num_splits)),
         _pool_stream(pool, stream))
     _check(st, "pkv_window_attention")
 
@@ -529,15 +543,15 @@ def pkv_window_append_attend(pool: Pool, layer, q, k, v, k_pool, v_pool, block_t
                              num_splits=0, stream=None):
     """Append (at seq_lens - 1, the key rotated with rope) and pkv_window_attention
     in one launch; k, v bf16 [B][8][64]."""
-    batch = _batch(seq_lens, batch)
+    batch = _int(_batch(seq_lens, batch))
     rows, new = batch * NUM_Q_HEADS * HEAD_DIM, batch * NUM_KV_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_append_attend(
-        pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
         _arg(pool, "v", v, new), _arg(pool, "k_pool", k_pool, pool.elements),
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
-        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), int(window),
-        int(sinks), *_rope_args(pool, rope, rope_positions, batch), batch, int(num_splits),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch, _int(int(num_splits)),
         _pool_stream(pool, stream))
     _check(st, "pkv_window_append_attend")
 
@@ -547,17 +561,17 @@ def pkv_window_prefill_attention(pool: Pool, layer, q, k_pool, v_pool, block_tab
                                  total_tokens=None, stream=None):
     """pkv_prefill_attention behind a window: every chunk token attends to the last
     `window` tokens up to itself and to the first `sinks` ones."""
-    batch = _batch(start_pos, batch)
-    total = int(q.shape[0]) if total_tokens is None else int(total_tokens)
+    batch = _int(_batch(start_pos, batch))
+    total = int(q.shape[0]) if total_tokens is None else _int(int(total_tokens))
     rows = total * NUM_Q_HEADS * HEAD_DIM
     st = pool._lib.pkv_window_prefill_attention(
-        pool.handle, int(layer), _arg(pool, "q", q, rows),
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows),
         _arg(pool, "k_pool", k_pool, pool.elements),
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
-        _arg(pool, "out", out, rows), int(window), int(sinks), batch, total,
-        int(max_chunk_tokens), _pool_stream(pool, stream))
+        _arg(pool, "out", out, rows), _length(int(window)), _length(int(sinks)),
+        batch, total, _int(int(max_chunk_tokens)), _pool_stream(pool, stream))
     _check(st, "pkv_window_prefill_attention")
 
 
@@ -569,17 +583,17 @@ def pkv_prefill_fill_axes(pool: Pool, layer, q, k, v, q_out, k_pool, v_pool, blo
     rope_positions: int32 [axes][>= T]."""
     if rope is None:
         raise ValueError("rope: missing")
-    batch = _batch(start_pos, batch)
-    total = int(k.shape[0]) if total_tokens is None else int(total_tokens)
+    batch = _int(_batch(start_pos, batch))
+    total = int(k.shape[0]) if total_tokens is None else _int(int(total_tokens))
     rows, new = total * NUM_Q_HEADS * HEAD_DIM, total * NUM_KV_HEADS * HEAD_DIM
     st = pool._lib.pkv_prefill_fill_axes(
-        pool.handle, int(layer), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
         _arg(pool, "v", v, new), _arg(pool, "q_out", q_out, rows),
         _arg(pool, "k_pool", k_pool, pool.elements),
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
-        *_rope_args(pool, rope, rope_positions, total), batch, total, int(max_chunk_tokens),
+        *_rope_args(pool, rope, rope_positions, total), batch, total, _int(int(max_chunk_tokens)),
         _pool_stream(pool, stream))
     _check(st, "pkv_prefill_fill_axes")
 
@@ -587,7 +601,7 @@ def pkv_prefill_fill_axes(pool: Pool, layer, q, k, v, q_out, k_pool, v_pool, blo
 def pkv_copy_pages(pool: Pool, src, dst, k_pool, v_pool, tokens=None, n=None, stream=None):
     """Copies page src[i] to page dst[i] in both pools: whole, or its first
     tokens[i] tokens (int32 tensors on the device)."""
-    n = int(src.shape[0]) if n is None else int(n)
+    n = int(src.shape[0]) if n is None else _int(int(n))
     st = pool._lib.pkv_copy_pages(
         pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
         _arg(pool, "tokens", tokens, n), _arg(pool, "k_pool", k_pool, pool.elements),
@@ -598,7 +612,7 @@ def pkv_copy_pages(pool: Pool, src, dst, k_pool, v_pool, tokens=None, n=None, st
 def pkv_compact_pages(pool: Pool, src, dst, k_pool, v_pool, block_tables, n=None, stream=None):
     """Moves page src[i] to page dst[i] in both pools and rewrites the block
     tables (all layers and rows) in place."""
-    n = int(src.shape[0]) if n is None else int(n)
+    n = int(src.shape[0]) if n is None else _int(int(n))
     st = pool._lib.pkv_compact_pages(
         pool.handle, _arg(pool, "src", src, n), _arg(pool, "dst", dst, n),
         _arg(pool, "k_pool", k_pool, pool.elements),

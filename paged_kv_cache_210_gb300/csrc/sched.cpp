@@ -25,7 +25,8 @@ struct Request {
   int64_t budget = 0;         // credits it reserves
   bool active = false;
   bool waited = false;
-  int pages_per_layer = 0;    // pages assigned in each layer
+  int pages_per_layer = 0;    // pages assigned in each layer (given back ones included)
+  int reach = 0;              // positions < reach are addressable
   std::vector<int32_t> pages; // [num_layers][max_pages_per_seq], first pages_per_layer valid
 };
 
@@ -98,9 +99,14 @@ pkv_status pkv_sched_create(const pkv_sched_config* config, pkv_sched_t* out) {
   if (!s) return PKV_ERR_INVALID_ARG;
   s->cfg = *config;
   s->max_pages_per_seq = config->max_seq_len / config->page_size;
-  s->free_heap.resize(static_cast<size_t>(config->num_pages));
+  try {
+    s->free_heap.resize(static_cast<size_t>(config->num_pages));
+    s->owners.assign(static_cast<size_t>(config->num_pages), 0);
+  } catch (const std::bad_alloc&) {
+    delete s;
+    return PKV_ERR_INVALID_ARG;
+  }
   for (int i = 0; i < config->num_pages; ++i) s->free_heap[i] = i;   // sorted: a valid min-heap
-  s->owners.assign(static_cast<size_t>(config->num_pages), 0);
   s->credits = config->num_pages;
   s->stats.pool_pages = config->num_pages;
   *out = s;
@@ -172,6 +178,7 @@ pkv_status extend_locked(pkv_sched* s, int request_id, int length) {
   if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
   Request& r = it->second;
   if (length < 0 || length > r.prefix) return PKV_ERR_INVALID_ARG;
+  r.reach = std::max(r.reach, length);
   const int need = (length + s->cfg.page_size - 1) / s->cfg.page_size;
   if (need > r.pages_per_layer) {
     for (int layer = 0; layer < s->cfg.num_layers; ++layer)
@@ -228,9 +235,10 @@ pkv_status pkv_sched_fork(pkv_sched_t s, int request_id, int length, int max_new
   if (capacity < s->cfg.num_layers) return PKV_ERR_INVALID_ARG;
   auto it = s->requests.find(request_id);
   if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
+  const Request& parent = it->second;   // stays in place when the map grows
   const int page = s->cfg.page_size;
-  if (length < 1 || length > static_cast<long long>(it->second.pages_per_layer) * page)
-    return PKV_ERR_INVALID_ARG;
+  // pages are shared only once nothing more will be written to them
+  if (length < 1 || length > parent.reach) return PKV_ERR_INVALID_ARG;
   Request r;
   r.prompt_tokens = length;
   if (budget_of(s->cfg, length, max_new_tokens, nullptr, &r.prefix, &r.budget) != PKV_OK)
@@ -239,7 +247,7 @@ pkv_status pkv_sched_fork(pkv_sched_t s, int request_id, int length, int max_new
   const bool partial = length % page != 0;
   int64_t holes = 0;   // shared places whose page the parent gave back
   for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
-    const int32_t* row = it->second.pages.data() + static_cast<size_t>(layer) * s->max_pages_per_seq;
+    const int32_t* row = parent.pages.data() + static_cast<size_t>(layer) * s->max_pages_per_seq;
     holes += std::count(row, row + shared, -1);
     // a partial page that the parent gave back cannot be copied
     if (partial && row[shared] < 0) return PKV_ERR_INVALID_ARG;
@@ -247,26 +255,34 @@ pkv_status pkv_sched_fork(pkv_sched_t s, int request_id, int length, int max_new
   r.budget -= holes;
   if (r.budget > s->credits) return PKV_ERR_REJECTED;
   r.active = true;
-  r.pages.assign(static_cast<size_t>(s->cfg.num_layers) * s->max_pages_per_seq, -1);
+  r.reach = length;
+  r.pages_per_layer = shared + (partial ? 1 : 0);
+  const int id = s->next_id;
+  Request* child = nullptr;
+  try {                // whatever may fail for memory comes before the first change
+    r.pages.assign(parent.pages.size(), -1);
+    s->active.reserve(s->active.size() + 1);
+    child = &s->requests.emplace(id, std::move(r)).first->second;
+  } catch (const std::bad_alloc&) {
+    return PKV_ERR_INVALID_ARG;
+  }
+  ++s->next_id;
   for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
     const size_t row = static_cast<size_t>(layer) * s->max_pages_per_seq;
     for (int i = 0; i < shared; ++i) {
-      const int32_t p = it->second.pages[row + i];
-      r.pages[row + i] = p;
+      const int32_t p = parent.pages[row + i];
+      child->pages[row + i] = p;
       if (p >= 0) ++s->owners[p];
     }
     if (partial) {
-      r.pages[row + shared] = s->take_page();
-      src[*count] = it->second.pages[row + shared];
-      dst[*count] = r.pages[row + shared];
+      child->pages[row + shared] = s->take_page();
+      src[*count] = parent.pages[row + shared];
+      dst[*count] = child->pages[row + shared];
       ++*count;
     }
   }
   if (partial) *tokens = length % page;
-  r.pages_per_layer = shared + (partial ? 1 : 0);
-  s->credits -= r.budget;
-  const int id = s->next_id++;
-  s->requests.emplace(id, std::move(r));
+  s->credits -= child->budget;
   s->active.push_back(id);
   ++s->stats.submitted;
   ++s->stats.admitted;
@@ -285,7 +301,7 @@ pkv_status pkv_sched_release(pkv_sched_t s, int request_id, int first_visible, i
   if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
   Request& r = it->second;
   const int page = s->cfg.page_size;
-  if (first_visible > static_cast<long long>(r.pages_per_layer) * page) return PKV_ERR_INVALID_ARG;
+  if (first_visible > r.reach) return PKV_ERR_INVALID_ARG;
   const int begin = sinks / page + (sinks % page != 0 ? 1 : 0);
   const int end = first_visible / page;
   int n = 0;
@@ -309,9 +325,14 @@ pkv_status pkv_sched_compact(pkv_sched_t s, int32_t* src, int32_t* dst, int capa
   if (!s || !count || capacity < 0 || (capacity > 0 && (!src || !dst))) return PKV_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> g(s->lock);
   *count = 0;
+  std::vector<int32_t> to;
+  try {
+    to.assign(s->owners.size(), -1);
+  } catch (const std::bad_alloc&) {
+    return PKV_ERR_INVALID_ARG;
+  }
   // the lowest free ids against the highest assigned ones, until they meet
   std::sort(s->free_heap.begin(), s->free_heap.end());   // sorted: a valid min-heap
-  std::vector<int32_t> to(s->owners.size(), -1);
   int n = 0;
   int32_t high = static_cast<int32_t>(s->owners.size()) - 1;
   while (n < capacity && n < static_cast<int>(s->free_heap.size())) {

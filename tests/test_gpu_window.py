@@ -467,14 +467,21 @@ def test_refusals():
     cos, sin = W.angles(50)
     rope = pkv.pkv_axes_rope(cos, sin, SECTIONS[2])
     pos = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    big = 2 ** 32      # wraps to small C ints: 2^32 + 5 must not become 5
 
     def call(window=8, sinks=0, layer=0, num_splits=0, batch=None, **kw):
         pkv.pkv_window_append_attend(pool, layer, q, k, k, kp, vp, c.tables, lens, out, window,
                                      sinks=sinks, num_splits=num_splits, batch=batch, **kw)
     call(rope=rope, rope_positions=pos)
     call(batch=0)
+    whole, wide = torch.zeros_like(out), torch.zeros_like(out)
+    for o, w in ((whole, 4096), (wide, big + 3)):
+        pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, lens, o, w)
+    assert torch.equal(whole, wide)
     for kw in (dict(window=0), dict(window=-3), dict(sinks=-1), dict(layer=1), dict(layer=-1),
-               dict(num_splits=-1), dict(num_splits=65), dict(batch=-1)):
+               dict(num_splits=-1), dict(num_splits=65), dict(batch=-1), dict(layer=big),
+               dict(window=5 - big), dict(sinks=3 - big), dict(num_splits=big + 1),
+               dict(batch=1 - big)):
         assert status(lambda: call(**kw)) == pkv.PKV_ERR_INVALID_ARG
     for kw in (dict(rope=rope), dict(rope_positions=pos), dict(batch=2),
                dict(rope=rope, rope_positions=pos[:1]),
