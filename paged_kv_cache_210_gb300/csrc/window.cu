@@ -294,10 +294,13 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
   #pragma unroll
   for (int e = 0; e < kHeld; ++e) held_len[e] = len_of(me + e * kGroupSize);
   #pragma unroll
-  for (int e = 0; e < kHeld; ++e) held[e] = pages_of(held_len[e]);
+  for (int e = 0; e < kHeld; ++e)
+    held[e] = prm.batch > e * kGroupSize ? pages_of(held_len[e]) : 0;
   auto each = [&](auto fn) {                  // for every sequence of this thread
+    fn(held[0]);
     #pragma unroll
-    for (int e = 0; e < kHeld; ++e) fn(held[e]);
+    for (int e = 1; e < kHeld; ++e)
+      if (prm.batch > e * kGroupSize) fn(held[e]);
     if (kBlock)
       for (int s = me + kHeld * kGroupSize; s < prm.batch; s += kGroupSize) fn(pages_of(len_of(s)));
   };
@@ -348,9 +351,10 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
     for (int k = kTries - 1; k >= 0; --k) {
       const int r = min((r0 * (kTries + k) + kTries - 1) / kTries, 131071);
       const float fr = static_cast<float>(r), inv = __frcp_rn(fr);
-      int units = 0;
+      int units = ceil_of(held[0], fr, inv);
       #pragma unroll
-      for (int e = 0; e < kHeld; ++e) units += ceil_of(held[e], fr, inv);
+      for (int e = 1; e < kHeld; ++e)
+        if (prm.batch > e * 32) units += ceil_of(held[e], fr, inv);
       if (static_cast<int>(__reduce_add_sync(0xffffffffu, units)) <= prm.wave_units) range = r;
     }
   }
@@ -491,6 +495,16 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  PageRing<kStagesW>& ws = sm.warp[warp];
+  unsigned long long* bars = sm.bar[warp];
+  if (lane == 0) {
+    for (int s = 0; s < kStagesW; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      prefetch_tensormap(&tmap_k);
+      prefetch_tensormap(&tmap_v);
+    }
+  }
   // Before the wait (programmatic dependent launch) this block reads only
   // seq_lens, the block table, the rotary inputs and pool rows below the
   // appended position.
@@ -564,16 +578,6 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
     return;                                              // every block of the sequence
   }
 
-  PageRing<kStagesW>& ws = sm.warp[warp];
-  unsigned long long* bars = sm.bar[warp];
-  if (lane == 0) {
-    for (int s = 0; s < kStagesW; ++s) mbar_init(&bars[s], 1);
-    fence_mbar_init();
-    if (warp == 0) {
-      prefetch_tensormap(&tmap_k);
-      prefetch_tensormap(&tmap_v);
-    }
-  }
   if (kCluster && n_splits > 1) async_inbox_setup(inbox);
   __syncwarp();
 
