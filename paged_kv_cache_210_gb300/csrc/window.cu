@@ -12,6 +12,17 @@
 // through its own ring of stages, filled by the tensor copy engine. Splits
 // merge inside the launch: through a thread-block cluster's shared memory,
 // or through global partials and a ticket.
+//
+// What bounds it: the bytes of the visible pages, 4 KiB per (page, kv head).
+// 4 blocks of 4 warps with 3 stages keep 192 KiB in flight per SM. Four
+// sequences of 120,000 to 131,072 tokens take 155 us (6.6 TB/s, 99 % of the
+// measured copy rate), 256 full 4,096-token windows 316 us (102 %), 256
+// ragged ones behind 4,096 tokens with append and rotation 107 us (89 %; the
+// last blocks' ranges are the rest). In smaller launches the latencies before
+// the first page lands are what is left: 64 ragged sequences behind 1,024 tokens
+// take 16.5 us, of which the block reads the lengths and finds its work for 2.1,
+// its page ids for 1.2, its first page for 2.4, and merges for 1.5 to 2.3; one
+// 517-token window 4.2 us. (Inputs larger than L2, launches in a graph.)
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -265,8 +276,10 @@ struct SeenPages {
 //  * a batch that may fit one wave of resident blocks (wave_units > 0) takes
 //    the smallest range of r0 (8 + k) / 8, r0 = T / wave_units, k < 8, whose
 //    units fit it: a second wave of full ranges costs more than longer ranges
-//    (32 sequences at a 1,024-token window: 15.2 us in one wave, 19.7 in two);
-//  * others take T / range_div, but at least least_pages.
+//    (32 full 1,024-token windows: 17.9 us in one wave, 20.6 in two);
+//  * others take T / range_div, range_div 3/5 of a wave, but at least
+//    least_pages (128 ragged sequences behind 1,024 tokens: 22.4 us; with 4/5
+//    25.8, with 17/10 28.5).
 // So there are fewer than batch + range_div units, or at most wave_units.
 // They are handed out largest first (all full ranges, then the short ones by
 // quarters of a range), so what does not fit the first wave is short (256

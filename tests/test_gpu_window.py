@@ -328,6 +328,39 @@ def test_full_window_agrees_with_the_full_attention():
     pool.close()
 
 
+def _relative(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+def test_outputs_are_those_of_fp32_arithmetic():
+    """Relative 2-norm error below 3e-6. A score is off by some sqrt(64) 2^-24 of
+    itself, weights by 2^-22, which leaves 3e-7; a value sum of the prefill takes
+    4 steps x 12 products on the tensor cores, each of which drops half of
+    2^-23 of the accumulator on average while it grows to its final size:
+    48 x 2^-24 / 2 = 1.4e-6. Probabilities of two BF16 terms would be off by
+    2^-16 / sqrt(12) = 4.4e-6."""
+    n, window, sinks = 2048, 700, 4
+    c = W.Cache([n, n])
+    kp, vp = c.pools(lambda b: np.ones(n, bool), 0.0)
+    pool = _pool(c)
+    at = torch.arange(n - 300, n, device="cuda")
+    q = torch.randn(600, 32, 64, generator=c.gen, device="cuda").bfloat16()
+    ref = torch.cat([W.attend(q[300 * b:300 * b + 300].double(), c.k[b].double(),
+                              c.v[b].double(), at, window, sinks)[0] for b in range(2)])
+    out = torch.zeros(600, 32, 64, device="cuda")
+    cu = torch.tensor([0, 300, 600], dtype=torch.int32, device="cuda")
+    start = torch.tensor([n - 300] * 2, dtype=torch.int32, device="cuda")
+    pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, cu, start, out, 300, window,
+                                     sinks=sinks)
+    assert _relative(out, ref) < 3e-6
+    last = q[[299, 599]].contiguous()
+    one = torch.zeros(2, 32, 64, device="cuda")
+    pkv.pkv_window_attention(pool, 0, last, kp, vp, c.tables, c.lens_tensor(), one, window,
+                             sinks=sinks)
+    assert _relative(one, ref[[299, 599]]) < 3e-6
+    pool.close()
+
+
 # ---------------------------------------------------------------- prefill
 def _prefill(chunks, starts, window, sinks, max_seq_len=2048, seed=11, junk="mixed", k_scale=1.0,
              max_chunk=None, **kw):
