@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         // one before it, ...), the 8 KV heads of a tile in a row
         RingAt<kKStages> at;
         int n = 0;                              // tiles handed over
+        int q_loads = 0;
         auto hand_over = [&](const TileWork& work) {
           const int slot = n % kWorkSlots;
           bool good = true;
@@ -438,13 +439,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         };
         const unsigned long long total =
             static_cast<unsigned long long>(prm.tiles_max) * prm.batch * kHkv;
-        for (;;) {
-          // drawn once the last tile's copies are all on their way, a few
-          // steps before they are used up: any earlier, and a CTA would hold a
-          // tile back from those that run out of work
-          unsigned long long index = 0;
-          if (lane == 0) index = atomicAdd(prm.next_tile, 1ull);
-          index = __shfl_sync(0xffffffffu, index, 0);
+        for (bool first = true;; first = false) {
+          // The first tile is this CTA's own (nothing to wait for); each other
+          // one is drawn once the last one's copies are all on their way, a
+          // few steps before they are used up: any earlier, and a CTA would
+          // hold a tile back from those that run out of work.
+          unsigned long long index = blockIdx.x;
+          if (!first) {
+            if (lane == 0) index = gridDim.x + atomicAdd(prm.next_tile, 1ull);
+            index = __shfl_sync(0xffffffffu, index, 0);
+          }
           if (index >= total) break;
           const int g = static_cast<int>(index % kHkv);
           const unsigned long long pair = index / kHkv;
@@ -471,6 +475,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           work.count = min(kTileTokens, rows - tile * kTileTokens);
           const TileView view(work.p_first, work.count, prm.window, prm.sinks);
           const int32_t* trow = prm.table + static_cast<size_t>(b) * prm.table_stride;
+          const int buffer = n % kQBuffers;
+          if (lane == 0) {
+            if (n >= kQBuffers) ok = mbar_wait(&sm.q_free[buffer], (n / kQBuffers - 1) & 1);
+            if (ok) {
+              mbar_arrive_expect_tx(&sm.bar_q[buffer], kRows * kRowBytes);
+              tma_load_3d(sm.q[buffer], &tmap_q, 0, g * kGroup, work.row, &sm.bar_q[buffer]);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          ++q_loads;
           // invalid ids among the pages that count
           bool bad = false;
           for (int i = lane; i < view.n_steps * kStepPages; i += 32) {
@@ -482,18 +497,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           work.bad_page = __any_sync(0xffffffffu, bad);
           if (work.bad_page && lane == 0) set_error(prm.err, PKV_DEV_ERR_PAGE);
           ok = hand_over(work);
-          if (ok) {
-            const int buffer = n % kQBuffers;
-            if (lane == 0) {
-              if (n >= kQBuffers)
-                ok = mbar_wait(&sm.q_free[buffer], (n / kQBuffers - 1) & 1);
-              if (ok) {
-                mbar_arrive_expect_tx(&sm.bar_q[buffer], kRows * kRowBytes);
-                tma_load_3d(sm.q[buffer], &tmap_q, 0, g * kGroup, work.row, &sm.bar_q[buffer]);
-              }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          }
           if (!ok) break;
           ++n;
           ok = load_tile(view, work, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued, kKStages,
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         }
         if (!ok && lane == 0) give_up();
         drain(sm.bar_k, issued, kKStages);
-        drain(sm.bar_q, n, kQBuffers);
+        drain(sm.bar_q, q_loads, kQBuffers);
         // the last CTA to stop drawing leaves the counters at zero
         if (lane == 0) {
           __threadfence();
