@@ -62,6 +62,7 @@ struct alignas(1024) WindowSmem {
     uint32_t c12[kWarps], c34[kWarps];
     int count[2][kWarps];
     int seq, split, len;
+    int4 unit;
   } find;
   int last;
 };
@@ -289,9 +290,9 @@ struct SeenPages {
 // length out of range has one, which reports it.
 //
 // kBlock: the block's threads share the batch, kHeld sequences each kept in
-// registers, the rest read again; otherwise (batch <= 32 kHeld) every warp
-// does it all without a barrier, which a small batch's latency would show.
-// Called by every thread of the block; false past the last unit.
+// registers, the rest read again, and all of them call; otherwise (batch <=
+// 32 kHeld) one warp calls, and does it all without a barrier. False past the
+// last unit.
 template <bool kBlock>
 __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, WindowSmem& sm, int& b,
                                           int& split, int& range, int& len) {
@@ -318,7 +319,7 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
       for (int s = me + kHeld * kGroupSize; s < prm.batch; s += kGroupSize) fn(pages_of(len_of(s)));
   };
   // ceil(p / r) by r's reciprocal, exact for p, r < 2^17 (the quotient of p + r -
-  // 1/2 stays 1 / (2 r) away from integers, the errors are below 2^-22 of it);
+  // 1/2 stays 1 / (2 r) away from integers, the errors are below 2^-21 of it);
   // adding 2^23 - 1/2 rounds it down into the low bits, without a conversion.
   auto ceil_of = [](int p, float r, float inv) {
     return __float_as_int(fmaf(static_cast<float>(p) + (r - 0.5f), inv, 8388607.5f)) - 0x4b000000;
@@ -363,7 +364,7 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
     #pragma unroll
     for (int k = kTries - 1; k >= 0; --k) {
       const int r = min((r0 * (kTries + k) + kTries - 1) / kTries, 131071);
-      const float fr = static_cast<float>(r), inv = __frcp_rn(fr);
+      const float fr = static_cast<float>(r), inv = __fdividef(1.f, fr);
       int units = ceil_of(held[0], fr, inv);
       #pragma unroll
       for (int e = 1; e < kHeld; ++e)
@@ -372,7 +373,7 @@ __device__ __forceinline__ bool find_unit(int u, const WindowParams& prm, Window
     }
   }
   range = min(range, max(most, 1));
-  const float f_range = static_cast<float>(range), inv_range = __frcp_rn(f_range);
+  const float f_range = static_cast<float>(range), inv_range = __fdividef(1.f, f_range);
   // a sequence's full ranges and the class of what is left: 1 (longest) .. 4, 0: nothing
   auto classify = [&](int p, int& full) {
     full = ceil_of(p + 1, f_range, inv_range) - 1;
@@ -531,8 +532,24 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
   int len;
   if (units) {
     const int u = static_cast<int>(blockIdx.x) / kHkv;
-    if (!(prm.wave_units > 0 ? find_unit<false>(u, prm, sm, b, split, range, len)
-                             : find_unit<true>(u, prm, sm, b, split, range, len))) {
+    bool found;
+    if (prm.wave_units > 0) {
+      // one warp searches: four doing the same compete for the issue slots
+      if (warp == 0) {
+        found = find_unit<false>(u, prm, sm, b, split, range, len);
+        if (lane == 0) sm.find.unit = found ? make_int4(b, split, range, len) : make_int4(-1, 0, 0, 0);
+      }
+      __syncthreads();
+      const int4 unit = sm.find.unit;
+      found = unit.x >= 0;
+      b = unit.x;
+      split = unit.y;
+      range = unit.z;
+      len = unit.w;
+    } else {
+      found = find_unit<true>(u, prm, sm, b, split, range, len);
+    }
+    if (!found) {
       leave();
       return;
     }
