@@ -68,9 +68,9 @@ typedef enum {
 
 /* Pool geometry. page_size, num_q_heads, num_kv_heads and head_dim must be
  * 16, 32, 8 and 64. max_seq_len is a multiple of 16, at most 2048 (more with
- * PKV_FLAG_LONG_CONTEXT), and sets the block-table row length (max_seq_len / 16). max_splits bounds the
- * split-KV count per sequence (0 selects 64; at most 128) and sizes the
- * handle's split workspace. flags: PKV_FLAG_* below (0 for none).
+ * PKV_FLAG_LONG_CONTEXT), and sets the block-table row length
+ * (max_seq_len / 16). max_splits bounds the split-KV count per sequence (0
+ * selects 64; at most 128) and sizes the handle's split workspace. flags: PKV_FLAG_* below (0 for none).
  * num_pages is the number of pages in the pool the caller allocates: 4096
  * pages is the pages' default 128 MiB pool
  * [samir-vllm: Build LLM Inference From Scratch in C++ and CUDA, "Hardware

@@ -12,10 +12,11 @@
  * Geometry, pools, block tables and dtypes are those of pkv.h and
  * pkv_prefill.h; a handle created with PKV_FLAG_LONG_CONTEXT raises
  * max_seq_len. Lists of int32 (seq_lens, cu_tokens, start_pos, rope_positions)
- * need 4-byte alignment only. Pages that hold no visible token are never read and their
- * block-table entries may hold anything (-1 after pkv_sched_release). Inside
- * a page that is read, tokens that no query of the sequence sees may hold any
- * bits, NaN and infinities included; visible K and V are finite.
+ * need 4-byte alignment only. Pages that hold no visible token are never
+ * read and their block-table entries may hold anything (-1 after
+ * pkv_sched_release). Inside a page that is read, tokens that no query of the
+ * sequence sees may hold any bits, NaN and infinities included; visible K and
+ * V are finite.
  *
  * An invalid page id is flagged and its tokens are skipped (weight 0); a row
  * all of whose visible tokens are skipped is 0.
@@ -77,9 +78,10 @@ pkv_status pkv_window_append_attend(pkv_pool_t pool, int layer, const void* q, c
 
 /* pkv_prefill_attention behind the window: the chunk token at position p
  * attends to the tokens visible from p. Its K/V must be in the pages already
- * (pkv_prefill_fill or pkv_prefill_fill_axes, earlier on the stream). Inside
- * a sequence, V of a token that some row of a 64-token tile of the chunk sees
- * must be finite for all rows of that tile. Errors as pkv_prefill_attention,
+ * (pkv_prefill_fill or pkv_prefill_fill_axes, earlier on the stream). V of
+ * a token that some row of a 32-token tile (counted from the chunk's first
+ * token) sees must be finite for the results of all rows of that tile; K that
+ * is not finite concerns the rows that see it alone. Errors as pkv_prefill_attention,
  * INVALID_ARG also for window < 1 and sinks < 0. */
 pkv_status pkv_window_prefill_attention(pkv_pool_t pool, int layer, const void* q,
                                         const void* k_pool, const void* v_pool,

@@ -533,8 +533,8 @@ def pkv_window_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, seq
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
-        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch, _int(int(num_splits)),
-        _pool_stream(pool, stream))
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch,
+        _int(int(num_splits)), _pool_stream(pool, stream))
     _check(st, "pkv_window_attention")
 
 
@@ -551,8 +551,8 @@ def pkv_window_append_attend(pool: Pool, layer, q, k, v, k_pool, v_pool, block_t
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries),
         _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
-        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch, _int(int(num_splits)),
-        _pool_stream(pool, stream))
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch,
+        _int(int(num_splits)), _pool_stream(pool, stream))
     _check(st, "pkv_window_append_attend")
 
 

@@ -3,7 +3,7 @@
 // writes q back and k and v into their pages.
 //
 // The work is memory traffic: 12 KiB per token (q, k, v read and written
-// once) against 7.5 KFLOP, so HBM bounds it: eight 4,096-token prompts 60.9 us
+// once) against 7.5 KFLOP, so HBM bounds it: eight 4,096-token prompts 60.4 us
 // (6.6 TB/s, 99 % of the measured copy rate), eight of 1,536 to 2,048 tokens
 // 28.3 us, of which the launch and the first loads are 2; a 77-token prompt 2.4
 // us, all latency.
@@ -22,7 +22,8 @@ using namespace pkv_axes_dev;
 
 namespace {
 
-constexpr int kFillWarps = 2;   // tokens per block (8: 31.0 us at eight 2,048-token prompts, 2: 28.3)
+// Tokens per block (8: 31.0 us at eight 2,048-token prompts, 2: 28.3).
+constexpr int kFillWarps = 2;
 
 struct FillParams {
   const uint16_t* q;

@@ -26,7 +26,8 @@ struct pkv_pool {
                                     // low half as destination, high half as source
   int* page_to;                     // [num_pages] 1 + where a page moves (0: it stays); follows
                                     // page_marks in one allocation
-  unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between launches)
+  unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between
+                                    // launches)
   int window_blocks_per_sm;         // resident blocks of the windowed decode's ticket shape
   int window_cluster_blocks_per_sm; // ... and of its cluster shape
   int layer_clusters[5];   // resident clusters of the multi-layer kernel, S = 1, 2, 4, 8, 16

@@ -17,10 +17,10 @@
 // 4 blocks of 4 warps with 3 stages keep 192 KiB in flight per SM. Four
 // sequences of 120,000 to 131,072 tokens take 155 us (6.6 TB/s, 99 % of the
 // measured copy rate), 256 full 4,096-token windows 316 us (102 %), 256
-// ragged ones behind 4,096 tokens with append and rotation 107 us (89 %; the
+// ragged ones behind 4,096 tokens with append and rotation 106.5 us (90 %; the
 // last blocks' ranges are the rest). In smaller launches the latencies before
 // the first page lands are what is left: 64 ragged sequences behind 1,024 tokens
-// take 16.5 us, of which the block reads the lengths and finds its work for 2.1,
+// take 15.5 us, of which the block reads the lengths and finds its work for 1.7,
 // its page ids for 1.2, its first page for 2.4, and merges for 1.5 to 2.3; one
 // 517-token window 4.2 us. (Inputs larger than L2, launches in a graph.)
 
@@ -140,8 +140,10 @@ __device__ __forceinline__ void load_queries(const uint16_t* qrow, int lane, flo
       const float2 own = bf16x2_to_float2(w[i]);
       const float2 par = bf16x2_to_float2(pw);
       const int pair = 16 * (qq & 1) + 2 * i;
-      const float c0 = __shfl_sync(0xffffffffu, c, pair), c1 = __shfl_sync(0xffffffffu, c, pair + 1);
-      const float s0 = __shfl_sync(0xffffffffu, s, pair), s1 = __shfl_sync(0xffffffffu, s, pair + 1);
+      const float c0 = __shfl_sync(0xffffffffu, c, pair);
+      const float c1 = __shfl_sync(0xffffffffu, c, pair + 1);
+      const float s0 = __shfl_sync(0xffffffffu, s, pair);
+      const float s1 = __shfl_sync(0xffffffffu, s, pair + 1);
       const float sgn = qq < 2 ? -1.f : 1.f;
       const float r0 = __fadd_rn(__fmul_rn(own.x, c0), sgn * __fmul_rn(par.x, s0));
       const float r1 = __fadd_rn(__fmul_rn(own.y, c1), sgn * __fmul_rn(par.y, s1));
@@ -277,14 +279,14 @@ struct SeenPages {
 //  * a batch that may fit one wave of resident blocks (wave_units > 0) takes
 //    the smallest range of r0 (8 + k) / 8, r0 = T / wave_units, k < 8, whose
 //    units fit it: a second wave of full ranges costs more than longer ranges
-//    (32 full 1,024-token windows: 17.9 us in one wave, 20.6 in two);
+//    (32 full 1,024-token windows: 17.1 us in one wave, 20.6 in two);
 //  * others take T / range_div, range_div 3/5 of a wave, but at least
-//    least_pages (128 ragged sequences behind 1,024 tokens: 22.4 us; with 4/5
+//    least_pages (128 ragged sequences behind 1,024 tokens: 22.0 us; with 4/5
 //    25.8, with 17/10 28.5).
 // So there are fewer than batch + range_div units, or at most wave_units.
 // They are handed out largest first (all full ranges, then the short ones by
 // quarters of a range), so what does not fit the first wave is short (256
-// ragged sequences behind 4,096 tokens: 105.9 us, in batch order 124.2). Each
+// ragged sequences behind 4,096 tokens: 106.5 us, in batch order 124.2). Each
 // block finds its own unit: sums over the batch, the class of size the unit
 // falls into, and a prefix sum within it. Padding rows have no units; a
 // length out of range has one, which reports it.
@@ -822,7 +824,7 @@ struct WindowPlan {
 };
 
 // Small batches take a cluster per (sequence, kv head): its merge is shorter
-// than the ticket's (us, one 2,048-token sequence: cluster of 12 5.8, units
+// than the ticket's (us, one 2,048-token sequence: cluster of 12 5.7, units
 // 6.8; 4 sequences at a 1,024-token window: 6.0 and 6.9), as long as all blocks
 // are resident at once (4 sequences, cluster of 16: 9.4) and either fill half
 // of the slots or have few pages (one 131,072-token sequence: cluster of 12

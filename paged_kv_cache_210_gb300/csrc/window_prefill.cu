@@ -38,9 +38,9 @@
 // 1,200 cycles by itself, measured alone; with the hand-offs it is about 2,000,
 // against 1,024 of the tensor pipe (two CTAs' 16 products of 32 cycles); a
 // tile's start and end cost it some 4,000 more. Two 4,096-token chunks behind a
-// 4,096-token window: 525 us (526 TFLOP/s of score and value products counted
-// once); eight prompts of up to 2,048 tokens behind 512: 123 us; sixteen of 512
-// tokens behind 128: 46 us. What was measured on the way, the first of these:
+// 4,096-token window: 523 us (527 TFLOP/s of score and value products counted
+// once); eight prompts of up to 2,048 tokens behind 512: 122 us; sixteen of 512
+// tokens behind 128: 45 us. What was measured on the way, the first of these:
 // 718 us as a plain port of the step loop; 696 with the products issued by a
 // converged warp (one thread in a divergent branch takes 55 cycles an issue
 // for its operands); 654 with the split's subtractions in mixed precision; 613
@@ -49,8 +49,9 @@
 // edge tests and failure paths placed out of line; 520 with page ids fetched
 // ahead. The second: 159 us up to there, one CTA per tile; 134 with tiles drawn
 // by resident CTAs, V cleared by its loader and results written through shared
-// memory; 123 with word masks. Two threads per row (16 softmax warps per SM)
-// took 10 % longer than one at the same stage.
+// memory; 123 with word masks; 122 with a first tile that needs no draw. Two
+// threads per row (16 softmax warps per SM) took 10 % longer than one at the
+// same stage.
 
 #include <cuda.h>
 #include <cuda_runtime.h>

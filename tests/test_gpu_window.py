@@ -424,6 +424,35 @@ def test_prefill_pages_past_four_gib():
     _prefill([100], [30], 64, 4, junk=float("nan"), base_page=280000)
 
 
+@pytest.mark.parametrize("start,at", [(0, 0), (5, 40), (100, 131), (13, 111)])
+def test_prefill_rows_that_do_not_see_a_bad_token(start, at):
+    """A NaN key concerns the rows that see it, a NaN value the 32-token tiles that do."""
+    n, window = 150, 9
+    c = W.Cache([start + n])
+    q = torch.randn(n, 32, 64, device="cuda", generator=c.gen).bfloat16()
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    first = torch.tensor([start], dtype=torch.int32, device="cuda")
+    pos = torch.arange(start, start + n, device="cuda")
+    pool = _pool(c)
+    page, slot = int(c.table[0, 0, at // 16]), at % 16
+    seen = W.visible(pos, torch.tensor(at, device="cuda"), window, 0)
+    for which in (0, 1):
+        pools = c.pools(lambda b: np.ones(start + n, bool))
+        pools[which][page, :, slot] = float("nan")
+        out = torch.empty(n, 32, 64, device="cuda")
+        pkv.pkv_window_prefill_attention(pool, 0, q, *pools, c.tables, cu, first, out, n, window)
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+        hit = seen
+        if which == 1:
+            tiles = torch.arange(n, device="cuda") // 32
+            hit = torch.isin(tiles, tiles[seen])
+        assert bool(seen.any()) and not bool(hit.all())
+        assert torch.isnan(out[seen]).all()
+        ref, tol = W.attend(q[~hit].double(), c.k[0].double(), c.v[0].double(), pos[~hit], window,
+                            0)
+        W.check(out[~hit], ref, tol, f"start {start}, token {at}, pool {which}")
+
+
 def test_prefill_flags_bad_data():
     chunks, starts = [100, 100, 100], [0, 50, 0]
     lens = [100, 150, 100]
