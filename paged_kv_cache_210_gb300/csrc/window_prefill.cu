@@ -178,6 +178,35 @@ __device__ __forceinline__ bool wait_phase(unsigned long long* bar, uint32_t par
   return __all_sync(0xffffffffu, done);
 }
 
+// Whether a phase is complete, without waiting for it.
+__device__ __forceinline__ bool phase_done(unsigned long long* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// wait_phase after an early look at the phase: the barrier's own latency is
+// paid only where the look came too soon.
+__device__ __forceinline__ bool wait_phase_after(bool done, unsigned long long* bar,
+                                                 uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, done)) return true;
+  return wait_phase(bar, parity, abort_flag);
+}
+
+// Lane 0's arrival, predicated instead of branched around.
+__device__ __forceinline__ void arrive_lane0(unsigned long long* bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lane)
+      : "memory");
+}
+
 // One lane of a converged warp, always the same. The issuing warps run their
 // loops whole and only the tcgen05 instructions under this predicate, so the
 // operands stay in uniform registers.
@@ -201,6 +230,19 @@ __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
 }
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
   return max3(__uint_as_float(a), b, c);
+}
+
+// 16 consecutive columns, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // 64 consecutive 32-bit columns of this thread's tensor-memory lane.
@@ -639,9 +681,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
       for (int d = 0; d < kDim / 2; ++d) o_sum[d] = make_float2(0.f, 0.f);
       const int plain_from = any_bad_page ? n_steps : view.plain_from;
       const int plain_count = any_bad_page ? 0 : max(view.plain_to - view.plain_from, 0);
+      bool s_done = false;                              // the next step's S is known to be there
       int segment = 0;                                  // j % kSegment, kSegment before a join
       for (int j = 0; j < n_steps; ++j, ++steps) {
-        if (!wait_phase(&sm.bar_s, steps & 1, abort_flag)) {
+        if (!wait_phase_after(s_done, &sm.bar_s, steps & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -650,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         tmem_ld64(tmem + lane_addr, sv);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free);
+        arrive_lane0(&sm.s_free, lane);
         const bool plain =
             static_cast<unsigned>(j - plain_from) < static_cast<unsigned>(plain_count);
         if (rarely(!plain)) {
@@ -697,11 +740,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[60 + e]));
         const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
-        // Once P(j - 1) V(j - 1) is done (P(j) V(j) cannot start before this
-        // thread hands over P(j)): after a segment O joins the sum, and
-        // elsewhere a row that grew its max rescales its O.
-        const bool join = segment == kSegment;
-        if (rarely(__any_sync(0xffffffffu, grow || join))) {
+        if (rarely(__any_sync(0xffffffffu, grow))) {
           float alpha = 1.f;
           if (grow) {
             alpha = fast_exp2(m_run - m_step);
@@ -714,42 +753,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
               break;
             }
             tc_fence_after();
-            const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
-            const float2 a2 = make_float2(alpha, alpha), b2 = make_float2(beta, beta);
             #pragma unroll
-            for (int dh = 0; dh < 2; ++dh) {
-              uint32_t ov[32];
-              tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
-              if (join) {
-                #pragma unroll
-                for (int d = 0; d < 16; ++d) {
-                  const float2 x = __fmul2_rn(make_float2(__uint_as_float(ov[2 * d]),
-                                                          __uint_as_float(ov[2 * d + 1])), a2);
-                  o_sum[dh * 16 + d] = __ffma2_rn(o_sum[dh * 16 + d], b2, x);
-                }
-              } else {
-                #pragma unroll
-                for (int d = 0; d < 32; ++d)
-                  ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
-                tmem_st32(tmem + lane_addr + kTmemO + dh * 32, ov);
-              }
+            for (int dq = 0; dq < 4; ++dq) {
+              uint32_t ov[16];
+              tmem_ld16(tmem + lane_addr + kTmemO + dq * 16, ov);
+              #pragma unroll
+              for (int d = 0; d < 16; ++d)
+                ov[d] = __float_as_uint(__uint_as_float(ov[d]) * alpha);
+              tmem_st16(tmem + lane_addr + kTmemO + dq * 16, ov);
             }
-            if (join) {
-              m_sum = m_run;
-              segment = 0;
-            }
+            tmem_wait_st();
           }
         }
-        ++segment;
-        // the probabilities, their sum and their three BF16 parts, 32 keys at a
-        // time; into tensor memory once the last step's product has read its P
-        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        // The probabilities, their sum and their three BF16 parts, 32 keys at a
+        // time. The first half does not wait for the step's maximum: it uses
+        // the running one, and is done again for a row that outgrew it.
+        const bool p_free = phase_done(&sm.p_done, (steps - 1) & 1);
         const float2 c2 = make_float2(c, c);
-        const float2 nm2 = make_float2(-mu, -mu);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi[16], mid[16], lo[16];
+        float2 acc[2];
+        auto half_of_p = [&](int h, uint32_t (&hi)[16], uint32_t (&mid)[16], uint32_t (&lo)[16]) {
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          const float2 nm2 = make_float2(-mu, -mu);
           #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const int k = h * 32 + i;
@@ -759,25 +783,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
             acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], pp);
             split3(pp.x, pp.y, hi[i / 2], mid[i / 2], lo[i / 2]);
           }
-          if (h == 0 && steps > 0) {
-            if (!wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
+        };
+        auto store_half = [&](int h, const uint32_t (&hi)[16], const uint32_t (&mid)[16],
+                              const uint32_t (&lo)[16]) {
+          const uint32_t p_half = tmem + lane_addr + kTmemP + 3 * h * kPartCols;
+          tmem_st16(p_half, hi);
+          tmem_st16(p_half + kPartCols, mid);
+          tmem_st16(p_half + 2 * kPartCols, lo);
+        };
+        {
+          uint32_t hi[16], mid[16], lo[16];
+          acc[0] = acc[1] = make_float2(0.f, 0.f);
+          half_of_p(0, hi, mid, lo);
+          if (steps > 0) {
+            if (!wait_phase_after(p_free, &sm.p_done, (steps - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          const uint32_t p_half = tmem + lane_addr + kTmemP + 3 * h * kPartCols;
-          tmem_st16(p_half, hi);
-          tmem_st16(p_half + kPartCols, mid);
-          tmem_st16(p_half + 2 * kPartCols, lo);
+          store_half(0, hi, mid, lo);
         }
-        if (rarely(!ok)) break;
+        // after a segment O joins the sum (the next product, P(j) V(j), starts
+        // from zero once this thread hands over P(j))
+        if (rarely(segment == kSegment)) {
+          const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
+          const float2 b2 = make_float2(beta, beta);
+          #pragma unroll
+          for (int dh = 0; dh < 2; ++dh) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lane_addr + kTmemO + dh * 32, ov);
+            #pragma unroll
+            for (int d = 0; d < 16; ++d)
+              o_sum[dh * 16 + d] = __ffma2_rn(
+                  o_sum[dh * 16 + d], b2,
+                  make_float2(__uint_as_float(ov[2 * d]), __uint_as_float(ov[2 * d + 1])));
+          }
+          m_sum = m_run;
+          segment = 0;
+        }
+        ++segment;
+        {
+          uint32_t hi[16], mid[16], lo[16];
+          half_of_p(1, hi, mid, lo);
+          store_half(1, hi, mid, lo);
+        }
+        s_done = phase_done(&sm.bar_s, (steps + 1) & 1);
         const float2 a = __fadd2_rn(acc[0], acc[1]);
         l_run += a.x + a.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar_p);
+        arrive_lane0(&sm.bar_p, lane);
       }
       if (!ok || !wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
         ok = false;
