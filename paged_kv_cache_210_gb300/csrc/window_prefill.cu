@@ -3,7 +3,7 @@
 // include/pkv_window.h).
 //
 // out_i = sum_t p_it V_t / sum_t p_it, p_it = 2^(q_i.K_t log2(e) / 8 - m_i), over
-// the tokens visible from position p_i: one pass per 64-token query tile
+// the tokens visible from position p_i: one pass per 32-token query tile
 // with a running maximum m_i and sum per row.
 //
 // Like the full-context kernel (prefill.cu) a CTA takes the rows (token x 4
@@ -33,25 +33,30 @@
 //    one, always downwards, 12 times a step, which over a 4,096-token window
 //    came to 1.5e-5 of the output (1.1e-6 with segments).
 //
-// What bounds it: the softmax warps, two per scheduler. A step's arithmetic
-// (maximum, exponentials, sums, the split into three terms) takes two warps
-// 1,200 cycles by itself, measured alone; with the hand-offs it is about 2,000,
-// against 1,024 of the tensor pipe (two CTAs' 16 products of 32 cycles); a
-// tile's start and end cost it some 4,000 more. Two 4,096-token chunks behind a
-// 4,096-token window: 523 us (527 TFLOP/s of score and value products counted
-// once); eight prompts of up to 2,048 tokens behind 512: 122 us; sixteen of 512
-// tokens behind 128: 45 us. What was measured on the way, the first of these:
-// 718 us as a plain port of the step loop; 696 with the products issued by a
-// converged warp (one thread in a divergent branch takes 55 cycles an issue
-// for its operands); 654 with the split's subtractions in mixed precision; 613
-// with O summed in registers (192 a thread, setmaxnreg) instead of shared
-// memory; 534 with one hand-over of P per step, one flag instead of a step's
-// edge tests and failure paths placed out of line; 520 with page ids fetched
-// ahead. The second: 159 us up to there, one CTA per tile; 134 with tiles drawn
-// by resident CTAs, V cleared by its loader and results written through shared
-// memory; 123 with word masks; 122 with a first tile that needs no draw. Two
-// threads per row (16 softmax warps per SM) took 10 % longer than one at the
-// same stage.
+// What bounds it: the softmax warps, two per scheduler, and of their time less
+// the arithmetic (maximum, exponentials, sums, the split into three terms: 1,200
+// cycles for two warps by itself, measured alone) than what a warp waits for in
+// turn: its barriers, tensor memory, votes and instructions. A step of two CTAs
+// takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
+// cycles each); a tile's start and end cost it some 4,000 more. The products are
+// never waited for: every barrier of theirs is complete when it is first looked
+// at. Two 4,096-token chunks behind a 4,096-token window: 472 us (585 TFLOP/s of
+// score and value products counted once); eight prompts of up to 2,048 tokens
+// behind 512: 116 us; sixteen of 512 tokens behind 128: 45.6 us. What was measured
+// on the way, the first of these: 718 us as a plain port of the step loop; 696
+// with the products issued by a converged warp (one thread in a divergent branch
+// takes 55 cycles an issue for its operands); 654 with the split's subtractions
+// in mixed precision; 613 with O summed in registers (192 a thread, setmaxnreg)
+// instead of shared memory; 534 with one hand-over of P per step, one flag
+// instead of a step's edge tests and failure paths placed out of line; 523 with
+// page ids fetched ahead; 505 with barriers looked at ahead of their use and
+// predicated arrivals; 472 with O joined behind the first half of P, when the
+// products it waits for are long done. The second: 159 us up to the page ids, one
+// CTA per tile; 134 with tiles drawn by resident CTAs, V cleared by its loader
+// and results written through shared memory; 122 with word masks and a first
+// tile that needs no draw. Slower: two threads per row (16 softmax warps per SM,
+// by 10 %), and the first half of P taken against the running maximum before
+// the step's own is known, done again for a row that outgrew it (by 12 %).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -739,6 +744,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[60 + e]));
         const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        // a row that grew its max rescales its O (P(j) V(j) cannot start before
+        // this thread hands over P(j))
         const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
         if (rarely(__any_sync(0xffffffffu, grow))) {
           float alpha = 1.f;
@@ -766,8 +773,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           }
         }
         // The probabilities, their sum and their three BF16 parts, 32 keys at a
-        // time. The first half does not wait for the step's maximum: it uses
-        // the running one, and is done again for a row that outgrew it.
+        // time; into tensor memory once the last step's product has read its P.
         const bool p_free = phase_done(&sm.p_done, (steps - 1) & 1);
         const float2 c2 = make_float2(c, c);
         float2 acc[2];
@@ -804,8 +810,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           }
           store_half(0, hi, mid, lo);
         }
-        // after a segment O joins the sum (the next product, P(j) V(j), starts
-        // from zero once this thread hands over P(j))
+        // after a segment O joins the sum; the next product, P(j) V(j), starts
+        // from zero
         if (rarely(segment == kSegment)) {
           const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
           const float2 b2 = make_float2(beta, beta);
