@@ -31,7 +31,9 @@
 //  * O leaves tensor memory every kSegment steps and is added up in FP32 in
 //    registers: a tensor-core sum drops the bits below its accumulator's last
 //    one, always downwards, 12 times a step, which over a 4,096-token window
-//    came to 1.5e-5 of the output (1.1e-6 with segments).
+//    came to 1.5e-5 of the output. With segments of four steps it is 1.1e-6
+//    (472 us in the first case below), of two 6.4e-7 (483 us), of one 4.4e-7
+//    (506 us).
 //
 // What bounds it: the softmax warps, two per scheduler, and of their time less
 // the arithmetic (maximum, exponentials, sums, the split into three terms: 1,200
@@ -40,9 +42,9 @@
 // takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
 // cycles each); a tile's start and end cost it some 4,000 more. The products are
 // never waited for: every barrier of theirs is complete when it is first looked
-// at. Two 4,096-token chunks behind a 4,096-token window: 472 us (585 TFLOP/s of
+// at. Two 4,096-token chunks behind a 4,096-token window: 483 us (571 TFLOP/s of
 // score and value products counted once); eight prompts of up to 2,048 tokens
-// behind 512: 116 us; sixteen of 512 tokens behind 128: 45.6 us. What was measured
+// behind 512: 118 us; sixteen of 512 tokens behind 128: 45.9 us. What was measured
 // on the way, the first of these: 718 us as a plain port of the step loop; 696
 // with the products issued by a converged warp (one thread in a divergent branch
 // takes 55 cycles an issue for its operands); 654 with the split's subtractions
@@ -51,10 +53,11 @@
 // instead of a step's edge tests and failure paths placed out of line; 523 with
 // page ids fetched ahead; 505 with barriers looked at ahead of their use and
 // predicated arrivals; 472 with O joined behind the first half of P, when the
-// products it waits for are long done. The second: 159 us up to the page ids, one
-// CTA per tile; 134 with tiles drawn by resident CTAs, V cleared by its loader
-// and results written through shared memory; 122 with word masks and a first
-// tile that needs no draw. Slower: two threads per row (16 softmax warps per SM,
+// products it waits for are long done; 483 with segments of two steps instead of
+// four. The second: 159 us up to the page ids, one CTA per tile; 134 with tiles
+// drawn by resident CTAs, V cleared by its loader and results written through
+// shared memory; 122 with word masks and a first tile that needs no draw; 118 at
+// the end. Slower: two threads per row (16 softmax warps per SM,
 // by 10 %), and the first half of P taken against the running maximum before
 // the step's own is known, done again for a row that outgrew it (by 12 %).
 
@@ -97,7 +100,7 @@ constexpr uint32_t kPartCols = kHalfKeys / 2;        // ... of three parts, two 
 constexpr uint32_t kTmemO = kTmemP + 2 * 3 * kPartCols;
 static_assert(kTmemO + kDim <= kTmemCols, "S, P and O fit the CTA's tensor memory");
 constexpr float kRescaleLog2 = 8.f;                  // lazy max: p <= 2^8
-constexpr int kSegment = 4;                          // steps whose O stays in tensor memory
+constexpr int kSegment = 2;                          // steps whose O stays in tensor memory
 // Registers a thread, once the roles are taken: 128 at launch, shared by the
 // CTA's two warpgroups.
 constexpr int kSoftmaxRegs = 192;
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         }
         // after a segment O joins the sum; the next product, P(j) V(j), starts
         // from zero
-        if (rarely(segment == kSegment)) {
+        if (segment == kSegment) {
           const float beta = m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m_run);
           const float2 b2 = make_float2(beta, beta);
           #pragma unroll
