@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(256) mark_pages_kernel(const int32_t* src, con
 // One block per (pair, pool): 128 threads move the page's 16 KiB, 8 vectors
 // of 16 bytes each, all loads before the first store. Vector j of a page is
 // token (j / 8) % 16 of its KV head. kScan: the block reads the list itself;
-// else the counts are in marks. page_to (compaction): the pair's move.
+// else the counts are in marks. page_to (compaction): 1 + the pair that moves
+// its source, 0 for a pair that is skipped.
 template <bool kScan>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(
     const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
@@ -61,16 +62,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(
   if (kScan) {
     bool clash = false;
     for (int j = t; j < n; j += kCopyThreads)
-      clash |= src[j] == d || (j != i && dst[j] == d);
+      clash |= src[j] == d || (j != i && (dst[j] == d || (page_to && src[j] == s)));
     ok = !__syncthreads_or(clash) && ok;
   } else if (ok) {
     ok = marks[d] == 1ull && (!page_to || (marks[s] >> 32) == 1ull);
   }
+  // two pairs of one source are both skipped: they write the same
+  if (page_to && t == 0 && !(blockIdx.x & 1) && s >= 0 && s < num_pages)
+    page_to[s] = ok ? i + 1 : 0;
   if (!ok) {
     if (t == 0) set_error(err, PKV_DEV_ERR_PAGE);
     return;
   }
-  if (page_to && t == 0 && !(blockIdx.x & 1)) page_to[s] = d + 1;
   const uint4* from = pool + static_cast<size_t>(s) * kPageVecs;
   uint4* to = pool + static_cast<size_t>(d) * kPageVecs;
   // this thread's vectors are t + 128 j: the same token of KV head j
@@ -83,10 +86,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(
 }
 static_assert(kCopyThreads == kPage * 8, "a thread's vectors belong to one token");
 
-// Entries naming a moved page take its new id, 4 entries per thread.
-__global__ void __launch_bounds__(256) rewrite_tables_kernel(int32_t* tables, size_t entries,
-                                                             int num_pages,
-                                                             const int* __restrict__ page_to) {
+// Entries naming a moved page take its new id, 4 entries per thread. What
+// page_to holds for a page that no pair of this list names as its source is
+// left from earlier lists: the pair it points to has another source.
+__global__ void __launch_bounds__(256) rewrite_tables_kernel(
+    const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n_pairs,
+    int32_t* tables, size_t entries, int num_pages, const int* __restrict__ page_to) {
   const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= entries) return;
   const int n = static_cast<int>(min(entries - at, static_cast<size_t>(4)));
@@ -100,9 +105,9 @@ __global__ void __launch_bounds__(256) rewrite_tables_kernel(int32_t* tables, si
   }
   #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int to = id[e] >= 0 && id[e] < num_pages ? page_to[id[e]] : 0;
-    if (to) {
-      id[e] = to - 1;
+    const int pair = id[e] >= 0 && id[e] < num_pages ? page_to[id[e]] - 1 : -1;
+    if (pair >= 0 && pair < n_pairs && src[pair] == id[e]) {
+      id[e] = dst[pair];
       moved = true;
     }
   }
@@ -131,24 +136,24 @@ pkv_status launch_copies(pkv_pool_t pool, const int32_t* src, const int32_t* dst
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint4* kp = static_cast<uint4*>(k_pool);
   uint4* vp = static_cast<uint4*>(v_pool);
-  if (!compact && n <= kScanPairs) {
+  int* page_to = compact ? pool->page_to : nullptr;
+  if (n <= kScanPairs) {
     copy_pages_kernel<true><<<2 * n, kCopyThreads, 0, st>>>(src, dst, tokens, kp, vp, n,
-                                                            c.num_pages, nullptr, nullptr,
+                                                            c.num_pages, nullptr, page_to,
                                                             pool->err);
-    return pkv_check_launch();
+  } else {
+    const size_t scratch = static_cast<size_t>(c.num_pages) * sizeof(unsigned long long);
+    if (cudaMemsetAsync(pool->page_marks, 0, scratch, st) != cudaSuccess) return PKV_ERR_CUDA;
+    mark_pages_kernel<<<(n + 255) / 256, 256, 0, st>>>(src, dst, n, c.num_pages,
+                                                       pool->page_marks);
+    copy_pages_kernel<false><<<2 * n, kCopyThreads, 0, st>>>(
+        src, dst, tokens, kp, vp, n, c.num_pages, pool->page_marks, page_to, pool->err);
   }
-  const size_t scratch = static_cast<size_t>(c.num_pages) *
-                         (sizeof(unsigned long long) + (compact ? sizeof(int) : 0));
-  if (cudaMemsetAsync(pool->page_marks, 0, scratch, st) != cudaSuccess) return PKV_ERR_CUDA;
-  mark_pages_kernel<<<(n + 255) / 256, 256, 0, st>>>(src, dst, n, c.num_pages, pool->page_marks);
-  copy_pages_kernel<false><<<2 * n, kCopyThreads, 0, st>>>(
-      src, dst, tokens, kp, vp, n, c.num_pages, pool->page_marks,
-      compact ? pool->page_to : nullptr, pool->err);
   if (compact) {
     const size_t entries = static_cast<size_t>(c.num_layers) * c.max_batch *
                            (c.max_seq_len / kPage);
     rewrite_tables_kernel<<<static_cast<unsigned>((entries + 1023) / 1024), 256, 0, st>>>(
-        tables, entries, c.num_pages, pool->page_to);
+        src, dst, n, tables, entries, c.num_pages, page_to);
   }
   return pkv_check_launch();
 }

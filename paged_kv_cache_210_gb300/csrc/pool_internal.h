@@ -24,8 +24,9 @@ struct pkv_pool {
   int* seq_done;     // [max_batch]: layer completions per sequence (multi-layer launch)
   unsigned long long* page_marks;   // [num_pages] how often the call's pairs name a page:
                                     // low half as destination, high half as source
-  int* page_to;                     // [num_pages] 1 + where a page moves (0: it stays); follows
-                                    // page_marks in one allocation
+  int* page_to;                     // [num_pages] 1 + the pair that moves a page (0: none), of the
+                                    // last compaction that named it; follows page_marks in one
+                                    // allocation
   unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between
                                     // launches)
   int window_blocks_per_sm;         // resident blocks of the windowed decode's ticket shape

@@ -124,6 +124,42 @@ def test_compaction_skips_clashes():
     pool.close()
 
 
+@pytest.mark.parametrize("n", [5, 60, 256, 257, 400])
+def test_compactions_one_after_another(n):
+    """Random lists with sources and destinations named twice, ids out of range and
+    pages that are both, over one handle: what one list leaves behind does not
+    reach the next."""
+    pages = 900
+    kp, vp = _pools(pages, n)
+    rng = np.random.RandomState(n)
+    pool = pkv.pkv_pool_create(2, pages, 3, max_seq_len=512)
+    table = rng.randint(-1, pages, (2, 3, 32)).astype(np.int32)
+    t = _i32(table)
+    for _ in range(6):
+        ids = rng.permutation(pages)
+        src, dst = ids[:n].copy(), ids[n:2 * n].copy()
+        for _ in range(4):                     # several rules broken at once
+            a, b = rng.randint(0, n, 2)
+            rng.choice([lambda: src.__setitem__(a, src[b]), lambda: dst.__setitem__(a, dst[b]),
+                        lambda: dst.__setitem__(a, src[b]), lambda: src.__setitem__(a, -1),
+                        lambda: dst.__setitem__(a, pages)])()
+        ok = [0 <= s < pages and 0 <= d < pages and (src == s).sum() == 1
+              and (dst == d).sum() == 1 and not (src == d).any() for s, d in zip(src, dst)]
+        good_s, good_d = src[ok], dst[ok]
+        want = [kp.clone(), vp.clone()]
+        for w in want:
+            if len(good_s):
+                _bits(w)[torch.as_tensor(good_d).cuda()] = _bits(w)[torch.as_tensor(good_s).cuda()]
+        to = {int(s): int(d) for s, d in zip(good_s, good_d)}
+        table = np.vectorize(lambda p: to.get(int(p), int(p)))(table).astype(np.int32)
+        pkv.pkv_compact_pages(pool, _i32(src), _i32(dst), kp, vp, t)
+        st = pkv.pkv_get_error(pool)
+        assert st == (pkv.PKV_OK if all(ok) else pkv.PKV_ERR_OUT_OF_RANGE)
+        assert np.array_equal(t.cpu().numpy(), table)
+        assert torch.equal(_bits(kp), _bits(want[0])) and torch.equal(_bits(vp), _bits(want[1]))
+    pool.close()
+
+
 def test_captured_and_replayed_with_other_lists():
     """Replays take the lists' current content; nothing is left over from the last."""
     pages, n = 700, 300
