@@ -26,10 +26,12 @@ constexpr int kCopyThreads = 128;
 constexpr int kPageVecs = kHkv * kPage * kRowBytes / 16;     // 16-byte vectors of a page: 1024
 constexpr int kVecsPerThread = kPageVecs / kCopyThreads;     // 8
 
-// Lists of up to this many pairs are checked by every copy block for itself,
-// in one launch (256 pairs 3.4 us); longer ones are counted per page first, in
-// two launches more (257 pairs 5.4 us), since the checks grow with n^2.
-constexpr int kScanPairs = 256;
+// Lists of up to this many pairs are checked by every copy block for itself, in
+// one launch; longer ones are counted per page first, in two launches more (a
+// memset and the counts), since the checks grow with n^2. Partial copies, the
+// launches in a graph, checked and counted (us): 257 pairs 3.4 and 4.9, 800 6.3
+// and 7.1, 1,024 7.3 and 8.1, 1,500 10.3 and 9.0.
+constexpr int kScanPairs = 1024;
 
 // How often each page is named: destinations in the low half of a page's
 // count, sources in the high half.

@@ -26,7 +26,7 @@ def _bits(t):
     return t.view(torch.int16)
 
 
-@pytest.mark.parametrize("n", [1, 2, 31, 256, 257, 1000, 5000])
+@pytest.mark.parametrize("n", [1, 2, 31, 256, 257, 1000, 1024, 1025, 5000])
 @pytest.mark.parametrize("partial", [False, True])
 def test_copies(n, partial):
     pages = 2 * n + 7
@@ -51,7 +51,7 @@ def test_copies(n, partial):
     pool.close()
 
 
-@pytest.mark.parametrize("filler", [0, 300])
+@pytest.mark.parametrize("filler", [0, 300, 1200])
 def test_pairs_that_clash_or_leave_the_pool_are_skipped(filler):
     """The same outcome in the one-launch form and, with `filler` good pairs
     around, in the counted one."""
@@ -124,12 +124,12 @@ def test_compaction_skips_clashes():
     pool.close()
 
 
-@pytest.mark.parametrize("n", [5, 60, 256, 257, 400])
+@pytest.mark.parametrize("n", [5, 60, 256, 257, 400, 1024, 1025])
 def test_compactions_one_after_another(n):
     """Random lists with sources and destinations named twice, ids out of range and
     pages that are both, over one handle: what one list leaves behind does not
     reach the next."""
-    pages = 900
+    pages = max(900, 2 * n + 50)
     kp, vp = _pools(pages, n)
     rng = np.random.RandomState(n)
     pool = pkv.pkv_pool_create(2, pages, 3, max_seq_len=512)
@@ -160,9 +160,9 @@ def test_compactions_one_after_another(n):
     pool.close()
 
 
-def test_captured_and_replayed_with_other_lists():
+@pytest.mark.parametrize("pages,n", [(700, 300), (2300, 1100)])
+def test_captured_and_replayed_with_other_lists(pages, n):
     """Replays take the lists' current content; nothing is left over from the last."""
-    pages, n = 700, 300
     kp, vp = _pools(pages)
     want = [kp.clone(), vp.clone()]
     pool = pkv.pkv_pool_create(1, pages, 1, max_seq_len=256)
@@ -176,9 +176,9 @@ def test_captured_and_replayed_with_other_lists():
         ids = np.random.RandomState(seed).permutation(pages)
         src.copy_(_i32(ids[:n]))
         dst.copy_(_i32(ids[n:2 * n]))
-        table.copy_(_i32(ids[290:306]).view(1, 1, 16))
-        want_t = np.where(np.arange(290, 306) < n, ids[np.minimum(np.arange(590, 606), pages - 1)],
-                          ids[290:306])
+        at = np.arange(n - 10, n + 6)
+        table.copy_(_i32(ids[at]).view(1, 1, 16))
+        want_t = np.where(at < n, ids[at + n], ids[at])
         for w in want:
             _bits(w)[torch.as_tensor(ids[n:2 * n]).cuda()] = \
                 _bits(w)[torch.as_tensor(ids[:n]).cuda()]
