@@ -11,10 +11,12 @@
 // 64 keys (4 pages) by two loader warps, scores and values run on tcgen05 with
 // accumulators in tensor memory, and the softmax warps hold one row per
 // thread. What is different, and why:
-//  * the steps of a tile are those that hold a visible key: the sink steps and
-//    the window's steps. Pages in them without a visible token, or with an
-//    invalid id, are read as a page past the pool's end, which the copy
-//    engine fills with zeros, so every step moves the same bytes;
+//  * a tile's steps are its visible pages, the sinks' and then the window's, four
+//    at a time wherever they lie (steps aligned to 64 tokens, with one more for
+//    four sinks, took 4 % longer behind 512 and 3 % behind 4,096 tokens). What
+//    the last step lacks, and pages with an invalid id, are read as a page past
+//    the pool's end, which the copy engine fills with zeros, so every step
+//    moves the same bytes;
 //  * page ids come straight from the block table, eight steps at a time, so
 //    the context's length does not appear in shared memory;
 //  * a tile has 32 tokens (128 rows), two CTAs share an SM, and the CTAs of one
@@ -32,8 +34,8 @@
 //    registers: a tensor-core sum drops the bits below its accumulator's last
 //    one, always downwards, 12 times a step, which over a 4,096-token window
 //    came to 1.5e-5 of the output. With segments of four steps it is 1.1e-6
-//    (472 us in the first case below), of two 6.4e-7 (483 us), of one 4.4e-7
-//    (506 us).
+//    (472 us in the first case below, then), of two 6.4e-7 (483 us), of one
+//    4.4e-7 (506 us).
 //
 // What bounds it: the softmax warps, two per scheduler, and of their time less
 // the arithmetic (maximum, exponentials, sums, the split into three terms: 1,200
@@ -42,9 +44,9 @@
 // takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
 // cycles each); a tile's start and end cost it some 4,000 more. The products are
 // never waited for: every barrier of theirs is complete when it is first looked
-// at. Two 4,096-token chunks behind a 4,096-token window: 483 us (571 TFLOP/s of
+// at. Two 4,096-token chunks behind a 4,096-token window: 469 us (589 TFLOP/s of
 // score and value products counted once); eight prompts of up to 2,048 tokens
-// behind 512: 118 us; sixteen of 512 tokens behind 128: 45.9 us. What was measured
+// behind 512: 114 us; sixteen of 512 tokens behind 128: 44.1 us. What was measured
 // on the way, the first of these: 718 us as a plain port of the step loop; 696
 // with the products issued by a converged warp (one thread in a divergent branch
 // takes 55 cycles an issue for its operands); 654 with the split's subtractions
@@ -54,12 +56,13 @@
 // page ids fetched ahead; 505 with barriers looked at ahead of their use and
 // predicated arrivals; 472 with O joined behind the first half of P, when the
 // products it waits for are long done; 483 with segments of two steps instead of
-// four. The second: 159 us up to the page ids, one CTA per tile; 134 with tiles
-// drawn by resident CTAs, V cleared by its loader and results written through
-// shared memory; 122 with word masks and a first tile that needs no draw; 118 at
-// the end. Slower: two threads per row (16 softmax warps per SM,
-// by 10 %), and the first half of P taken against the running maximum before
-// the step's own is known, done again for a row that outgrew it (by 12 %).
+// four; 469 with steps of any four pages. The second: 159 us up to the page ids,
+// one CTA per tile; 134 with tiles drawn by resident CTAs, V cleared by its
+// loader and results written through shared memory; 122 with word masks and a
+// first tile that needs no draw; 114 at the end. Slower: two threads per row (16
+// softmax warps per SM, by 10 %), and the first half of P taken against the
+// running maximum before the step's own is known, done again for a row that
+// outgrew it (by 12 %).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -283,46 +286,50 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
 
 // What the tile (and each of its steps) sees of the sequence.
 struct TileView {
-  int p_first, p_last;   // positions of the tile's first and last token
-  int n_keys;            // p_last + 1
+  int p_first;           // position of the tile's first token
+  int n_keys;            // position of its last token + 1
   int lo;                // first key inside some row's window
-  int sink_steps;        // steps of sinks before the window's
-  int win_step;          // the window's first step
-  int n_steps;
   int sinks;
+  int sink_pages;        // pages of sinks before the window's
+  int win_page;          // the window's first page
+  int n_pages;
+  int n_steps;
   int plain_from, plain_to;   // steps whose keys every row sees
 
   __device__ TileView(int first, int count, int window, int sinks_) {
     p_first = first;
-    p_last = first + count - 1;
-    n_keys = p_last + 1;
-    lo = max(p_first - window + 1, 0);
+    n_keys = first + count;
+    lo = max(first - window + 1, 0);
     sinks = sinks_;
-    win_step = lo / kStepKeys;
-    sink_steps = min((sinks + kStepKeys - 1) / kStepKeys, win_step);
-    n_steps = sink_steps + (n_keys + kStepKeys - 1) / kStepKeys - win_step;
-    const int hidden = p_last - window;        // the last key outside some row's window
-    plain_from = sink_steps + (hidden < 0 ? 0 : hidden / kStepKeys + 1 - win_step);
-    plain_to = sink_steps + (p_first + 1) / kStepKeys - win_step;
+    win_page = lo / kPage;
+    sink_pages = min((sinks + kPage - 1) / kPage, win_page);
+    n_pages = sink_pages + (n_keys + kPage - 1) / kPage - win_page;
+    n_steps = (n_pages + kStepPages - 1) / kStepPages;
+    const int hidden = n_keys - 1 - window;    // the last key outside some row's window
+    const int whole_from = hidden < sinks ? 0 : sink_pages + hidden / kPage + 1 - win_page;
+    const int whole_to = sink_pages + (first + 1) / kPage - win_page;
+    plain_from = (whole_from + kStepPages - 1) / kStepPages;
+    plain_to = whole_to / kStepPages;
   }
-  __device__ int step(int j) const { return j < sink_steps ? j : j - sink_steps + win_step; }
-  // whether a step whose first key is key0 has keys that no row sees
-  __device__ bool has_dead(int key0) const {
-    return key0 + kStepKeys > n_keys || max(key0, sinks) < min(key0 + kStepKeys, lo);
-  }
-  // whether logical page lp holds a key that some row sees
-  __device__ bool wants(int lp) const {
-    return lp * kPage < n_keys && ((lp + 1) * kPage > lo || lp * kPage < sinks);
+  // logical page i of the tile; past the last one (i >= n_pages) it has no key
+  __device__ int page(int i) const { return i < sink_pages ? i : i - sink_pages + win_page; }
+  // whether step j has keys that no row sees: past the last key, past the
+  // sinks, or before the window
+  __device__ bool has_dead(int j) const {
+    return (j == n_steps - 1 && (n_pages % kStepPages != 0 || n_keys % kPage != 0)) ||
+           (sinks < sink_pages * kPage && j == (sink_pages - 1) / kStepPages) ||
+           (max(win_page * kPage, sinks) < lo && j == sink_pages / kStepPages);
   }
 };
 
 // V rows that no row of the tile sees (past its last key, or between the sinks
 // and the window) set to zero, so that p = 0 times them stays 0. By one warp.
-__device__ __forceinline__ void zero_rows(uint8_t* stage, int key0, const TileView& view,
+__device__ __forceinline__ void zero_rows(uint8_t* stage, int j, const TileView& view,
                                           int lane) {
   #pragma unroll 4
   for (int idx = lane; idx < kStepKeys * 8; idx += 32) {
-    const int key = key0 + (idx >> 3);
+    const int row = idx >> 3;
+    const int key = view.page(j * kStepPages + row / kPage) * kPage + row % kPage;
     if (key >= view.n_keys || (key >= view.sinks && key < view.lo))
       *reinterpret_cast<uint4*>(stage + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
     if (warp < kScoreWarp) {
       // ---------------------------------------------------------- copy engine
       // Lanes 0..3 copy a step's 4 pages in one instruction once lane 0 saw
-      // the stage free. A page that does not count is copied from past the
+      // the stage free. A page that is not there is copied from past the
       // pool's end: zeros.
       // lane 4 s + e holds the e-th page of the s-th of 8 steps; the next 8
       // steps' are fetched while these are in use
@@ -417,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         const int32_t* trow = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
         auto page_of = [&](int j, int e) {      // the e-th page of step j, past the end if none
           int id = prm.num_pages;
-          if (j < view.n_steps) {
-            const int lp = view.step(j) * kStepPages + e;
-            if (view.wants(lp)) id = __ldg(trow + lp);
+          const int i = j * kStepPages + e;
+          if (i < view.n_pages) {
+            id = __ldg(trow + view.page(i));
             if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
           }
           return id;
@@ -432,8 +439,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
             ids_next = page_of(j + 8 + lane / kStepPages, lane % kStepPages);
           }
           const int page = __shfl_sync(0xffffffffu, ids, (j & 7) * kStepPages + lane % kStepPages);
-          const int key0 = view.step(j) * kStepKeys;
-          const bool edge = is_v && view.has_dead(key0);
+          const bool edge = is_v && view.has_dead(j);
           unsigned long long* landed = edge ? &sm.bar_edge : &full[at.stage];
           uint8_t* to = ring + at.stage * kStepBytes;
           bool good = true;
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           if (edge) {
             if (!__all_sync(0xffffffffu, mbar_wait(&sm.bar_edge, edges & 1))) return false;
             ++edges;
-            zero_rows(to, key0, view, lane);
+            zero_rows(to, j, view, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[at.stage]);
           }
@@ -539,10 +545,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
           ++q_loads;
           // invalid ids among the pages that count
           bool bad = false;
-          for (int i = lane; i < view.n_steps * kStepPages; i += 32) {
-            const int lp = view.step(i / kStepPages) * kStepPages + i % kStepPages;
-            if (!view.wants(lp)) continue;
-            const int id = __ldg(trow + lp);
+          for (int i = lane; i < view.n_pages; i += 32) {
+            const int id = __ldg(trow + view.page(i));
             bad |= id < 0 || id >= prm.num_pages;
           }
           work.bad_page = __any_sync(0xffffffffu, bad);
@@ -705,32 +709,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         const bool plain =
             static_cast<unsigned>(j - plain_from) < static_cast<unsigned>(plain_count);
         if (rarely(!plain)) {
-          const int key0 = view.step(j) * kStepKeys;
-          // bit i of seen[w]: key 32 w + i of the step is visible (one word test
-          // and one select per key: the code of an edge step is fetched anew
-          // each time, and a compare per condition and key made it 1,600
-          // cycles)
-          uint32_t seen[2];
+          // bit i of seen[w]: key 32 w + i of the step is visible (16 bits a
+          // page; one word test and one select per key: the code of an edge step
+          // is fetched anew each time, and a compare per condition and key made
+          // it 1,600 cycles)
+          uint32_t seen[2] = {0u, 0u};
           #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int base = key0 + 32 * w;
-            seen[w] = low_bits32(pos + 1 - base) &
-                      (low_bits32(view.sinks - base) | ~low_bits32(pos - prm.window + 1 - base));
-          }
-          if (any_bad_page) {
-            for (int e = 0; e < kStepPages; ++e) {
-              const int lp = key0 / kPage + e;
-              const int id = view.wants(lp) ? __ldg(prm.table + static_cast<size_t>(work.b) *
-                                                                    prm.table_stride + lp)
-                                            : -1;
-              if (id < 0 || id >= prm.num_pages) {
-                if (e < 2) {
-                  seen[0] &= ~(0xffffu << (16 * e));
-                } else {
-                  seen[1] &= ~(0xffffu << (16 * (e - 2)));
-                }
-              }
+          for (int e = 0; e < kStepPages; ++e) {
+            const int base = view.page(j * kStepPages + e) * kPage;
+            uint32_t bits =
+                low_bits32(pos + 1 - base) &
+                (low_bits32(view.sinks - base) | ~low_bits32(pos - prm.window + 1 - base));
+            if (any_bad_page && j * kStepPages + e < view.n_pages) {
+              const int id = __ldg(prm.table + static_cast<size_t>(work.b) * prm.table_stride +
+                                   base / kPage);
+              if (id < 0 || id >= prm.num_pages) bits = 0u;
             }
+            seen[e / 2] |= (bits & 0xffffu) << (16 * (e % 2));
           }
           #pragma unroll
           for (int i = 0; i < kStepKeys; ++i)
