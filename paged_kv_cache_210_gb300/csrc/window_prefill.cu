@@ -44,9 +44,9 @@
 // takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
 // cycles each); a tile's start and end cost it some 4,000 more. The products are
 // never waited for: every barrier of theirs is complete when it is first looked
-// at. Two 4,096-token chunks behind a 4,096-token window: 469 us (589 TFLOP/s of
+// at. Two 4,096-token chunks behind a 4,096-token window: 465 us (593 TFLOP/s of
 // score and value products counted once); eight prompts of up to 2,048 tokens
-// behind 512: 114 us; sixteen of 512 tokens behind 128: 44.1 us. What was measured
+// behind 512: 112 us; sixteen of 512 tokens behind 128: 43.3 us. What was measured
 // on the way, the first of these: 718 us as a plain port of the step loop; 696
 // with the products issued by a converged warp (one thread in a divergent branch
 // takes 55 cycles an issue for its operands); 654 with the split's subtractions
@@ -56,10 +56,11 @@
 // page ids fetched ahead; 505 with barriers looked at ahead of their use and
 // predicated arrivals; 472 with O joined behind the first half of P, when the
 // products it waits for are long done; 483 with segments of two steps instead of
-// four; 469 with steps of any four pages. The second: 159 us up to the page ids,
-// one CTA per tile; 134 with tiles drawn by resident CTAs, V cleared by its
-// loader and results written through shared memory; 122 with word masks and a
-// first tile that needs no draw; 114 at the end. Slower: two threads per row (16
+// four; 469 with steps of any four pages; 465 with the next tile looked up under
+// the last product. The second: 159 us up to the page ids, one CTA per tile; 134
+// with tiles drawn by resident CTAs, V cleared by its loader and results written
+// through shared memory; 122 with word masks and a first tile that needs no
+// draw; 112 at the end. Slower: two threads per row (16
 // softmax warps per SM, by 10 %), and the first half of P taken against the
 // running maximum before the step's own is known, done again for a row that
 // outgrew it (by 12 %).
@@ -678,10 +679,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
     bool ok = true;
     uint32_t steps = 0;                                 // of all tiles so far
-    for (int n = 0; ok; ++n) {
-      TileWork work;
-      ok = next_work(n, work);
-      if (!ok || work.count == 0) break;
+    TileWork work;
+    ok = next_work(0, work);
+    for (int n = 1; ok && work.count > 0; ++n) {
       const TileView view(work.p_first, work.count, prm.window, prm.sinks);
       const int n_steps = view.n_steps;
       const bool any_bad_page = work.bad_page != 0;
@@ -840,7 +840,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
         __syncwarp();
         arrive_lane0(&sm.bar_p, lane);
       }
-      if (!ok || !wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
+      // the next tile is looked up while the last product runs
+      TileWork next;
+      if (!ok || !next_work(n, next) || !wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -878,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) window_prefill_kernel(
       }
       // O is in registers before the next tile's first P is handed over
       tc_fence_before();
+      work = next;
     }
     if (!ok) give_up();
   }
