@@ -60,10 +60,9 @@
 // the last product. The second: 159 us up to the page ids, one CTA per tile; 134
 // with tiles drawn by resident CTAs, V cleared by its loader and results written
 // through shared memory; 122 with word masks and a first tile that needs no
-// draw; 112 at the end. Slower: two threads per row (16
-// softmax warps per SM, by 10 %), and the first half of P taken against the
-// running maximum before the step's own is known, done again for a row that
-// outgrew it (by 12 %).
+// draw; 112 at the end. Slower: two threads per row (16 softmax warps per SM, by
+// 10 %), and the first half of P taken against the running maximum before the
+// step's own is known, done again for a row that outgrew it (by 12 %).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
