@@ -731,10 +731,11 @@ def pkv_sched_fork(sched: Scheduler, request_id, length, max_new_tokens):
     layers = sched.config.num_layers
     src, dst = np.empty(layers, np.intc), np.empty(layers, np.intc)
     rid, count, tokens = ctypes.c_int(-1), ctypes.c_int(), ctypes.c_int()
-    _check(sched._lib.pkv_sched_fork(sched.handle, int(request_id), int(length),
-                                     int(max_new_tokens), ctypes.byref(rid), src.ctypes.data,
-                                     dst.ctypes.data, layers, ctypes.byref(count),
-                                     ctypes.byref(tokens)), "pkv_sched_fork")
+    _check(sched._lib.pkv_sched_fork(sched.handle, _int(int(request_id)), _int(int(length)),
+                                     _int(int(max_new_tokens)), ctypes.byref(rid),
+                                     src.ctypes.data, dst.ctypes.data, layers,
+                                     ctypes.byref(count), ctypes.byref(tokens)),
+           "pkv_sched_fork")
     n = count.value
     return rid.value, src[:n], dst[:n], np.full(n, tokens.value, np.intc)
 
@@ -743,8 +744,9 @@ def pkv_sched_release(sched: Scheduler, request_id, first_visible, sinks=0) -> i
     """Gives back the request's pages all of whose positions lie in
     [sinks, first_visible); returns how many (over all layers)."""
     count = ctypes.c_int()
-    _check(sched._lib.pkv_sched_release(sched.handle, int(request_id), int(first_visible),
-                                        int(sinks), ctypes.byref(count)), "pkv_sched_release")
+    _check(sched._lib.pkv_sched_release(sched.handle, _int(int(request_id)),
+                                        _int(int(first_visible)), _length(int(sinks)),
+                                        ctypes.byref(count)), "pkv_sched_release")
     return count.value
 
 
@@ -754,7 +756,7 @@ def pkv_sched_compact(sched: Scheduler, max_moves=None):
     pkv_copy_pages before tables of pkv_sched_block_tables are used."""
     import numpy as np
     cap = sched.config.num_pages if max_moves is None else int(max_moves)
-    cap = min(cap, sched.config.num_pages)
+    cap = _int(min(cap, sched.config.num_pages))
     src, dst = np.empty(max(cap, 1), np.intc), np.empty(max(cap, 1), np.intc)
     count = ctypes.c_int()
     _check(sched._lib.pkv_sched_compact(sched.handle, src.ctypes.data, dst.ctypes.data, cap,

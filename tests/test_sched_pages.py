@@ -208,3 +208,25 @@ def test_random_operations_keep_owners_and_credits(lib):
                 pkv.pkv_sched_finish(s, i)
                 del model[i]
         check()
+
+
+def test_values_beyond_a_c_int(lib):
+    """A sink count beyond an int keeps every token, as attention reads it; ids,
+    lengths and counts beyond one are refused, not wrapped."""
+    s = _sched(lib, 64)
+    a = _start(s, 150, 20)
+    t, before = _table(s, a), pkv.pkv_sched_get_stats(s)
+    big = 2 ** 32      # wraps to small C ints: 2^32 + 5 must not become 5
+    for sinks in (2 ** 31 - 1, 2 ** 31, big, big + 20, 1 << 40):
+        assert pkv.pkv_sched_release(s, a, 128, sinks) == 0
+    for args in ((a, big + 128, 0), (a, 128 - big, 0), (a + big, 128, 0), (a - big, 128, 0),
+                 (a, 128, 3 - big), (a, 2 ** 31, 0)):
+        assert _status(lambda: pkv.pkv_sched_release(s, *args)) == pkv.PKV_ERR_INVALID_ARG
+    for args in ((a, big + 144, 5), (a, 144 - big, 5), (a + big, 144, 5), (a, 144, big + 5),
+                 (a, 144, 5 - big)):
+        assert _status(lambda: pkv.pkv_sched_fork(s, *args)) == pkv.PKV_ERR_INVALID_ARG
+    for moves in (-1, -big, 5 - big):
+        assert _status(lambda: pkv.pkv_sched_compact(s, max_moves=moves)) == \
+            pkv.PKV_ERR_INVALID_ARG
+    assert [len(x) for x in pkv.pkv_sched_compact(s, max_moves=1 << 40)] == [0, 0]
+    assert (_table(s, a) == t).all() and pkv.pkv_sched_get_stats(s) == before
