@@ -485,6 +485,8 @@ class AxesRope:
         for name, t in (("rope_cos", cos), ("rope_sin", sin)):
             if t.dim() != 2 or t.shape[1] != pairs or t.shape[0] < 1 or t.shape != cos.shape:
                 raise ValueError(f"{name}: expected [rows][{pairs}]")
+        if sin.device != cos.device:
+            raise ValueError(f"rope_sin: expected a tensor on {cos.device}, got {sin.device}")
         self.tables = (cos, sin)
         self.num_axes = max(axes) + 1
         self.device = cos.get_device()

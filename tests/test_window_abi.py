@@ -93,3 +93,11 @@ def test_page_lists():
     for kw in (dict(src=i.long(), dst=i), dict(src=i, dst=i[:2]), dict(src=i, dst=i, tokens=i[:1])):
         with pytest.raises(ValueError):
             pkv.pkv_copy_pages(POOL, k_pool=p, v_pool=p, **kw)
+
+
+def test_rotary_tables_lie_on_one_device():
+    """The kernels read both tables: one elsewhere is refused, not passed on."""
+    here, elsewhere = torch.zeros(10, 32), torch.zeros(10, 32, device="meta")
+    for cos, sin in ((here, elsewhere), (elsewhere, here)):
+        with pytest.raises(ValueError, match="rope_sin"):
+            pkv.pkv_axes_rope(cos, sin, [0] * 32)
