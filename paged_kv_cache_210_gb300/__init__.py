@@ -235,15 +235,24 @@ class Pool:
             pass
 
 
+def _current_device():
+    """The current CUDA device's index, or None where torch does not have one."""
+    try:
+        import torch
+        return torch.cuda.current_device()
+    except (ImportError, AssertionError, RuntimeError):   # no torch, no CUDA in it, no device
+        return None
+
+
 def pkv_pool_create(num_layers, num_pages, max_batch, max_seq_len=MAX_SEQ_LEN, max_splits=0,
                     flags=0, lib=None) -> Pool:
     lib = lib or load()
     cfg = PoolConfig(num_layers, num_pages, PAGE_SIZE, NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM,
                      max_seq_len, max_batch, max_splits, flags)
+    device = _current_device()      # before the handle exists: nothing after it may fail
     handle = ctypes.c_void_p()
     _check(lib.pkv_pool_create(ctypes.byref(cfg), ctypes.byref(handle)), "pkv_pool_create")
-    import torch
-    return Pool(handle.value, cfg, lib, torch.cuda.current_device())
+    return Pool(handle.value, cfg, lib, device)
 
 
 def pkv_pool_destroy(pool: Pool):

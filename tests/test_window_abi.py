@@ -2,6 +2,7 @@
 before any CUDA call, the long-context flag's limits, and argument marshalling."""
 
 import ctypes
+import sys
 
 import pytest
 import torch
@@ -101,3 +102,40 @@ def test_rotary_tables_lie_on_one_device():
     for cos, sin in ((here, elsewhere), (elsewhere, here)):
         with pytest.raises(ValueError, match="rope_sin"):
             pkv.pkv_axes_rope(cos, sin, [0] * 32)
+
+
+class _Creates:
+    """Stands in for the CUDA library: hands out handle 7 and takes it back."""
+
+    def __init__(self):
+        self.destroyed = []
+
+    def pkv_pool_create(self, config, out):
+        out._obj.value = 7
+        return pkv.PKV_OK
+
+    def pkv_pool_destroy(self, handle):
+        self.destroyed.append(handle)
+        return pkv.PKV_OK
+
+
+def _no_torch(monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)       # an import raises
+
+
+def _no_device(monkeypatch):
+    def current_device():
+        raise RuntimeError("no CUDA device")
+    monkeypatch.setattr(torch.cuda, "current_device", current_device)
+
+
+@pytest.mark.parametrize("missing", [_no_torch, _no_device])
+def test_a_handle_needs_no_torch(monkeypatch, missing):
+    """Raw addresses do without torch: the handle is there, and owned, where torch
+    or its CUDA device is not."""
+    missing(monkeypatch)
+    lib = _Creates()
+    pool = pkv.pkv_pool_create(1, 16, 1, lib=lib)
+    assert pool.handle == 7 and pool.device is None
+    pool.close()
+    assert lib.destroyed == [7]
