@@ -120,14 +120,28 @@ pkv_status pkv_sched_finish(pkv_sched_t sched, int request_id);
  * do not cover it now. Shared pages are freed when their last owner gives
  * them back. In the counters a fork is a submission that was admitted.
  *
+ * Whole pages that the parent gave back (pkv_sched_release) are missing from
+ * the child too: their entries are -1, and attention that would see them flags
+ * and skips their tokens. pkv_sched_held tells what a child has.
+ *
  * *count (0, or num_layers when length is not a whole number of pages) page
  * copies are due before the child is used: the first *tokens tokens of src[i] to
  * dst[i] (pkv_copy_pages of pkv_pages.h). INVALID_ARG if capacity is below
- * num_layers, the request is not active, length is out of range or the child's
- * submission would be invalid. */
+ * num_layers, the request is not active, length is out of range, the partial
+ * page that the child would copy was given back or the child's submission would
+ * be invalid. */
 pkv_status pkv_sched_fork(pkv_sched_t sched, int request_id, int length, int max_new_tokens,
                           int* child_id, int32_t* src, int32_t* dst, int capacity, int* count,
                           int* tokens);
+
+/* What an active request still has of the tokens it reached (pkv_sched_extend,
+ * or its fork's length): the pages of positions [0, *head) and of [*tail, reach)
+ * are there in every layer, *head being the first missing position (reach if
+ * none is missing) and *tail the one after the last missing (0 if none is).
+ * Attention (pkv_window.h) of the next token finds every token it sees if *tail
+ * is 0, or if its window starts at *tail or later and its sinks do not go beyond
+ * *head. INVALID_ARG if the request is not active. */
+pkv_status pkv_sched_held(pkv_sched_t sched, int request_id, int* head, int* tail);
 
 /* Gives back, in every layer, the request's pages all of whose positions lie in
  * [sinks, first_visible): what attention behind a window starting at

@@ -36,8 +36,8 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_append", "pkv_decode_att
             "pkv_prefill_attention", "pkv_prefill", "pkv_plan_decode",
             "pkv_pool_device_figures", "pkv_window_attention", "pkv_window_append_attend",
             "pkv_window_prefill_attention", "pkv_prefill_fill_axes", "pkv_copy_pages",
-            "pkv_compact_pages", "pkv_sched_fork", "pkv_sched_release", "pkv_sched_compact",
-            "pkv_status_string")
+            "pkv_compact_pages", "pkv_sched_fork", "pkv_sched_held", "pkv_sched_release",
+            "pkv_sched_compact", "pkv_status_string")
 
 
 class PkvError(RuntimeError):
@@ -142,6 +142,7 @@ def load(path: str = None):
     lib.pkv_copy_pages.argtypes = [P, P, P, P, P, P, i, P]
     lib.pkv_compact_pages.argtypes = [P, P, P, P, P, P, i, P]
     lib.pkv_sched_fork.argtypes = [P, i, i, i, SP, P, P, i, SP, SP]
+    lib.pkv_sched_held.argtypes = [P, i, SP, SP]
     lib.pkv_sched_release.argtypes = [P, i, i, i, SP]
     lib.pkv_sched_compact.argtypes = [P, P, P, i, SP]
     lib.pkv_status_string.argtypes = [i]
@@ -737,7 +738,8 @@ def pkv_sched_fork(sched: Scheduler, request_id, length, max_new_tokens):
     dst, tokens): the page copies (one per layer, or none) that the child needs
     before it is used, the first `tokens` tokens of each; int32 arrays for
     pkv_copy_pages. PkvError(PKV_ERR_REJECTED) when the free credits do not
-    cover the child."""
+    cover the child. Pages that the parent gave back are missing from the child
+    as well: pkv_sched_held tells which tokens it has."""
     import numpy as np
     layers = sched.config.num_layers
     src, dst = np.empty(layers, np.intc), np.empty(layers, np.intc)
@@ -749,6 +751,17 @@ def pkv_sched_fork(sched: Scheduler, request_id, length, max_new_tokens):
            "pkv_sched_fork")
     n = count.value
     return rid.value, src[:n], dst[:n], np.full(n, tokens.value, np.intc)
+
+
+def pkv_sched_held(sched: Scheduler, request_id):
+    """(head, tail): the pages of the request's first `head` positions and of those
+    from `tail` on are there in every layer (a whole request: head is its length,
+    tail 0). Attention behind a window that starts at or after `tail`, with at
+    most `head` sinks, finds every token."""
+    head, tail = ctypes.c_int(), ctypes.c_int()
+    _check(sched._lib.pkv_sched_held(sched.handle, _int(int(request_id)), ctypes.byref(head),
+                                     ctypes.byref(tail)), "pkv_sched_held")
+    return head.value, tail.value
 
 
 def pkv_sched_release(sched: Scheduler, request_id, first_visible, sinks=0) -> int:

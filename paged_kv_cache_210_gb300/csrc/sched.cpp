@@ -292,6 +292,26 @@ pkv_status pkv_sched_fork(pkv_sched_t s, int request_id, int length, int max_new
   return PKV_OK;
 }
 
+pkv_status pkv_sched_held(pkv_sched_t s, int request_id, int* head, int* tail) {
+  if (!s || !head || !tail) return PKV_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> g(s->lock);
+  auto it = s->requests.find(request_id);
+  if (it == s->requests.end() || !it->second.active) return PKV_ERR_INVALID_ARG;
+  const Request& r = it->second;
+  const int page = s->cfg.page_size;
+  *head = r.reach;
+  *tail = 0;
+  for (int layer = 0; layer < s->cfg.num_layers; ++layer) {
+    const int32_t* row = r.pages.data() + static_cast<size_t>(layer) * s->max_pages_per_seq;
+    for (int i = 0; i < (r.reach + page - 1) / page; ++i) {
+      if (row[i] >= 0) continue;
+      *head = std::min(*head, i * page);
+      *tail = std::max(*tail, std::min((i + 1) * page, r.reach));
+    }
+  }
+  return PKV_OK;
+}
+
 pkv_status pkv_sched_release(pkv_sched_t s, int request_id, int first_visible, int sinks,
                              int* released) {
   if (!s || first_visible < 0 || sinks < 0) return PKV_ERR_INVALID_ARG;

@@ -230,3 +230,50 @@ def test_values_beyond_a_c_int(lib):
             pkv.PKV_ERR_INVALID_ARG
     assert [len(x) for x in pkv.pkv_sched_compact(s, max_moves=1 << 40)] == [0, 0]
     assert (_table(s, a) == t).all() and pkv.pkv_sched_get_stats(s) == before
+
+
+def test_what_a_request_still_holds(lib):
+    """A fork inherits its parent's holes; what it lacks can be asked for before the
+    first step behind a window."""
+    s = _sched(lib, 128)
+    a = _start(s, 200, 5)
+    assert pkv.pkv_sched_held(s, a) == (200, 0)
+    whole = pkv.pkv_sched_fork(s, a, 37, 5)[0]
+    assert pkv.pkv_sched_held(s, whole) == (37, 0)
+    pkv.pkv_sched_release(s, a, 160, 20)              # pages 2 .. 9 go
+    assert pkv.pkv_sched_held(s, a) == (32, 160)
+    assert pkv.pkv_sched_held(s, pkv.pkv_sched_fork(s, a, 170, 5)[0]) == (32, 160)
+    assert pkv.pkv_sched_held(s, pkv.pkv_sched_fork(s, a, 96, 5)[0]) == (32, 96)
+    assert pkv.pkv_sched_held(s, pkv.pkv_sched_fork(s, a, 32, 5)[0]) == (32, 0)
+    pkv.pkv_sched_release(s, a, 160, 0)
+    none = pkv.pkv_sched_fork(s, a, 160, 5)[0]        # nothing of it is there
+    assert pkv.pkv_sched_held(s, none) == (0, 160) and (_table(s, none) == -1).all()
+    pkv.pkv_sched_extend(s, none, 164)
+    assert pkv.pkv_sched_held(s, none) == (0, 160)
+    assert pkv.pkv_sched_held(s, whole) == (37, 0)    # a release by the parent is not its
+    b = pkv.pkv_sched_submit(s, 10, 5)
+    for i in (b, b + 1, -1, 2 ** 32 + a):             # waiting, unknown, not wrapped
+        assert _status(lambda: pkv.pkv_sched_held(s, i)) == pkv.PKV_ERR_INVALID_ARG
+    assert pkv.pkv_sched_admit(s) == [b]
+    assert pkv.pkv_sched_held(s, b) == (0, 0)         # no position reached yet
+
+
+def test_held_positions_under_random_releases(lib):
+    """Against the block table, entry by entry."""
+    rng = np.random.RandomState(11)
+    s = _sched(lib, 4000, 3)
+    for _ in range(60):
+        n = rng.randint(1, 250)
+        a = _start(s, n, 5)
+        for _ in range(rng.randint(0, 4)):
+            pkv.pkv_sched_release(s, a, rng.randint(0, n + 1), rng.randint(0, 200))
+        if rng.rand() < 0.5:
+            length = rng.randint(1, n + 1)
+            try:
+                a, n = pkv.pkv_sched_fork(s, a, length, 5)[0], length
+            except pkv.PkvError:                      # its partial page is gone
+                pass
+        there = (_table(s, a) >= 0).all(0).repeat(16)[:n]
+        head, tail = pkv.pkv_sched_held(s, a)
+        assert there[:head].all() and (head == n or not there[head])
+        assert there[tail:].all() and (tail == 0 or not there[tail - 1])
