@@ -420,6 +420,110 @@ def test_prefill_launch_wider_than_the_chunks():
     _prefill([3, 70], [0, 0], 32, 4, max_chunk=2048, max_batch=4, num_layers=2, layer=1)
 
 
+# groups of 32 sequences: on both sides of one, two and three, with whole groups
+# empty, and equal, single and ragged numbers of tiles
+@pytest.mark.parametrize("chunks", [
+    [1] * 31, [40] * 32, [1] * 33, [0] * 70 + [100] + [0] * 29, [70] + [0] * 63 + [33],
+    [(37 * i * i) % 140 for i in range(75)], [200] + [3] * 64 + [0, 0, 161],
+    [32 * (i % 5) for i in range(100)]])
+@pytest.mark.parametrize("max_chunk", [None, 2048])
+def test_prefill_many_sequences(chunks, max_chunk):
+    starts = [(53 * i) % 300 for i in range(len(chunks))]
+    _prefill(chunks, starts, 60, 4, max_chunk=max_chunk, seed=len(chunks))
+
+
+def test_prefill_without_tokens_in_its_sequences():
+    """Rows that belong to no sequence stay as they were."""
+    c = W.Cache([5, 5])
+    kp, vp = c.pools(lambda b: np.ones(5, bool))
+    pool = _pool(c)
+    q = torch.randn(40, 32, 64, device="cuda").bfloat16()
+    out = torch.full((40, 32, 64), 7.5, device="cuda")
+    zeros = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, zeros, zeros[:2], out, 2048, 8)
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK and (out == 7.5).all()
+    pool.close()
+
+
+@pytest.mark.parametrize("where", [0, 31, 32, 69])
+def test_prefill_one_bad_sequence_among_many(where):
+    """It is flagged and skipped; the others' results keep their bits."""
+    chunks, starts = [50 + i % 20 for i in range(70)], [(11 * i) % 90 for i in range(70)]
+    lens = [s + n for s, n in zip(starts, chunks)]
+    c = W.Cache(lens)
+    kp, vp = c.pools(lambda b: np.ones(lens[b], bool), 0.0)
+    pool = _pool(c)
+    cu = np.concatenate([[0], np.cumsum(chunks)])
+    q = torch.randn(cu[-1], 32, 64, device="cuda", generator=c.gen).bfloat16()
+    start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def run(start_=start, cu_=cu_t):
+        out = torch.full((cu[-1], 32, 64), 7.5, device="cuda")
+        pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, cu_, start_, out, 100, 64,
+                                         sinks=4)
+        return out, pkv.pkv_get_error(pool)
+
+    good, st = run()
+    assert st == pkv.PKV_OK
+    mine = torch.zeros(cu[-1], dtype=torch.bool, device="cuda")
+    mine[cu[where]:cu[where + 1]] = True
+    for bad in (-1, 2040, 2 ** 31 - 1):
+        s = start.clone()
+        s[where] = bad
+        out, st = run(start_=s)
+        assert st == pkv.PKV_ERR_OUT_OF_RANGE and (out[mine] == 7.5).all()
+        assert torch.equal(out[~mine], good[~mine])
+    bad_cu = cu_t.clone()
+    bad_cu[where + 1] = 2 ** 31 - 1              # this sequence and the next one have no rows
+    skipped = mine.clone()
+    if where < 69:
+        skipped[cu[where + 1]:cu[where + 2]] = True
+    out, st = run(cu_=bad_cu)
+    assert st == pkv.PKV_ERR_OUT_OF_RANGE and (out[skipped] == 7.5).all()
+    assert torch.equal(out[~skipped], good[~skipped])
+    out, st = run()
+    assert st == pkv.PKV_OK and torch.equal(out, good)
+    pool.close()
+
+
+@pytest.mark.parametrize("batch,bound", [(1, 131072), (16, 32768)])
+def test_prefill_time_follows_the_chunks(batch, bound):
+    """Chunks of 32 tokens take the same time under a launch bound far above them:
+    what is drawn are the tiles there are, 8 a sequence. Were every tile below the
+    bound drawn, each of 304 resident CTAs would draw 108 or 430 in vain one after the
+    other, half a microsecond each at the least, on top of some 10."""
+    c = W.Cache([32] * batch, max_seq_len=131072)
+    kp, vp = c.pools(lambda b: np.ones(32, bool), 0.0)
+    pool = _pool(c)
+    n = 32 * batch
+    q = torch.randn(n, 32, 64, device="cuda").bfloat16()
+    out = torch.zeros(n, 32, 64, device="cuda")
+    cu = torch.arange(0, n + 1, 32, dtype=torch.int32, device="cuda")
+    start = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    times = {}
+    for chunk in (32, bound):
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, cu, start, out, chunk,
+                                                 64)
+        ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        times[chunk] = []
+        for _ in range(8):
+            ends[0].record()
+            graph.replay()
+            ends[1].record()
+            torch.cuda.synchronize()
+            times[chunk].append(ends[0].elapsed_time(ends[1]))
+        del graph
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    assert min(times[bound]) < 3 * min(times[32]), times
+    pool.close()
+
+
 def test_prefill_pages_past_four_gib():
     _prefill([100], [30], 64, 4, junk=float("nan"), base_page=280000)
 
