@@ -693,6 +693,10 @@ pkv_status pkv_prefill(pkv_pool_t pool, int layer, const void* q, const void* k,
                        void* k_pool, void* v_pool, const int32_t* block_tables,
                        const int32_t* cu_tokens, const int32_t* start_pos, float* out,
                        int batch, int total_tokens, int max_chunk_tokens, void* stream) {
+  // a handle that the attention refuses gets its answer before the fill writes
+  if (pool && !pkv_short_context(pool))
+    return launch_attention(pool, layer, q, k_pool, v_pool, block_tables, cu_tokens, start_pos,
+                            out, batch, total_tokens, max_chunk_tokens, stream);
   pkv_status st = launch_fill(pool, layer, k, v, k_pool, v_pool, block_tables, cu_tokens,
                               start_pos, batch, total_tokens, max_chunk_tokens, stream);
   if (st != PKV_OK) return st;
