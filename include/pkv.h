@@ -102,7 +102,13 @@ typedef struct {
  * of two or more layers, consecutive decode steps meet it: the step before
  * wrote the rows of the same layer one launch per layer earlier. A
  * one-layer model's consecutive fused steps do not: put another kernel
- * between them or leave this flag off.) Off by default. */
+ * between them or leave this flag off.) The handle's own calls that write
+ * pages or tables between steps, pkv_copy_pages, pkv_compact_pages and
+ * pkv_prefill_fill_axes, may come immediately before a decode launch: the first
+ * one called after them waits for the kernel before it to complete. (That
+ * goes by the order of the calls: where a graph's replay puts a decode launch
+ * right behind such a call captured elsewhere, the contract is the caller's.)
+ * Off by default. */
 #define PKV_FLAG_PDL 1
 
 /* A handle whose max_seq_len may be any multiple of 16 up to

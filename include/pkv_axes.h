@@ -59,7 +59,9 @@ typedef struct {
  * row is left as it was) and flagged; errors otherwise as pkv_prefill_fill,
  * INVALID_ARG also for a null rope, null or misaligned tables or positions,
  * rows < 1, num_axes outside [1, 4], a pair's axis outside [0, num_axes) or
- * position_stride < total_tokens. Takes long-context handles. */
+ * position_stride < total_tokens. With PKV_FLAG_PDL it may come right before a
+ * decode launch of the handle (the limits are those of pkv.h). Takes
+ * long-context handles. */
 pkv_status pkv_prefill_fill_axes(pkv_pool_t pool, int layer, const void* q, const void* k,
                                  const void* v, void* q_out, void* k_pool, void* v_pool,
                                  const int32_t* block_tables, const int32_t* cu_tokens,

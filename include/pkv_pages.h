@@ -14,8 +14,9 @@
  * Calls are asynchronous on `stream`. Host-detectable errors (null or
  * misaligned pointers, n outside [0, num_pages], another current device)
  * return INVALID_ARG and launch nothing; n == 0 is a no-op. Both calls use
- * scratch of the handle, so they share its rule: one stream per handle. Takes
- * long-context handles.
+ * scratch of the handle, so they share its rule: one stream per handle. With
+ * PKV_FLAG_PDL either may come right before a decode launch of the handle (the
+ * limits are those of pkv.h). Takes long-context handles.
  */
 #ifndef PKV_PAGES_H
 #define PKV_PAGES_H

@@ -158,7 +158,8 @@ pkv_status pkv_sched_release(pkv_sched_t sched, int request_id, int first_visibl
  * and dst and their number to *count. The tables of pkv_sched_block_tables name
  * the new ids from now on, so the moves must be carried out on the device
  * (pkv_compact_pages of pkv_pages.h on the tables in use, or pkv_copy_pages
- * before new tables are used) before any other use of the pool. */
+ * before new tables are used) before any other use of the pool. Copies that an
+ * earlier fork asked for name the old ids: issue them first. */
 pkv_status pkv_sched_compact(pkv_sched_t sched, int32_t* src, int32_t* dst, int capacity,
                              int* count);
 

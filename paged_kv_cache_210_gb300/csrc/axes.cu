@@ -170,6 +170,7 @@ extern "C" pkv_status pkv_prefill_fill_axes(pkv_pool_t pool, int layer, const vo
   prm.max_seq_len = c.max_seq_len;
   prm.max_chunk = max_chunk_tokens;
   prm.total_tokens = total_tokens;
+  pool->pages_written = true;
   fill_axes_kernel<<<dim3((max_chunk_tokens + kFillWarps - 1) / kFillWarps, batch),
                      kFillWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(prm);
   return pkv_check_launch();

@@ -139,6 +139,7 @@ pkv_status launch_copies(pkv_pool_t pool, const int32_t* src, const int32_t* dst
   uint4* kp = static_cast<uint4*>(k_pool);
   uint4* vp = static_cast<uint4*>(v_pool);
   int* page_to = compact ? pool->page_to : nullptr;
+  pool->pages_written = true;
   if (n <= kScanPairs) {
     copy_pages_kernel<true><<<2 * n, kCopyThreads, 0, st>>>(src, dst, tokens, kp, vp, n,
                                                             c.num_pages, nullptr, page_to,

@@ -771,6 +771,10 @@ pkv_status launch_decode(pkv_pool_t pool, int layer, const void* q, const void* 
   cfg.blockDim = dim3(block_threads(shape), 1, 1);
   cfg.dynamicSmemBytes = smem_bytes(shape);
   cfg.stream = static_cast<cudaStream_t>(stream);
+  CUtensorMap tk, tv;
+  if (!pkv_pool_tensor_map(k_pool, c.num_pages, &tk) ||
+      !pkv_pool_tensor_map(v_pool, c.num_pages, &tv))
+    return PKV_ERR_CUDA;
   cudaLaunchAttribute attrs[2];
   int n_attrs = 0;
   if (cluster) {
@@ -780,17 +784,13 @@ pkv_status launch_decode(pkv_pool_t pool, int layer, const void* q, const void* 
     attrs[n_attrs].val.clusterDim.z = 1;
     ++n_attrs;
   }
-  if (c.flags & PKV_FLAG_PDL) {
+  if (pkv_starts_early(pool)) {
     attrs[n_attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[n_attrs].val.programmaticStreamSerializationAllowed = 1;
     ++n_attrs;
   }
   cfg.attrs = attrs;
   cfg.numAttrs = n_attrs;
-  CUtensorMap tk, tv;
-  if (!pkv_pool_tensor_map(k_pool, c.num_pages, &tk) ||
-      !pkv_pool_tensor_map(v_pool, c.num_pages, &tv))
-    return PKV_ERR_CUDA;
   cudaError_t e;
   if (rope) {
     e = shape == kNarrowShape ? cudaLaunchKernelEx(&cfg, narrow_kernel<kFused, true>, tk, tv, prm)

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pkv.h"
 
 struct pkv_pool {
@@ -31,6 +33,8 @@ struct pkv_pool {
                                     // launches)
   int window_blocks_per_sm;         // resident blocks of the windowed decode's ticket shape
   int window_cluster_blocks_per_sm; // ... and of its cluster shape
+  std::atomic<bool> pages_written{false};   // the handle's last page or fill call (pkv_pages.h,
+                                            // pkv_axes.h) has had no decode launch after it
   int layer_clusters[5];   // resident clusters of the multi-layer kernel, S = 1, 2, 4, 8, 16
 };
 
@@ -56,6 +60,13 @@ inline pkv_status pkv_check_launch() {
 // Whether the handle is in the range of the entry points limited to
 // 2,048-token contexts (their kernels hold a whole block-table row).
 inline bool pkv_short_context(const pkv_pool* pool) { return pool->cfg.max_seq_len <= 2048; }
+
+// Whether the next decode launch may start under the kernel before it
+// (PKV_FLAG_PDL): it then reads tables and pages ahead of that kernel's end, so
+// not if that may be the handle's own call that writes them.
+inline bool pkv_starts_early(pkv_pool* pool) {
+  return (pool->cfg.flags & PKV_FLAG_PDL) != 0 && !pool->pages_written.exchange(false);
+}
 
 // pkv.cu: a K or V pool of num_pages pages as the copy engine's 3-D tensor
 // map (dim, kv head x 16 + token, page), boxes of one (page, kv head) tile

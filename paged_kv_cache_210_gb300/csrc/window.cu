@@ -923,6 +923,10 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
   cfg.blockDim = dim3(kThreadsW, 1, 1);
   cfg.dynamicSmemBytes = cluster ? kClusterSmemBytes : kTicketSmemBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
+  CUtensorMap tk, tv;
+  if (!pkv_pool_tensor_map(k_pool, c.num_pages, &tk) ||
+      !pkv_pool_tensor_map(v_pool, c.num_pages, &tv))
+    return PKV_ERR_CUDA;
   cudaLaunchAttribute attrs[2];
   int n_attrs = 0;
   if (cluster) {
@@ -932,17 +936,13 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
     attrs[n_attrs].val.clusterDim.z = 1;
     ++n_attrs;
   }
-  if (c.flags & PKV_FLAG_PDL) {
+  if (pkv_starts_early(pool)) {
     attrs[n_attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[n_attrs].val.programmaticStreamSerializationAllowed = 1;
     ++n_attrs;
   }
   cfg.attrs = attrs;
   cfg.numAttrs = n_attrs;
-  CUtensorMap tk, tv;
-  if (!pkv_pool_tensor_map(k_pool, c.num_pages, &tk) ||
-      !pkv_pool_tensor_map(v_pool, c.num_pages, &tv))
-    return PKV_ERR_CUDA;
   const WindowKernel kernel = cluster ? window_kernel<true>(kFused, rope != nullptr)
                                       : window_kernel<false>(kFused, rope != nullptr);
   if (cudaLaunchKernelEx(&cfg, kernel, tk, tv, prm) != cudaSuccess) return PKV_ERR_CUDA;
