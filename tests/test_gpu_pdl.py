@@ -156,3 +156,76 @@ def test_handles_without_the_flag_have_plain_launches():
         x.unfused(stream=s)
     assert _edges(step) == [False] * 3
     x.pool.close()
+
+
+# (batch, splits): one cluster, units found by one warp and by a block, tickets
+@pytest.mark.parametrize("batch,num_splits", [(3, 0), (64, 0), (120, 0), (6, 33), (6, 5)])
+@pytest.mark.parametrize("rotated", [False, True])
+def test_the_same_bits_as_without_the_flag(batch, num_splits, rotated):
+    """Steps of two layers: append and attend, a launch whose rows are all padding, and
+    attention again over what was appended two launches before; called one by one and
+    replayed from a graph, lengths changing in between."""
+    lens = np.random.RandomState(batch).randint(1, 1500, batch).tolist()
+    results = []
+    for flags, captured in ((0, False), (pkv.PKV_FLAG_PDL, False), (pkv.PKV_FLAG_PDL, True)):
+        x = Batch(lens, flags, window=600)
+        rope = x.rope if rotated else None
+        kw = dict(rope=rope, num_splits=num_splits)
+
+        def step():
+            for layer in range(x.layers):
+                x.fused(layer, **kw)
+                x.unfused(layer, lens=x.none, **kw)
+                x.unfused(layer, **kw)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                step()
+        seen = []
+        for _ in range(5):
+            graph.replay() if captured else step()
+            torch.cuda.synchronize()
+            seen += [x.out.clone(), x.again.clone()]
+            x.n += 1
+            torch.cuda.synchronize()
+        assert pkv.pkv_get_error(x.pool) == pkv.PKV_OK
+        results.append((torch.stack(seen), x.kp.view(torch.int16), x.vp.view(torch.int16)))
+        if captured:
+            del graph
+        del step
+        x.pool.close()
+    assert not torch.isnan(results[0][0]).any() and (results[0][0] != 0).any(-1).all()
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("batch", [3, 64])
+def test_decode_right_after_a_compaction(batch):
+    """Pages move, the tables follow, and what the pages held before is overwritten: the
+    decode after them gives the bits it gave before them."""
+    lens = np.random.RandomState(batch).randint(40, 1500, batch).tolist()
+    x = Batch(lens, window=2048)
+    want = None
+    src = torch.from_numpy(x.table[0, :min(batch, 30), 0].copy()).cuda()
+    dst = torch.from_numpy(x.spare[:len(src)].copy()).cuda()
+    gone = torch.from_numpy(x.spare[30:30 + 1].copy()).cuda().expand(len(src)).contiguous()
+    x.kp[x.spare[30]], x.vp[x.spare[30]] = float("nan"), float("nan")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x.unfused()
+        pkv.pkv_compact_pages(x.pool, src, dst, x.kp, x.vp, x.tables)
+        pkv.pkv_copy_pages(x.pool, gone, src, x.kp, x.vp)
+        x.unfused(layer=1)
+        x.unfused()
+    x.unfused()
+    want = x.again[0].clone()
+    graph.replay()
+    assert pkv.pkv_get_error(x.pool) == pkv.PKV_OK
+    assert torch.equal(x.again[0], want)
+    assert torch.isnan(x.kp[src.long()].float()).all()
+    assert torch.equal(x.tables[0, :len(src), 0], dst)
+    del graph
+    x.pool.close()
