@@ -361,6 +361,79 @@ def test_outputs_are_those_of_fp32_arithmetic():
     pool.close()
 
 
+# Relative 2-norm errors of FP32-grade results, inputs N(0, 1). A score (64 products in
+# FP32, the argument in base 2 up to 8, 2^x to 2^-22) leaves a weight some 2.7e-7 off,
+# a rotated query (two products and a sum, each rounded) 5e-8 more, and sums in FP32
+# over the pages of a warp less than that; weights and values average to the same
+# relative error of the output. Limits are some three times that. What they hold: a
+# rotated query without its third BF16 term is 2^-17 / sqrt(3) = 4.4e-6 off an element,
+# 1e-5 in the output; sums kept in the tensor cores over 100,000 tokens 1.8e-6.
+DECODE_LIMIT = 1e-6
+
+
+@pytest.mark.parametrize("lens,window,sinks,max_seq_len", [
+    ([2048, 1500, 700], 700, 4, 2048), ([900] * 64, 600, 4, 2048),
+    ([120000, 100003], 2 ** 31 - 1, 0, 131072)])
+@pytest.mark.parametrize("axes", [0, 1, 3])
+@pytest.mark.parametrize("fused", [False, True])
+def test_decode_is_fp32_arithmetic(lens, window, sinks, max_seq_len, axes, fused):
+    c = W.Cache(lens, max_seq_len, seed=21)
+    kp, vp = c.pools(lambda b: np.ones(lens[b], bool), 0.0)
+    pool = _pool(c)
+    B = len(lens)
+    q = torch.randn(B, 32, 64, generator=c.gen, device="cuda").bfloat16()
+    out = torch.zeros(B, 32, 64, device="cuda")
+    rope, q64 = {}, q.double()
+    new = [torch.stack([t[b][-1] for b in range(B)]) for t in (c.k, c.v)]
+    if axes:
+        cos, sin = W.angles(4000)
+        pos = torch.randint(0, 4000, (axes, B), generator=c.gen, device="cuda").int()
+        rope = dict(rope=pkv.pkv_axes_rope(cos, sin, SECTIONS[axes]), rope_positions=pos)
+        q64 = W.rotate(q, cos, sin, pos, SECTIONS[axes], torch.float64)
+        if fused:
+            turned = W.rotate(new[0], cos, sin, pos, SECTIONS[axes], torch.float32).bfloat16()
+            for b in range(B):
+                c.k[b][-1] = turned[b]
+    if fused:
+        pkv.pkv_window_append_attend(pool, 0, q, *new, kp, vp, c.tables, c.lens_tensor(), out,
+                                     window, sinks=sinks, **rope)
+    else:
+        pkv.pkv_window_attention(pool, 0, q, kp, vp, c.tables, c.lens_tensor(), out, window,
+                                 sinks=sinks, **rope)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    pool.close()
+    ref = torch.cat([W.attend(q64[b:b + 1], c.k[b].double(), c.v[b].double(),
+                              torch.tensor([lens[b] - 1], device="cuda"), window, sinks)[0]
+                     for b in range(B)])
+    assert _relative(out, ref) < DECODE_LIMIT
+
+
+def test_prefill_is_fp32_arithmetic_over_long_windows():
+    """A 4,096-token window, where a tile's sums are longest. A tensor-core sum drops
+    0.36 of 2^-23 of its accumulator on average at each product, towards zero, while
+    the accumulator grows as the square root of the products done: over the 12 n
+    products of n steps 2/3 x 12 n x 0.36 x 2^-23 of it, for n = 2 6.9e-7, with the
+    2.7e-7 of the weights 7.4e-7; sums left in the tensor cores for four steps come to
+    1.4e-6."""
+    window, sinks, n, start_at = 4096, 16, 128, 8000
+    lens = [start_at + n] * 2
+    c = W.Cache(lens, 16384, seed=22)
+    kp, vp = c.pools(lambda b: np.ones(lens[b], bool), 0.0)
+    pool = _pool(c)
+    q = torch.randn(2 * n, 32, 64, generator=c.gen, device="cuda").bfloat16()
+    out = torch.zeros(2 * n, 32, 64, device="cuda")
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    start = torch.tensor([start_at] * 2, dtype=torch.int32, device="cuda")
+    pkv.pkv_window_prefill_attention(pool, 0, q, kp, vp, c.tables, cu, start, out, n, window,
+                                     sinks=sinks)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    pool.close()
+    at = torch.arange(start_at, start_at + n, device="cuda")
+    ref = torch.cat([W.attend(q[n * b:n * b + n].double(), c.k[b].double(), c.v[b].double(), at,
+                              window, sinks)[0] for b in range(2)])
+    assert _relative(out, ref) < 8.5e-7
+
+
 # ---------------------------------------------------------------- prefill
 def _prefill(chunks, starts, window, sinks, max_seq_len=2048, seed=11, junk="mixed", k_scale=1.0,
              max_chunk=None, **kw):
