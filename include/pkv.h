@@ -70,7 +70,8 @@ typedef enum {
  * 16, 32, 8 and 64. max_seq_len is a multiple of 16, at most 2048 (more with
  * PKV_FLAG_LONG_CONTEXT), and sets the block-table row length
  * (max_seq_len / 16). max_splits bounds the split-KV count per sequence (0
- * selects 64; at most 128) and sizes the handle's split workspace. flags: PKV_FLAG_* below (0 for none).
+ * selects 64; at most 128) and sizes the handle's split workspace. flags:
+ * PKV_FLAG_* below (0 for none).
  * num_pages is the number of pages in the pool the caller allocates: 4096
  * pages is the pages' default 128 MiB pool
  * [samir-vllm: Build LLM Inference From Scratch in C++ and CUDA, "Hardware
@@ -114,8 +115,9 @@ typedef struct {
 /* A handle whose max_seq_len may be any multiple of 16 up to
  * PKV_MAX_LONG_CONTEXT. Where max_seq_len exceeds 2,048 it serves the calls
  * without a context limit of their own: pkv_append, pkv_append_rope,
- * pkv_prefill_fill, and those of pkv_window.h, pkv_axes.h and pkv_pages.h; the other
- * attention calls return PKV_ERR_UNSUPPORTED (pkv_plan_decode INVALID_ARG). */
+ * pkv_prefill_fill, and those of pkv_window.h, pkv_axes.h and pkv_pages.h; the
+ * other attention calls return PKV_ERR_UNSUPPORTED (pkv_plan_decode INVALID_ARG),
+ * and pkv_prefill does so before it fills. */
 #define PKV_FLAG_LONG_CONTEXT 2
 #define PKV_MAX_LONG_CONTEXT 1048576
 

@@ -4,9 +4,9 @@
  * compact a pool (pkv_sched_compact).
  *
  * src, dst: device int32 [n] page ids (4-byte aligned; the pools and tables 16,
- * as everywhere). A page may be the source of several pairs. A destination must be named by
- * one pair only and be no pair's source: pairs that break this are skipped
- * and flagged (PKV_ERR_OUT_OF_RANGE from pkv_get_error), the others are
+ * as everywhere). A page may be the source of several pairs. A destination must
+ * be named by one pair only and be no pair's source: pairs that break this are
+ * skipped and flagged (PKV_ERR_OUT_OF_RANGE from pkv_get_error), the others are
  * carried out, so the result never depends on the order of the copies. Pairs
  * with an id outside [0, num_pages) are skipped and flagged; an id in range
  * counts as named even where the rest of its pair is bad.

@@ -44,9 +44,9 @@
 // takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
 // cycles each); a tile's start and end cost it some 4,000 more. The products are
 // never waited for: every barrier of theirs is complete when it is first looked
-// at. Two 4,096-token chunks behind a 4,096-token window: 465 us (593 TFLOP/s of
+// at. Two 4,096-token chunks behind a 4,096-token window: 467 us (591 TFLOP/s of
 // score and value products counted once); eight prompts of up to 2,048 tokens
-// behind 512: 112 us; sixteen of 512 tokens behind 128: 43.3 us. What was measured
+// behind 512: 111 us; sixteen of 512 tokens behind 128: 44.3 us. What was measured
 // on the way, the first of these: 718 us as a plain port of the step loop; 696
 // with the products issued by a converged warp (one thread in a divergent branch
 // takes 55 cycles an issue for its operands); 654 with the split's subtractions
@@ -57,10 +57,11 @@
 // predicated arrivals; 472 with O joined behind the first half of P, when the
 // products it waits for are long done; 483 with segments of two steps instead of
 // four; 469 with steps of any four pages; 465 with the next tile looked up under
-// the last product. The second: 159 us up to the page ids, one CTA per tile; 134
-// with tiles drawn by resident CTAs, V cleared by its loader and results written
-// through shared memory; 122 with word masks and a first tile that needs no
-// draw; 112 at the end. Slower: two threads per row (16 softmax warps per SM, by
+// the last product; 467 with no tile drawn that does not exist. The second: 159
+// us up to the page ids, one CTA per tile; 134 with tiles drawn by resident CTAs,
+// V cleared by its loader and results written through shared memory; 122 with
+// word masks and a first tile that needs no draw; 112, and 111 with the last of
+// the above, at the end. Slower: two threads per row (16 softmax warps per SM, by
 // 10 %), and the first half of P taken against the running maximum before the
 // step's own is known, done again for a row that outgrew it (by 12 %).
 
@@ -365,6 +366,8 @@ struct TileWalk {
   int top = 0, bottom = 0;        // tiles top - 1 .. bottom belong to the same sequences, ...
   uint32_t in = 0;                // ... these
   uint32_t before = 0, here = 0;  // tiles in front of those; how many they are
+  int nth;                        // this lane's place among `in`, -1 if it is not one of them
+  float per_level;                // 1 / the number of `in`
   int ahead_row0, ahead_end, ahead_start;
 
   __device__ __forceinline__ void fetch(const WindowPrefillParams& prm, int b) {
@@ -393,16 +396,17 @@ struct TileWalk {
       in = __ballot_sync(0xffffffffu, tiles >= top);
       bottom = __reduce_max_sync(0xffffffffu, tiles < top ? tiles : 0);
       here = static_cast<uint32_t>(__popc(in) * (top - bottom));
+      nth = (in >> lane & 1u) ? __popc(in & ((1u << lane) - 1u)) : -1;
+      per_level = __fdividef(1.f, static_cast<float>(__popc(in)));
     }
-    // down / count, exact: down < 2^20, so the quotient's error stays below a
-    // quarter of 1 / count, and down + 1/2 half of it away from the next integer
-    const int down = static_cast<int>(n - before), count = __popc(in);
-    const int level = static_cast<int>(
-        __fdividef(static_cast<float>(down) + 0.5f, static_cast<float>(count)));
+    // down / count, exact: down < 2^20, so the product's error stays below a
+    // quarter of 1 / count, and (down + 1/2) / count is half of it or more away
+    // from an integer
+    const int down = static_cast<int>(n - before);
+    const int level = static_cast<int>((static_cast<float>(down) + 0.5f) * per_level);
     tile = top - 1 - level;
-    const bool mine =
-        (in >> lane & 1u) && __popc(in & ((1u << lane) - 1u)) == down - level * count;
-    const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    const int from =
+        __ffs(__ballot_sync(0xffffffffu, nth == down - level * __popc(in))) - 1;
     b = first + from;
     b_row0 = __shfl_sync(0xffffffffu, row0, from);
     b_rows = __shfl_sync(0xffffffffu, rows, from);
