@@ -22,7 +22,7 @@
 // the first page lands are what is left: 64 ragged sequences behind 1,024 tokens
 // take 15.5 us, of which the block reads the lengths and finds its work for 1.7,
 // its page ids for 1.2, its first page for 2.4, and merges for 1.5 to 2.3; one
-// 517-token window 4.2 us. (Inputs larger than L2, launches in a graph.)
+// sequence behind 512 tokens 4.2 us. (Inputs larger than L2, launches in a graph.)
 
 #include <cuda.h>
 #include <cuda_runtime.h>
