@@ -7,6 +7,7 @@ linked statically, so it loads beside any PyTorch build. Rebuilds when a
 source or a public header is newer than the library.
 """
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -44,11 +45,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = LIBRARY + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-cudart", "static", "-I", INCLUDE, "-o", tmp, *sources()]
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+        flags.insert(0, "-Xptxas=-v")
+
+    def compile_one(source):
+        obj = os.path.join(BUILD_DIR, f"{os.path.basename(source)}.{os.getpid()}.o")
+        subprocess.run([nvcc(), *flags, "-c", "-o", obj, source], check=True)
+        return obj
+
+    objects = []
+    try:
+        # one compiler per source at a time, as many as there are cores
+        with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+            objects = list(pool.map(compile_one, sources()))
+        subprocess.run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o",
+                        tmp, *objects], check=True)
+    finally:
+        for obj in objects:
+            os.remove(obj)
     os.replace(tmp, LIBRARY)
     return LIBRARY
 

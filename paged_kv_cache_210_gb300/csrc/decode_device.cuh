@@ -503,12 +503,12 @@ __device__ __forceinline__ void attend_page_mma(const uint8_t* kt, const uint8_t
 
 // ---------------------------------------------------------------- merges
 // The block's warps merged in shared memory: lanes 0..15 of each warp store
-// head lane / 4's max, sum (summed over the lane quad) and output tiles;
-// then thread t < 128 gets the log-sum-exp state of head g = (t / 32) % 4
-// for dims d0 = 2 (t % 32), d0 + 1 (M: max, L: sum, O: unnormalised output).
-template <int kWarps, class Smem>
-__device__ __forceinline__ void block_merge_mma(Smem& sm, MmaState& st, int warp, int lane,
-                                                float& M, float& L, float2& O) {
+// head lane / 4's max, sum (summed over the lane quad) and output tiles
+// (block_merge_store); then thread t < 128 gets the log-sum-exp state of head
+// g = (t / 32) % 4 for dims d0 = 2 (t % 32), d0 + 1 (M: max, L: sum, O:
+// unnormalised output; block_merge_read).
+template <class Smem>
+__device__ __forceinline__ void block_merge_store(Smem& sm, MmaState& st, int warp, int lane) {
   st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 1);
   st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 2);
   if (lane < 16) {
@@ -523,7 +523,10 @@ __device__ __forceinline__ void block_merge_mma(Smem& sm, MmaState& st, int warp
       *reinterpret_cast<float2*>(&sm.acc[warp][g][8 * j + 2 * qq]) =
           make_float2(st.o[j][0], st.o[j][1]);
   }
-  __syncthreads();
+}
+
+template <int kWarps, class Smem>
+__device__ __forceinline__ void block_merge_read(Smem& sm, float& M, float& L, float2& O) {
   const int g = (threadIdx.x >> 5) & (kGroup - 1);
   const int d0 = 2 * (threadIdx.x & 31);
   M = -INFINITY;
@@ -540,6 +543,14 @@ __device__ __forceinline__ void block_merge_mma(Smem& sm, MmaState& st, int warp
     O.x += f * sm.acc[w][g][d0];
     O.y += f * sm.acc[w][g][d0 + 1];
   }
+}
+
+template <int kWarps, class Smem>
+__device__ __forceinline__ void block_merge_mma(Smem& sm, MmaState& st, int warp, int lane,
+                                                float& M, float& L, float2& O) {
+  block_merge_store(sm, st, warp, lane);
+  __syncthreads();
+  block_merge_read<kWarps>(sm, M, L, O);
 }
 
 

@@ -11,6 +11,12 @@
 
 #include "pkv.h"
 
+// Resident blocks per SM of a windowed decode kernel's shapes.
+struct WindowResidency {
+  int blocks_per_sm;           // ticket merge
+  int cluster_blocks_per_sm;   // cluster merge
+};
+
 struct pkv_pool {
   pkv_pool_config cfg;
   int device;
@@ -31,8 +37,8 @@ struct pkv_pool {
                                     // allocation
   unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between
                                     // launches)
-  int window_blocks_per_sm;         // resident blocks of the windowed decode's ticket shape
-  int window_cluster_blocks_per_sm; // ... and of its cluster shape
+  WindowResidency window;           // the windowed decode over BF16 pages
+  WindowResidency quant;            // ... and over 8-bit pages
   std::atomic<bool> pages_written{false};   // the handle's last page or fill call (pkv_pages.h,
                                             // pkv_axes.h) has had no decode launch after it
   int layer_clusters[5];   // resident clusters of the multi-layer kernel, S = 1, 2, 4, 8, 16
@@ -77,7 +83,8 @@ bool pkv_pool_tensor_map(const void* pool, int num_pages, CUtensorMap* map);
 // many of its clusters the device holds at once (pool->layer_clusters).
 bool pkv_layers_setup(pkv_pool* pool);
 
-// window.cu: the windowed decode kernels' attributes and residency.
+// window.cu, quant.cu: the windowed decode kernels' attributes and residency.
 bool pkv_window_setup(pkv_pool* pool);
+bool pkv_quant_setup(pkv_pool* pool);
 
 #endif  // PKV_POOL_INTERNAL_H
