@@ -37,7 +37,8 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_append", "pkv_decode_att
             "pkv_pool_device_figures", "pkv_window_attention", "pkv_window_append_attend",
             "pkv_window_prefill_attention", "pkv_prefill_fill_axes", "pkv_copy_pages",
             "pkv_compact_pages", "pkv_sched_fork", "pkv_sched_held", "pkv_sched_release",
-            "pkv_sched_compact", "pkv_status_string")
+            "pkv_sched_compact", "pkv_quant_fill", "pkv_quant_read", "pkv_quant_attention",
+            "pkv_quant_append_attend", "pkv_status_string")
 
 
 class PkvError(RuntimeError):
@@ -67,6 +68,7 @@ class PoolConfig(ctypes.Structure):
 PKV_FLAG_PDL, PKV_FLAG_LONG_CONTEXT = 1, 2
 PKV_MAX_LONG_CONTEXT = 1048576
 PKV_MAX_AXES = 4
+PKV_QUANT_TILE_BYTES = 2080    # a (page, kv head) tile of the 8-bit cache
 
 
 class AxesRopeConfig(ctypes.Structure):
@@ -145,6 +147,10 @@ def load(path: str = None):
     lib.pkv_sched_held.argtypes = [P, i, SP, SP]
     lib.pkv_sched_release.argtypes = [P, i, i, i, SP]
     lib.pkv_sched_compact.argtypes = [P, P, P, i, SP]
+    lib.pkv_quant_fill.argtypes = [P, i, P, P, P, P, P, P, P, P, i, i, i, i, P]
+    lib.pkv_quant_read.argtypes = [P, i, P, P, P, P, P, P, i, i, i, P]
+    lib.pkv_quant_attention.argtypes = [P, i, P, P, P, P, P, i, i, P, P, i, i, i, P]
+    lib.pkv_quant_append_attend.argtypes = [P, i, P, P, P, P, P, P, P, i, i, P, P, i, i, i, P]
     lib.pkv_status_string.argtypes = [i]
     lib.pkv_status_string.restype = ctypes.c_char_p
     for name in EXPORTED[:-1]:
@@ -166,8 +172,8 @@ def _dtype_name(dtype):
 
 def _addr(x, dtype=None, what="tensor"):
     """Address of a tensor (or an int address, or None). A tensor must be
-    contiguous and, when `dtype` is given ("bfloat16", "float32", "int32"),
-    of that dtype: the library reads raw memory in the layouts include/*.h
+    contiguous and, when `dtype` is given ("bfloat16", "float32", "int32",
+    ...), of that dtype: the library reads raw memory in the layouts include/*.h
     documents."""
     if x is None:
         return None
@@ -189,7 +195,8 @@ _DTYPES = {"q": "bfloat16", "k": "bfloat16", "v": "bfloat16", "k_pool": "bfloat1
            "v_pool": "bfloat16", "block_tables": "int32", "positions": "int32",
            "seq_lens": "int32", "cu_tokens": "int32", "start_pos": "int32", "out": "float32",
            "rope_cos": "float32", "rope_sin": "float32", "rope_positions": "int32",
-           "q_out": "bfloat16", "src": "int32", "dst": "int32", "tokens": "int32"}
+           "q_out": "bfloat16", "src": "int32", "dst": "int32", "tokens": "int32",
+           "kv_pool": "uint8"}
 
 
 def _ptrs(**tensors):
@@ -220,6 +227,7 @@ class Pool:
         self.device = device     # CUDA device index, where known
         # elements of a pool tensor and entries of the block tables
         self.elements = config.num_pages * NUM_KV_HEADS * PAGE_SIZE * HEAD_DIM if config else 0
+        self.quant_bytes = config.num_pages * NUM_KV_HEADS * PKV_QUANT_TILE_BYTES if config else 0
         self.entries = config.num_layers * config.max_batch * \
             (config.max_seq_len // PAGE_SIZE) if config else 0
         self._lib = lib
@@ -631,6 +639,74 @@ def pkv_compact_pages(pool: Pool, src, dst, k_pool, v_pool, block_tables, n=None
         _arg(pool, "v_pool", v_pool, pool.elements),
         _arg(pool, "block_tables", block_tables, pool.entries), n, _pool_stream(pool, stream))
     _check(st, "pkv_compact_pages")
+
+
+# ---------------------------------------------------------------- 8-bit cache
+def pkv_quant_fill(pool: Pool, layer, k, v, kv_pool, block_tables, cu_tokens, start_pos,
+                   max_chunk_tokens, rope=None, rope_positions=None, batch=None,
+                   total_tokens=None, stream=None):
+    """Quantises chunk tokens' K/V (bf16 [T][8][64]) into their pages of kv_pool
+    (uint8 [pages][8][PKV_QUANT_TILE_BYTES]); rope, rope_positions int32
+    [axes][>= T]: the keys are rotated first."""
+    batch = _int(_batch(start_pos, batch))
+    total = int(k.shape[0]) if total_tokens is None else _int(int(total_tokens))
+    new = total * NUM_KV_HEADS * HEAD_DIM
+    st = pool._lib.pkv_quant_fill(
+        pool.handle, _int(int(layer)), _arg(pool, "k", k, new), _arg(pool, "v", v, new),
+        _arg(pool, "kv_pool", kv_pool, pool.quant_bytes),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
+        *_rope_args(pool, rope, rope_positions, total), batch, total, _int(int(max_chunk_tokens)),
+        _pool_stream(pool, stream))
+    _check(st, "pkv_quant_fill")
+
+
+def pkv_quant_read(pool: Pool, layer, kv_pool, block_tables, cu_tokens, start_pos, k, v,
+                   max_chunk_tokens, batch=None, total_tokens=None, stream=None):
+    """Reads tokens start_pos .. back into k, v (bf16 [T][8][64]), exactly."""
+    batch = _int(_batch(start_pos, batch))
+    total = int(k.shape[0]) if total_tokens is None else _int(int(total_tokens))
+    rows = total * NUM_KV_HEADS * HEAD_DIM
+    st = pool._lib.pkv_quant_read(
+        pool.handle, _int(int(layer)), _arg(pool, "kv_pool", kv_pool, pool.quant_bytes),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
+        _arg(pool, "k", k, rows), _arg(pool, "v", v, rows), batch, total,
+        _int(int(max_chunk_tokens)), _pool_stream(pool, stream))
+    _check(st, "pkv_quant_read")
+
+
+def pkv_quant_attention(pool: Pool, layer, q, kv_pool, block_tables, seq_lens, out, window,
+                        sinks=0, rope=None, rope_positions=None, batch=None, num_splits=0,
+                        stream=None):
+    """pkv_window_attention over the 8-bit cache (q bf16 [B][32][64], out fp32)."""
+    batch = _int(_batch(seq_lens, batch))
+    rows = batch * NUM_Q_HEADS * HEAD_DIM
+    st = pool._lib.pkv_quant_attention(
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows),
+        _arg(pool, "kv_pool", kv_pool, pool.quant_bytes),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch,
+        _int(int(num_splits)), _pool_stream(pool, stream))
+    _check(st, "pkv_quant_attention")
+
+
+def pkv_quant_append_attend(pool: Pool, layer, q, k, v, kv_pool, block_tables, seq_lens, out,
+                            window, sinks=0, rope=None, rope_positions=None, batch=None,
+                            num_splits=0, stream=None):
+    """Quantise and append (at seq_lens - 1, the key rotated with rope) and
+    pkv_quant_attention in one launch; k, v bf16 [B][8][64]."""
+    batch = _int(_batch(seq_lens, batch))
+    rows, new = batch * NUM_Q_HEADS * HEAD_DIM, batch * NUM_KV_HEADS * HEAD_DIM
+    st = pool._lib.pkv_quant_append_attend(
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows), _arg(pool, "k", k, new),
+        _arg(pool, "v", v, new), _arg(pool, "kv_pool", kv_pool, pool.quant_bytes),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "seq_lens", seq_lens, batch), _arg(pool, "out", out, rows), _length(int(window)),
+        _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch,
+        _int(int(num_splits)), _pool_stream(pool, stream))
+    _check(st, "pkv_quant_append_attend")
 
 
 # ---------------------------------------------------------------- admission scheduler (host)

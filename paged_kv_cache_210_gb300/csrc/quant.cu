@@ -1,0 +1,393 @@
+// Decode attention over the 8-bit KV cache for GB300 (sm_103a), with windows,
+// sinks, optional fused append and rotation by several position axes (declared
+// in include/pkv_quant.h). The kernel is window_device.cuh's; here are the
+// 8-bit pages' tiles and their products.
+//
+// A tile's codes c stand for c 2^e, e one exponent a token (K_t = c_t 2^ek_t, V_t
+// = d_t 2^ev_t), so with the codes as exact FP16 operands
+//   score_t = 2^ek_t (q . c_t),   out = sum_t (p_t 2^ev_t) d_t / sum_t p_t.
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pkv.h"
+#include "pkv_quant.h"
+#include "quant.cuh"
+#include "window_device.cuh"
+
+using namespace pkv_window;
+using namespace pkv_quant_dev;
+
+namespace {
+
+// ---------------------------------------------------------------- page math
+// One page's products are warp-wide mma.sync m16n8k16 of FP16 operands.
+//   scores: S = Q K^T, rows 0..7 = the 4 heads' queries, their high parts in rows
+//           0..3 and their low ones in rows 4..7 (rows 8..15 zero), columns =
+//           tokens, two products' worth;
+//   values: O^T += V^T P^T, rows = 16 dims, columns = the 4 heads' weights,
+//           high parts in columns 0..3 and low ones in 4..7, contraction over
+//           the 16 tokens: 4 products fill the instruction's whole shape.
+// The scores' accumulators are then P^T's operand fragments: lane (g, q) = (L /
+// 4, L % 4) holds head g % 4's tokens 2 q, 2 q + 1, 8 + 2 q and 9 + 2 q in both.
+//
+// FP16 has 11 bits and a narrow range: a factor that needs 24 bits (a rotated
+// query, a weight) is the sum of two FP16 terms after a scaling by a power of
+// two, one per head: queries so that the largest of 64 dims lies in [2^14,
+// 2^15), weights p 2^ev so that the largest seen lies in [2^7, 2^15]. Terms lose
+// what lies 2^-31 and more below the largest.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two FP32 values -> FP16 pair, rounded to nearest even.
+__device__ __forceinline__ uint32_t float2_to_half2(float e0, float e1) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(e1), "f"(e0));
+  return w;
+}
+
+// x - (an FP16 half of the pair h), exact where h holds x rounded.
+template <int kUpper>
+__device__ __forceinline__ float rest_of_half(float x, uint32_t h) {
+  float f;
+  if (kUpper)
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, u;\n\t}" : "=f"(f) : "r"(h));
+  else
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
+  return x - f;
+}
+
+// The high parts (lanes 0..15) or the low ones (16..31) of two values.
+__device__ __forceinline__ uint32_t half_terms(float x0, float x1, int lane) {
+  const uint32_t hi = float2_to_half2(x0, x1);
+  const uint32_t lo = float2_to_half2(rest_of_half<0>(x0, hi), rest_of_half<1>(x1, hi));
+  return lane < 16 ? hi : lo;
+}
+
+// Largest over the four lanes of a row.
+__device__ __forceinline__ float row_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+struct QuantTiles {
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kCopyBytes = kQuantTile;
+  struct alignas(16) Ring {
+    uint8_t tile[kStages][kQuantTile];
+  };
+  struct Source {
+    uint8_t* pool;               // [num_pages][8][kQuantTile]
+  };
+  // Lane (g, q): head g % 4, dims 16 q .. + 15 as 8 pairs; `to_log2` takes the
+  // products with the scaled query to the exponent's base-2 scores.
+  struct Queries {
+    uint32_t a[8];
+    float to_log2;
+  };
+  struct State {
+    float o[4][4];   // chunk c: dims 16 c + 2 g (0, 1) and + 1 (2, 3), columns 2 q, 2 q + 1
+    float m_run;     // the base-2 exponent p is taken against: p = 2^(x - m_run) <= 1
+    float l_run;     // this lane's share of the head's sum
+    float unit;      // the power of two that the weights p 2^ev are scaled by
+    __device__ __forceinline__ void reset() {
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+      m_run = -INFINITY;
+      l_run = 0.f;
+      unit = 0x1p126f;
+    }
+    // every column's sums times its head's factor (lane (g, q) holds head g's)
+    __device__ __forceinline__ void rescale(float factor, int lane) {
+      const int head = 2 * (lane & 1);
+      const float f0 = __shfl_sync(0xffffffffu, factor, 4 * head);
+      const float f1 = __shfl_sync(0xffffffffu, factor, 4 * head + 4);
+      #pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        o[c][0] *= f0;
+        o[c][1] *= f1;
+        o[c][2] *= f0;
+        o[c][3] *= f1;
+      }
+    }
+  };
+
+  static const WindowResidency& residency(const pkv_pool* pool) { return pool->quant; }
+  static __device__ __forceinline__ void prefetch(const Source&) {}
+
+  // One bulk copy moves the whole tile.
+  static __device__ __forceinline__ void copy(Ring& ws, int stage, const Source& src, int part,
+                                              int kvh, int phys, unsigned long long* bar) {
+    if (part != 0) return;
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(smem_u32(ws.tile[stage])),
+          "l"(src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile), "r"(kQuantTile),
+          "r"(smem_u32(bar))
+        : "memory");
+  }
+
+  // V codes and exponents of tokens that do not count: zero.
+  static __device__ __forceinline__ void hide_rows(Ring& ws, int stage, uint32_t seen, int lane) {
+    uint8_t* t = ws.tile[stage];
+    for (int idx = lane; idx < 4 * kPage; idx += 32)
+      if (!((seen >> (idx & (kPage - 1))) & 1u))
+        *reinterpret_cast<uint4*>(t + kCodeBytes + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < kPage && !((seen >> lane) & 1u)) t[kVExp + lane] = 0;
+  }
+
+  // The appended row (a 16-byte chunk per lane: K in lanes 0..7, V in 8..15):
+  // rotated, quantised, into its slot of the pool and of the stage.
+  template <bool kRope>
+  static __device__ __forceinline__ void put_row(Ring& ws, int stage, const Source& src, int kvh,
+                                                 int slot, int phys, bool to_pool, bool to_stage,
+                                                 uint4 val, float ang_c, float ang_s, int lane) {
+    const int c = lane & 7;
+    float x[8];
+    unpack8(val, x);
+    if (kRope) {
+      float cs[8], sn[8], partner[8];
+      unpack8(shfl_xor_uint4(val, 4), partner);
+      #pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        cs[e] = __shfl_sync(0xffffffffu, ang_c, 8 * (c & 3) + e);
+        sn[e] = __shfl_sync(0xffffffffu, ang_s, 8 * (c & 3) + e);
+      }
+      if (lane < 8) rotate8(x, partner, c >= 4, cs, sn);
+    }
+    uint2 codes;
+    const uint32_t e = quantise_row(x, codes);
+    if (lane >= 16) return;
+    const int at = lane < 8 ? k_at(slot, 8 * c) : v_at(slot, 8 * c);
+    const int exp_at = (lane < 8 ? kKExp : kVExp) + slot;
+    if (to_pool) {
+      uint8_t* t = src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile;
+      *reinterpret_cast<uint2*>(t + at) = codes;
+      if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
+    }
+    if (to_stage) {
+      uint8_t* t = ws.tile[stage];
+      *reinterpret_cast<uint2*>(t + at) = codes;
+      if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
+    }
+  }
+
+  template <bool kRope>
+  static __device__ __forceinline__ void load_queries(const uint16_t* qrow, int lane, float c,
+                                                      float s, Queries& q) {
+    const int g = (lane >> 2) & 3;
+    const int qq = lane & 3;
+    const uint4* src = reinterpret_cast<const uint4*>(qrow + g * kDim + 16 * qq);
+    const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    float x[16];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 own = bf16x2_to_float2(w[i]);
+      x[2 * i] = own.x;
+      x[2 * i + 1] = own.y;
+      if constexpr (kRope) {
+        // dims < 32: x cos - y sin; dims >= 32: y cos + x sin; the partner half
+        // sits in lane ^ 2
+        const float2 par = bf16x2_to_float2(__shfl_xor_sync(0xffffffffu, w[i], 2));
+        const int pair = 16 * (qq & 1) + 2 * i;
+        const float c0 = __shfl_sync(0xffffffffu, c, pair);
+        const float c1 = __shfl_sync(0xffffffffu, c, pair + 1);
+        const float s0 = __shfl_sync(0xffffffffu, s, pair);
+        const float s1 = __shfl_sync(0xffffffffu, s, pair + 1);
+        const float sgn = qq < 2 ? -1.f : 1.f;
+        x[2 * i] = __fadd_rn(__fmul_rn(own.x, c0), sgn * __fmul_rn(par.x, s0));
+        x[2 * i + 1] = __fadd_rn(__fmul_rn(own.y, c1), sgn * __fmul_rn(par.y, s1));
+      }
+    }
+    float most = 0.f;
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(x[i]));
+    most = row_max(most);
+    // 2^(14 - floor(log2 most)), at most 2^125
+    const uint32_t up = 268u - max(__float_as_uint(most) >> 23, 16u);
+    const float scale = scale_of(up);
+    q.to_log2 = 1.4426950408889634f * 0.125f * inverse_scale_of(up);   // log2(e) / sqrt(64)
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // without rotation the high parts are the queries (8 bits)
+      const float x0 = x[2 * i] * scale, x1 = x[2 * i + 1] * scale;
+      q.a[i] = kRope ? half_terms(x0, x1, lane) : float2_to_half2(x0, x1);
+    }
+  }
+
+  // One page; bit t of `seen` = token t counts (at least one does). The scores
+  // of the others are dropped by select; their V rows and exponents are zero.
+  // Lanes L and L + 16 hold the same scores, maxima and sums.
+  template <bool kRope>
+  static __device__ __forceinline__ void attend(Ring& ws, int stage, uint32_t seen, int lane,
+                                                const Queries& q, State& st) {
+    const uint8_t* t = ws.tile[stage];
+    const int g8 = lane >> 2;
+    const int qq = lane & 3;
+    float s[4], scale_v[4];
+    #pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const uint4 kw = *reinterpret_cast<const uint4*>(t + k_at(8 * nt + g8, 16 * qq));
+      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      #pragma unroll
+      for (int sl = 0; sl < 4; ++sl)
+        mma_f16(d, q.a[2 * sl], 0u, q.a[2 * sl + 1], 0u, codes_to_half2<0>(w[sl]),
+                codes_to_half2<1>(w[sl]));
+      if (kRope) {   // rows g and g + 4: the two parts of head g's query
+        d[0] += __shfl_xor_sync(0xffffffffu, d[0], 16);
+        d[1] += __shfl_xor_sync(0xffffffffu, d[1], 16);
+      }
+      const uint32_t ek = *reinterpret_cast<const uint16_t*>(t + kKExp + 8 * nt + 2 * qq);
+      const uint32_t ev = *reinterpret_cast<const uint16_t*>(t + kVExp + 8 * nt + 2 * qq);
+      s[2 * nt] = d[0] * scale_of(ek & 0xffu);
+      s[2 * nt + 1] = d[1] * scale_of(ek >> 8);
+      scale_v[2 * nt] = scale_of(ev & 0xffu);
+      scale_v[2 * nt + 1] = scale_of(ev >> 8);
+    }
+    if (seen != 0xffffu) {
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 8 * (i >> 1) + 2 * qq + (i & 1);
+        if (!((seen >> tok) & 1u)) s[i] = -INFINITY;
+      }
+    }
+    // p stays within 1: the exponent it is taken against moves 8 above the
+    // row's maximum whenever that passes it
+    const float lane_top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) * q.to_log2;
+    if (__any_sync(0xffffffffu, lane_top > st.m_run)) {
+      const float top = row_max(lane_top);
+      float alpha = 1.f;
+      if (top > st.m_run) {
+        alpha = fast_exp2(st.m_run - (top + kRescaleLog2));   // 0 on the first page
+        st.m_run = top + kRescaleLog2;
+        st.l_run *= alpha;
+      }
+      st.rescale(alpha, lane);
+    }
+    const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
+    float p[4], w[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = fast_exp2(fmaf(s[i], q.to_log2, -mu));
+      w[i] = p[i] * scale_v[i];
+    }
+    st.l_run += (p[0] + p[1]) + (p[2] + p[3]);
+    const float lane_most = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+    if (__any_sync(0xffffffffu, lane_most * st.unit > 32768.f)) {
+      const float most = row_max(lane_most);
+      float factor = 1.f;
+      if (most * st.unit > 32768.f) {
+        // 2^(7 - floor(log2 most)): the largest then lies in [2^7, 2^8)
+        const float unit = scale_of(261u - (__float_as_uint(most) >> 23));
+        factor = unit * inverse_scale_of(__float_as_uint(st.unit) >> 23);
+        st.unit = unit;
+      }
+      st.rescale(factor, lane);
+    }
+    uint32_t pb[2];
+    #pragma unroll
+    for (int h = 0; h < 2; ++h)
+      pb[h] = half_terms(w[2 * h] * st.unit, w[2 * h + 1] * st.unit, lane);
+    // lane L addresses token L % 16 of chunk 2 j (lanes 0..15) or 2 j + 1: a
+    // transposed matrix of 16-bit pairs, dims 2 g and 2 g + 1 of tokens 2 q, 2 q + 1
+    const uint32_t vrow = smem_u32(t) + kCodeBytes + lane * 16;
+    #pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t v[4];
+      ldsm_x4_trans(v, vrow + 2 * j * kChunkBytes);
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __byte_perm(v[2 * h], 0u, 0x3120);       // tokens 0..7
+        const uint32_t hi = __byte_perm(v[2 * h + 1], 0u, 0x3120);   // tokens 8..15
+        // from zero, and added up in FP32: a tensor-core sum drops the bits
+        // below its accumulator's last one, always downwards
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(d, codes_to_half2<0>(lo), codes_to_half2<1>(lo), codes_to_half2<0>(hi),
+                codes_to_half2<1>(hi), pb[0], pb[1]);
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[2 * j + h][e] += d[e];
+      }
+    }
+  }
+
+  // The warp's part for the block merge.
+  template <class Smem>
+  static __device__ __forceinline__ void finish(Smem& sm, State& st, int warp, int lane) {
+    const int g8 = lane >> 2;
+    const int qq = lane & 3;
+    st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 1);
+    st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 2);
+    st.rescale(inverse_scale_of(__float_as_uint(st.unit) >> 23), lane);
+    if (qq == 0 && g8 < kGroup) {
+      sm.m[warp][g8] = st.m_run;
+      sm.l[warp][g8] = st.l_run;
+    }
+    #pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // columns 2 q, 2 q + 1 and their low parts' 2 q + 4, 2 q + 5
+      #pragma unroll
+      for (int e = 0; e < 4; ++e)
+        st.o[c][e] += __shfl_xor_sync(0xffffffffu, st.o[c][e], 2);
+      if (qq < 2) {
+        #pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(&sm.acc[warp][2 * qq + e][16 * c + 2 * g8]) =
+              make_float2(st.o[c][e], st.o[c][e + 2]);
+      }
+    }
+  }
+};
+static_assert(4 * (kTicketSmemBytes<QuantTiles> + 1024) <= kSmemPerSm, "4 ticket blocks per SM");
+static_assert(3 * (kClusterSmemBytes<QuantTiles> + 1024) <= kSmemPerSm, "3 cluster blocks per SM");
+static_assert(sizeof(WindowSmem<QuantTiles>) % 16 == 0,
+              "the cluster inbox follows 16-byte aligned");
+
+template <bool kFused>
+pkv_status launch_quant(pkv_pool_t pool, int layer, const void* q, const void* k, const void* v,
+                        const void* kv_pool, const int32_t* block_tables,
+                        const int32_t* seq_lens, float* out, int window, int sinks,
+                        const pkv_axes_rope* rope, const int32_t* rope_positions,
+                        int position_stride, int batch, int num_splits, void* stream) {
+  auto source = [&](QuantTiles::Source& src) {
+    src.pool = const_cast<uint8_t*>(static_cast<const uint8_t*>(kv_pool));
+    return true;
+  };
+  return launch_window<QuantTiles, kFused>(
+      pool, layer, q, k, v, kv_pool && pkv_aligned16(kv_pool), source, block_tables, seq_lens,
+      out, window, sinks, rope, rope_positions, position_stride, batch, num_splits, stream);
+}
+
+}  // namespace
+
+bool pkv_quant_setup(pkv_pool* pool) { return setup_window<QuantTiles>(&pool->quant); }
+
+extern "C" {
+
+pkv_status pkv_quant_attention(pkv_pool_t pool, int layer, const void* q, const void* kv_pool,
+                               const int32_t* block_tables, const int32_t* seq_lens, float* out,
+                               int window, int sinks, const pkv_axes_rope* rope,
+                               const int32_t* rope_positions, int position_stride, int batch,
+                               int num_splits, void* stream) {
+  return launch_quant<false>(pool, layer, q, nullptr, nullptr, kv_pool, block_tables, seq_lens,
+                             out, window, sinks, rope, rope_positions, position_stride, batch,
+                             num_splits, stream);
+}
+
+pkv_status pkv_quant_append_attend(pkv_pool_t pool, int layer, const void* q, const void* k,
+                                   const void* v, void* kv_pool, const int32_t* block_tables,
+                                   const int32_t* seq_lens, float* out, int window, int sinks,
+                                   const pkv_axes_rope* rope, const int32_t* rope_positions,
+                                   int position_stride, int batch, int num_splits, void* stream) {
+  return launch_quant<true>(pool, layer, q, k, v, kv_pool, block_tables, seq_lens, out, window,
+                            sinks, rope, rope_positions, position_stride, batch, num_splits,
+                            stream);
+}
+
+}  // extern "C"

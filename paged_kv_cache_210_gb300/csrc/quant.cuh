@@ -1,0 +1,116 @@
+// Internal to libpkv: the 8-bit cache's tiles (include/pkv_quant.h) and the
+// quantisation of a row, shared by the fill (quant_store.cu) and the fused
+// decode (quant.cu).
+#ifndef PKV_QUANT_CUH
+#define PKV_QUANT_CUH
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pkv_quant.h"
+#include "device_common.cuh"
+
+namespace pkv_quant_dev {
+
+using namespace pkv_dev;
+
+constexpr int kQuantTile = PKV_QUANT_TILE_BYTES;
+constexpr int kCodeBytes = kPage * kDim;             // of K, and of V
+constexpr int kChunkDims = 16;                       // dims of a V chunk
+constexpr int kChunkBytes = kPage * kChunkDims;      // 256
+constexpr int kKExp = 2 * kCodeBytes;                // exponent bytes of K ...
+constexpr int kVExp = kKExp + kPage;                 // ... and of V
+static_assert(kVExp + kPage == kQuantTile && kQuantTile % 16 == 0, "the documented tile");
+
+// Where dims d .. of token t start in a tile (d a multiple of 8).
+__host__ __device__ constexpr int k_at(int t, int d) { return t * kDim + d; }
+__host__ __device__ constexpr int v_at(int t, int d) {
+  return kCodeBytes + d / kChunkDims * kChunkBytes + t * kChunkDims + d % kChunkDims;
+}
+
+constexpr float kLargest = 0x1.ep127f;               // 240 x 2^120, the largest value stored
+
+// Values beyond the largest are taken as that; NaN stays.
+__device__ __forceinline__ float within_range(float x) {
+  return fabsf(x) > kLargest ? copysignf(kLargest, x) : x;
+}
+
+// The exponent byte of a row whose largest magnitude is `most` (clamped): the
+// least e >= -124 with most <= 448 x 2^e = 1.75 x 2^(e + 8), plus 127. Adding
+// 0x1fffff carries into the exponent where the fraction is above 1.75.
+__device__ __forceinline__ uint32_t exponent_byte(float most) {
+  const int e = static_cast<int>((__float_as_uint(most) + 0x1fffffu) >> 23) - 8;
+  return static_cast<uint32_t>(max(e, 3));
+}
+
+// 2^(byte - 127) and its inverse, exact for 1 <= byte <= 253.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+__device__ __forceinline__ float inverse_scale_of(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+
+// Two values -> their e4m3 codes, the first in the low byte; rounded to
+// nearest, ties to even.
+__device__ __forceinline__ uint32_t codes_of(float x0, float x1) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x1), "f"(x0));
+  return c;
+}
+
+// Two codes (the low or the high half of w) -> FP16 pair, exact.
+template <int kUpper>
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
+  uint32_t h;
+  if (kUpper)
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}"
+        : "=r"(h)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+        : "=r"(h)
+        : "r"(w));
+  return h;
+}
+
+// A row of 64 values held by 8 neighbouring lanes, 8 each: its exponent byte
+// and this lane's 8 codes. Called by a whole warp (four rows).
+__device__ __forceinline__ uint32_t quantise_row(float (&x)[8], uint2& codes) {
+  float most = 0.f;
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = within_range(x[i]);
+    most = fmaxf(most, fabsf(x[i]));                 // a NaN does not count
+  }
+  #pragma unroll
+  for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const uint32_t e = exponent_byte(most);
+  const float inv = inverse_scale_of(e);
+  codes.x = codes_of(x[0] * inv, x[1] * inv) | codes_of(x[2] * inv, x[3] * inv) << 16;
+  codes.y = codes_of(x[4] * inv, x[5] * inv) | codes_of(x[6] * inv, x[7] * inv) << 16;
+  return e;
+}
+
+// BF16 chunk -> 8 FP32 values, exact.
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// 8 dims of a row rotated: own = dims 8 c .., partner = the other half's (c ^ 4),
+// with the angles of pairs 8 (c % 4) ..; products and sum each rounded in FP32.
+__device__ __forceinline__ void rotate8(float (&x)[8], const float (&partner)[8], bool high,
+                                        const float (&cs)[8], const float (&sn)[8]) {
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = __fmul_rn(x[i], cs[i]), b = __fmul_rn(partner[i], sn[i]);
+    x[i] = high ? __fadd_rn(a, b) : __fsub_rn(a, b);
+  }
+}
+
+}  // namespace pkv_quant_dev
+
+#endif  // PKV_QUANT_CUH
