@@ -127,8 +127,9 @@ typedef struct pkv_pool* pkv_pool_t;
  * handle owns only device scratch: the split-KV partials (two layer-parity
  * copies of max_batch x 32 x max_splits x (64 + 2) floats), one ticket
  * counter per (sequence, kv head) and parity, one layer counter per sequence
- * (pkv_append_attend_layers), 12 bytes per pool page (pkv_pages.h) and the
- * sticky error flag.
+ * (pkv_append_attend_layers), 12 bytes per pool page (pkv_pages.h), the parts of
+ * drafted trees' sums (pkv_tree.h; 128 x (64 + 2) floats for each of 4 parts per
+ * SM, about 20 MB) and the sticky error flag.
  * It does not own the pools, tables or tensors. A handle's launches share
  * that scratch, so they must be ordered in one stream (calls issued to
  * several streams at once need a handle each). Returns INVALID_ARG for a

@@ -38,7 +38,8 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_append", "pkv_decode_att
             "pkv_window_prefill_attention", "pkv_prefill_fill_axes", "pkv_copy_pages",
             "pkv_compact_pages", "pkv_sched_fork", "pkv_sched_held", "pkv_sched_release",
             "pkv_sched_compact", "pkv_quant_fill", "pkv_quant_read", "pkv_quant_attention",
-            "pkv_quant_append_attend", "pkv_status_string")
+            "pkv_quant_append_attend", "pkv_tree_attention", "pkv_tree_commit",
+            "pkv_status_string")
 
 
 class PkvError(RuntimeError):
@@ -68,6 +69,7 @@ class PoolConfig(ctypes.Structure):
 PKV_FLAG_PDL, PKV_FLAG_LONG_CONTEXT = 1, 2
 PKV_MAX_LONG_CONTEXT = 1048576
 PKV_MAX_AXES = 4
+PKV_MAX_TREE = 64              # drafted tokens of a sequence
 PKV_QUANT_TILE_BYTES = 2080    # a (page, kv head) tile of the 8-bit cache
 
 
@@ -151,6 +153,8 @@ def load(path: str = None):
     lib.pkv_quant_read.argtypes = [P, i, P, P, P, P, P, P, i, i, i, P]
     lib.pkv_quant_attention.argtypes = [P, i, P, P, P, P, P, i, i, P, P, i, i, i, P]
     lib.pkv_quant_append_attend.argtypes = [P, i, P, P, P, P, P, P, P, i, i, P, P, i, i, i, P]
+    lib.pkv_tree_attention.argtypes = [P, i, P, P, P, P, P, P, P, P, i, i, i, i, P]
+    lib.pkv_tree_commit.argtypes = [P, P, P, P, P, P, P, i, i, P]
     lib.pkv_status_string.argtypes = [i]
     lib.pkv_status_string.restype = ctypes.c_char_p
     for name in EXPORTED[:-1]:
@@ -196,7 +200,7 @@ _DTYPES = {"q": "bfloat16", "k": "bfloat16", "v": "bfloat16", "k_pool": "bfloat1
            "seq_lens": "int32", "cu_tokens": "int32", "start_pos": "int32", "out": "float32",
            "rope_cos": "float32", "rope_sin": "float32", "rope_positions": "int32",
            "q_out": "bfloat16", "src": "int32", "dst": "int32", "tokens": "int32",
-           "kv_pool": "uint8"}
+           "kv_pool": "uint8", "tree": "int64", "accepted": "int32", "counts": "int32"}
 
 
 def _ptrs(**tensors):
@@ -707,6 +711,41 @@ def pkv_quant_append_attend(pool: Pool, layer, q, k, v, kv_pool, block_tables, s
         _length(int(sinks)), *_rope_args(pool, rope, rope_positions, batch), batch,
         _int(int(num_splits)), _pool_stream(pool, stream))
     _check(st, "pkv_quant_append_attend")
+
+
+# ---------------------------------------------------------------- drafted trees
+def pkv_tree_attention(pool: Pool, layer, q, k_pool, v_pool, block_tables, cu_tokens, start_pos,
+                       tree, out, window, sinks=0, batch=None, total_tokens=None, stream=None):
+    """Attention of drafted tokens (q bf16 [T][32][64], out fp32) over their
+    sequences' committed tokens and the drafted ones that tree names: int64 [T],
+    bit j of row i = it sees its sequence's drafted token j."""
+    batch = _int(_batch(start_pos, batch))
+    total = int(q.shape[0]) if total_tokens is None else _int(int(total_tokens))
+    rows = total * NUM_Q_HEADS * HEAD_DIM
+    st = pool._lib.pkv_tree_attention(
+        pool.handle, _int(int(layer)), _arg(pool, "q", q, rows),
+        _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "cu_tokens", cu_tokens, batch + 1), _arg(pool, "start_pos", start_pos, batch),
+        _arg(pool, "tree", tree, total), _arg(pool, "out", out, rows), _length(int(window)),
+        _length(int(sinks)), batch, total, _pool_stream(pool, stream))
+    _check(st, "pkv_tree_attention")
+
+
+def pkv_tree_commit(pool: Pool, k_pool, v_pool, block_tables, start_pos, accepted, counts,
+                    batch=None, max_accepted=None, stream=None):
+    """Moves K and V of drafted token accepted[b][k] (int32 [B][max_accepted]) to
+    position start_pos[b] + k for every k < counts[b], in every layer."""
+    batch = _int(_batch(start_pos, batch))
+    most = int(accepted.shape[1]) if max_accepted is None else _int(int(max_accepted))
+    st = pool._lib.pkv_tree_commit(
+        pool.handle, _arg(pool, "k_pool", k_pool, pool.elements),
+        _arg(pool, "v_pool", v_pool, pool.elements),
+        _arg(pool, "block_tables", block_tables, pool.entries),
+        _arg(pool, "start_pos", start_pos, batch), _arg(pool, "accepted", accepted, batch * most),
+        _arg(pool, "counts", counts, batch), batch, most, _pool_stream(pool, stream))
+    _check(st, "pkv_tree_commit")
 
 
 # ---------------------------------------------------------------- admission scheduler (host)

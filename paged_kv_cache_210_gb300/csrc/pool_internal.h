@@ -37,6 +37,9 @@ struct pkv_pool {
                                     // allocation
   unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between
                                     // launches)
+  float* tree_part_o;               // [pkv_tree_slots][128][64] parts of drafted tokens' sums
+  float2* tree_part_ml;             // [pkv_tree_slots][128]
+  int* tree_part_len;               // [1 + max_batch]
   WindowResidency window;           // the windowed decode over BF16 pages
   WindowResidency quant;            // ... and over 8-bit pages
   std::atomic<bool> pages_written{false};   // the handle's last page or fill call (pkv_pages.h,
@@ -86,5 +89,8 @@ bool pkv_layers_setup(pkv_pool* pool);
 // window.cu, quant.cu: the windowed decode kernels' attributes and residency.
 bool pkv_window_setup(pkv_pool* pool);
 bool pkv_quant_setup(pkv_pool* pool);
+
+// tree.cu: parts of 128 rows whose sums one call may keep.
+size_t pkv_tree_slots(const pkv_pool* pool);
 
 #endif  // PKV_POOL_INTERNAL_H

@@ -1,6 +1,7 @@
-// Internal to libpkv: what the prefill attention kernels (prefill.cu,
-// window_prefill.cu) share: tensor copies, tensor memory, tcgen05 products
-// and their descriptors, and the host's tensor-map encoder.
+// Internal to libpkv: what the attention kernels on tcgen05 (prefill.cu,
+// window_prefill.cu, tree.cu) share: tensor copies, tensor memory, products and
+// their descriptors, the waits and rings of warps with different roles, and the
+// host's tensor-map encoder.
 #ifndef PKV_PREFILL_DEVICE_CUH
 #define PKV_PREFILL_DEVICE_CUH
 
@@ -143,6 +144,142 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool b_mn_major)
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
+
+// ---------------------------------------------------------------- warp roles
+// The lowest n bits of 32 (n clamped to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits32(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
+// Whether `x` holds, which is rare: the code under it is placed out of the
+// step loop's way.
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, 0); }
+
+// The rest of a bounded wait on an mbarrier phase that has not come yet; gives
+// up when the CTA does.
+static __device__ __noinline__ bool wait_longer(unsigned long long* bar, uint32_t parity,
+                                         volatile int* abort_flag) {
+  const long long start = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || clock64() - start > kWaitCycles) return false;
+  return true;
+}
+
+// One verdict per warp (what follows is warp-wide).
+__device__ __forceinline__ bool wait_phase(unsigned long long* bar, uint32_t parity,
+                                           volatile int* abort_flag) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) done = wait_longer(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, done);
+}
+
+// Whether a phase is complete, without waiting for it.
+__device__ __forceinline__ bool phase_done(unsigned long long* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// wait_phase after an early look at the phase: the barrier's own latency is
+// paid only where the look came too soon.
+__device__ __forceinline__ bool wait_phase_after(bool done, unsigned long long* bar,
+                                                 uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, done)) return true;
+  return wait_phase(bar, parity, abort_flag);
+}
+
+// Lane 0's arrival, predicated instead of branched around.
+__device__ __forceinline__ void arrive_lane0(unsigned long long* bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lane)
+      : "memory");
+}
+
+// One lane of a converged warp, always the same. The issuing warps run their
+// loops whole and only the tcgen05 instructions under this predicate, so the
+// operands stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The largest of three (the last two given as bits).
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;"
+      : "=f"(d)
+      : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  return max3(__uint_as_float(a), b, c);
+}
+
+// 16 consecutive columns, complete on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 64 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  #pragma unroll
+  for (int h = 0; h < 4; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[16 * h]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]),
+          "=r"(r[16 * h + 4]), "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]),
+          "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]), "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]),
+          "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]), "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+        : "r"(taddr + 16 * h));
+  // the registers are written once the wait returns: it takes them as operands
+  #pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t* x = r + 16 * h;
+    if (h == 0)
+      asm volatile("tcgen05.wait::ld.sync.aligned;"
+                   : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                     "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                     "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+    else
+      asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                        "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                        "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])::"memory");
+  }
+}
+
+// A step's place in a ring of stages, and how often the ring has gone round.
+template <int kStages>
+struct RingAt {
+  int stage = 0;
+  uint32_t round = 0;      // parity of the phase that the stage's barriers complete next
+  __device__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      round ^= 1u;
+    }
+  }
+};
 
 // ---------------------------------------------------------------- host
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
