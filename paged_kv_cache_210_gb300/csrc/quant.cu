@@ -21,15 +21,15 @@ using namespace pkv_quant_dev;
 namespace {
 
 // ---------------------------------------------------------------- page math
-// One page's products are warp-wide mma.sync m16n8k16 of FP16 operands.
-//   scores: S = Q K^T, rows 0..7 = the 4 heads' queries, their high parts in rows
-//           0..3 and their low ones in rows 4..7 (rows 8..15 zero), columns =
-//           tokens, two products' worth;
+// A warp takes two pages at a time. Their products are warp-wide mma.sync m16n8k16 of FP16 operands.
+//   scores: S = Q K^T, rows = the 4 heads' queries, their high parts in rows 0..3
+//           (again in 4..7) and with rotation their low ones in 8..11 (12..15),
+//           columns = 8 tokens;
 //   values: O^T += V^T P^T, rows = 16 dims, columns = the 4 heads' weights,
 //           high parts in columns 0..3 and low ones in 4..7, contraction over
-//           the 16 tokens: 4 products fill the instruction's whole shape.
+//           16 tokens: products that fill the instruction's whole shape.
 // The scores' accumulators are then P^T's operand fragments: lane (g, q) = (L /
-// 4, L % 4) holds head g % 4's tokens 2 q, 2 q + 1, 8 + 2 q and 9 + 2 q in both.
+// 4, L % 4) holds head g % 4's tokens 2 q, 2 q + 1 of every 8 in both.
 //
 // FP16 has 11 bits and a narrow range: a factor that needs 24 bits (a rotated
 // query, a weight) is the sum of two FP16 terms after a scaling by a power of
@@ -76,10 +76,14 @@ __device__ __forceinline__ float row_max(float x) {
 }
 
 struct QuantTiles {
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 3;
+  static constexpr int kStagePages = 2;
+  static constexpr int kParts = 1;
   static constexpr uint32_t kCopyBytes = kQuantTile;
+  static constexpr size_t kAlign = 128;
   struct alignas(16) Ring {
-    uint8_t tile[kStages][kQuantTile];
+    uint8_t tile[kStages][kStagePages][kQuantTile];
+    float2 scale[kStagePages * kPage];   // 2^ek, 2^ev of the group's tokens
   };
   struct Source {
     uint8_t* pool;               // [num_pages][8][kQuantTile]
@@ -87,7 +91,7 @@ struct QuantTiles {
   // Lane (g, q): head g % 4, dims 16 q .. + 15 as 8 pairs; `to_log2` takes the
   // products with the scaled query to the exponent's base-2 scores.
   struct Queries {
-    uint32_t a[8];
+    uint32_t a[8], l[8];       // high parts, and with rotation low ones
     float to_log2;
   };
   struct State {
@@ -121,12 +125,11 @@ struct QuantTiles {
   static __device__ __forceinline__ void prefetch(const Source&) {}
 
   // One bulk copy moves the whole tile.
-  static __device__ __forceinline__ void copy(Ring& ws, int stage, const Source& src, int part,
+  static __device__ __forceinline__ void copy(Ring& ws, int stage, int e, const Source& src, int,
                                               int kvh, int phys, unsigned long long* bar) {
-    if (part != 0) return;
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-        ::"r"(smem_u32(ws.tile[stage])),
+        ::"r"(smem_u32(ws.tile[stage][e])),
           "l"(src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile), "r"(kQuantTile),
           "r"(smem_u32(bar))
         : "memory");
@@ -134,18 +137,21 @@ struct QuantTiles {
 
   // V codes and exponents of tokens that do not count: zero.
   static __device__ __forceinline__ void hide_rows(Ring& ws, int stage, uint32_t seen, int lane) {
-    uint8_t* t = ws.tile[stage];
-    for (int idx = lane; idx < 4 * kPage; idx += 32)
-      if (!((seen >> (idx & (kPage - 1))) & 1u))
-        *reinterpret_cast<uint4*>(t + kCodeBytes + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
-    if (lane < kPage && !((seen >> lane) & 1u)) t[kVExp + lane] = 0;
+    #pragma unroll
+    for (int e = 0; e < kStagePages; ++e, seen >>= kPage) {
+      uint8_t* t = ws.tile[stage][e];
+      for (int idx = lane; idx < 4 * kPage; idx += 32)
+        if (!((seen >> (idx & (kPage - 1))) & 1u))
+          *reinterpret_cast<uint4*>(t + kCodeBytes + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+      if (lane < kPage && !((seen >> lane) & 1u)) t[kVExp + lane] = 0;
+    }
   }
 
   // The appended row (a 16-byte chunk per lane: K in lanes 0..7, V in 8..15):
   // rotated, quantised, into its slot of the pool and of the stage.
   template <bool kRope>
-  static __device__ __forceinline__ void put_row(Ring& ws, int stage, const Source& src, int kvh,
-                                                 int slot, int phys, bool to_pool, bool to_stage,
+  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int page, const Source& src,
+                                                 int kvh, int slot, int phys, bool to_pool, bool to_stage,
                                                  uint4 val, float ang_c, float ang_s, int lane) {
     const int c = lane & 7;
     float x[8];
@@ -171,7 +177,7 @@ struct QuantTiles {
       if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
     }
     if (to_stage) {
-      uint8_t* t = ws.tile[stage];
+      uint8_t* t = ws.tile[stage][page];
       *reinterpret_cast<uint2*>(t + at) = codes;
       if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
     }
@@ -217,50 +223,60 @@ struct QuantTiles {
     for (int i = 0; i < 8; ++i) {
       // without rotation the high parts are the queries (8 bits)
       const float x0 = x[2 * i] * scale, x1 = x[2 * i + 1] * scale;
-      q.a[i] = kRope ? half_terms(x0, x1, lane) : float2_to_half2(x0, x1);
+      q.a[i] = float2_to_half2(x0, x1);
+      q.l[i] = kRope ? float2_to_half2(rest_of_half<0>(x0, q.a[i]), rest_of_half<1>(x1, q.a[i]))
+                     : 0u;
     }
   }
 
-  // One page; bit t of `seen` = token t counts (at least one does). The scores
-  // of the others are dropped by select; their V rows and exponents are zero.
-  // Lanes L and L + 16 hold the same scores, maxima and sums.
+  // A group of pages; bit t of `seen` = token t counts (at least one does). The
+  // scores of the others are dropped by select; their V rows and exponents are
+  // zero. Lanes L and L + 16 hold the same scores, maxima and sums.
   template <bool kRope>
   static __device__ __forceinline__ void attend(Ring& ws, int stage, uint32_t seen, int lane,
                                                 const Queries& q, State& st) {
-    const uint8_t* t = ws.tile[stage];
+    constexpr int kTiles = 2 * kStagePages;          // of 8 tokens
     const int g8 = lane >> 2;
     const int qq = lane & 3;
-    float s[4], scale_v[4];
+    {
+      // a lane unpacks one token's exponents for all
+      const uint8_t* t = ws.tile[stage][lane / kPage];
+      ws.scale[lane] = make_float2(scale_of(t[kKExp + lane % kPage]),
+                                   scale_of(t[kVExp + lane % kPage]));
+    }
+    float2 s[kTiles], scale_v[kTiles];
+    float d[kTiles][4];
     #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const uint4 kw = *reinterpret_cast<const uint4*>(t + k_at(8 * nt + g8, 16 * qq));
+    for (int nt = 0; nt < kTiles; ++nt) {
+      const uint8_t* t = ws.tile[stage][nt / 2];
+      const uint4 kw = *reinterpret_cast<const uint4*>(t + k_at(8 * (nt % 2) + g8, 16 * qq));
       const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
       #pragma unroll
       for (int sl = 0; sl < 4; ++sl)
-        mma_f16(d, q.a[2 * sl], 0u, q.a[2 * sl + 1], 0u, codes_to_half2<0>(w[sl]),
-                codes_to_half2<1>(w[sl]));
-      if (kRope) {   // rows g and g + 4: the two parts of head g's query
-        d[0] += __shfl_xor_sync(0xffffffffu, d[0], 16);
-        d[1] += __shfl_xor_sync(0xffffffffu, d[1], 16);
-      }
-      const uint32_t ek = *reinterpret_cast<const uint16_t*>(t + kKExp + 8 * nt + 2 * qq);
-      const uint32_t ev = *reinterpret_cast<const uint16_t*>(t + kVExp + 8 * nt + 2 * qq);
-      s[2 * nt] = d[0] * scale_of(ek & 0xffu);
-      s[2 * nt + 1] = d[1] * scale_of(ek >> 8);
-      scale_v[2 * nt] = scale_of(ev & 0xffu);
-      scale_v[2 * nt + 1] = scale_of(ev >> 8);
+        mma_f16(d[nt], q.a[2 * sl], kRope ? q.l[2 * sl] : 0u, q.a[2 * sl + 1],
+                kRope ? q.l[2 * sl + 1] : 0u, codes_to_half2<0>(w[sl]), codes_to_half2<1>(w[sl]));
     }
-    if (seen != 0xffffu) {
+    __syncwarp();
+    #pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt) {
+      const float4 sc = *reinterpret_cast<const float4*>(&ws.scale[8 * nt + 2 * qq]);
+      float2 x = make_float2(d[nt][0], d[nt][1]);
+      // rows g and g + 8: the two parts of head g's query
+      if (kRope) x = __fadd2_rn(x, make_float2(d[nt][2], d[nt][3]));
+      s[nt] = __fmul2_rn(x, make_float2(sc.x, sc.z));
+      scale_v[nt] = make_float2(sc.y, sc.w);
+    }
+    if (seen != 0xffffffffu) {
       #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = 8 * (i >> 1) + 2 * qq + (i & 1);
-        if (!((seen >> tok) & 1u)) s[i] = -INFINITY;
+      for (int nt = 0; nt < kTiles; ++nt) {
+        if (!((seen >> (8 * nt + 2 * qq)) & 1u)) s[nt].x = -INFINITY;
+        if (!((seen >> (8 * nt + 2 * qq + 1)) & 1u)) s[nt].y = -INFINITY;
       }
     }
     // p stays within 1: the exponent it is taken against moves 8 above the
     // row's maximum whenever that passes it
-    const float lane_top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) * q.to_log2;
+    const float lane_top = largest(s) * q.to_log2;
     if (__any_sync(0xffffffffu, lane_top > st.m_run)) {
       const float top = row_max(lane_top);
       float alpha = 1.f;
@@ -272,14 +288,17 @@ struct QuantTiles {
       st.rescale(alpha, lane);
     }
     const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
-    float p[4], w[4];
+    const float2 to_log2 = make_float2(q.to_log2, q.to_log2), minus = make_float2(-mu, -mu);
+    float2 w[kTiles], sum = make_float2(0.f, 0.f);
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[i] = fast_exp2(fmaf(s[i], q.to_log2, -mu));
-      w[i] = p[i] * scale_v[i];
+    for (int nt = 0; nt < kTiles; ++nt) {
+      const float2 x = __ffma2_rn(s[nt], to_log2, minus);
+      const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      sum = __fadd2_rn(sum, p);
+      w[nt] = __fmul2_rn(p, scale_v[nt]);
     }
-    st.l_run += (p[0] + p[1]) + (p[2] + p[3]);
-    const float lane_most = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3]));
+    st.l_run += sum.x + sum.y;
+    const float lane_most = largest(w);
     if (__any_sync(0xffffffffu, lane_most * st.unit > 32768.f)) {
       const float most = row_max(lane_most);
       float factor = 1.f;
@@ -291,30 +310,49 @@ struct QuantTiles {
       }
       st.rescale(factor, lane);
     }
-    uint32_t pb[2];
+    const float2 unit = make_float2(st.unit, st.unit);
+    uint32_t pb[kTiles];
     #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      pb[h] = half_terms(w[2 * h] * st.unit, w[2 * h + 1] * st.unit, lane);
+    for (int nt = 0; nt < kTiles; ++nt) {
+      const float2 x = __fmul2_rn(w[nt], unit);
+      pb[nt] = half_terms(x.x, x.y, lane);
+    }
     // lane L addresses token L % 16 of chunk 2 j (lanes 0..15) or 2 j + 1: a
     // transposed matrix of 16-bit pairs, dims 2 g and 2 g + 1 of tokens 2 q, 2 q + 1
-    const uint32_t vrow = smem_u32(t) + kCodeBytes + lane * 16;
     #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      uint32_t v[4];
-      ldsm_x4_trans(v, vrow + 2 * j * kChunkBytes);
+      // from zero, and added up in FP32: a tensor-core sum drops the bits below
+      // its accumulator's last one, always downwards
+      float o[2][4] = {};
+      #pragma unroll
+      for (int e = 0; e < kStagePages; ++e) {
+        uint32_t v[4];
+        ldsm_x4_trans(v, smem_u32(ws.tile[stage][e]) + kCodeBytes + lane * 16 + 2 * j * kChunkBytes);
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = __byte_perm(v[2 * h], 0u, 0x3120);       // tokens 0..7
+          const uint32_t hi = __byte_perm(v[2 * h + 1], 0u, 0x3120);   // tokens 8..15
+          mma_f16(o[h], codes_to_half2<0>(lo), codes_to_half2<1>(lo), codes_to_half2<0>(hi),
+                  codes_to_half2<1>(hi), pb[2 * e], pb[2 * e + 1]);
+        }
+      }
       #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __byte_perm(v[2 * h], 0u, 0x3120);       // tokens 0..7
-        const uint32_t hi = __byte_perm(v[2 * h + 1], 0u, 0x3120);   // tokens 8..15
-        // from zero, and added up in FP32: a tensor-core sum drops the bits
-        // below its accumulator's last one, always downwards
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, codes_to_half2<0>(lo), codes_to_half2<1>(lo), codes_to_half2<0>(hi),
-                codes_to_half2<1>(hi), pb[0], pb[1]);
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[2 * j + h][e] += d[e];
+        float* sum_o = st.o[2 * j + h];
+        const float2 a = __fadd2_rn(make_float2(sum_o[0], sum_o[1]), make_float2(o[h][0], o[h][1]));
+        const float2 b = __fadd2_rn(make_float2(sum_o[2], sum_o[3]), make_float2(o[h][2], o[h][3]));
+        sum_o[0] = a.x;
+        sum_o[1] = a.y;
+        sum_o[2] = b.x;
+        sum_o[3] = b.y;
       }
     }
+  }
+  static __device__ __forceinline__ float largest(const float2 (&x)[2 * kStagePages]) {
+    float m = fmaxf(x[0].x, x[0].y);
+    #pragma unroll
+    for (int i = 1; i < 2 * kStagePages; ++i) m = fmaxf(fmaxf(m, x[i].x), x[i].y);
+    return m;
   }
 
   // The warp's part for the block merge.

@@ -197,7 +197,10 @@ __device__ __forceinline__ void attend_page(const uint8_t* kt, const uint8_t* vt
 // A page of one KV head: its K and V tiles, 2 KiB each.
 struct Bf16Tiles {
   static constexpr int kStages = 3;
+  static constexpr int kStagePages = 1;
+  static constexpr int kParts = 2;              // K and V
   static constexpr uint32_t kCopyBytes = 2 * kTileBytes;
+  static constexpr size_t kAlign = 1024;        // swizzled tiles
   using Ring = PageRing<kStages>;
   using State = PageState;
   struct Source {
@@ -215,7 +218,7 @@ struct Bf16Tiles {
     prefetch_tensormap(&src.k);
     prefetch_tensormap(&src.v);
   }
-  static __device__ __forceinline__ void copy(Ring& ws, int stage, const Source& src, int part,
+  static __device__ __forceinline__ void copy(Ring& ws, int stage, int, const Source& src, int part,
                                               int kvh, int phys, unsigned long long* bar) {
     tma_load_tile(part == 0 ? ws.k[stage] : ws.v[stage], part == 0 ? &src.k : &src.v,
                   kvh * kPage, phys, bar);
@@ -229,7 +232,7 @@ struct Bf16Tiles {
   // The appended row (a 16-byte chunk per lane: K in lanes 0..7, V in 8..15):
   // rotated, into its slot of the pool and of the stage.
   template <bool kRope>
-  static __device__ __forceinline__ void put_row(Ring& ws, int stage, const Source& src, int kvh,
+  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int, const Source& src, int kvh,
                                                  int slot, int phys, bool to_pool, bool to_stage,
                                                  uint4 val, float ang_c, float ang_s, int lane) {
     const int c = lane & 7;

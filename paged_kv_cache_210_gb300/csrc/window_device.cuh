@@ -52,7 +52,7 @@ struct UnitSearch {
 };
 
 template <class Tiles>
-struct alignas(1024) WindowSmem {
+struct alignas(Tiles::kAlign) WindowSmem {
   typename Tiles::Ring warp[kWarps];
   unsigned long long bar[kWarps][Tiles::kStages];
   float m[kWarps][kGroup];
@@ -340,6 +340,10 @@ __global__ void __launch_bounds__(kThreadsW, kCluster ? 3 : 4)
 window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
                      const WindowParams prm) {
   constexpr int kStages = Tiles::kStages;
+  constexpr int kPer = Tiles::kStagePages;      // pages of a stage: a group
+  constexpr int kParts = Tiles::kParts;         // copies of a page
+  static_assert(kPer == 1 || kParts == 1, "a group's valid pages are read off one vote");
+  static_assert(kStages * kPer * kParts <= 32, "one lane per copy of the prefetch");
   using Smem = WindowSmem<Tiles>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem_base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -420,28 +424,33 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   const bool active = split < n_splits;       // an idle cluster block only joins the merge
   const int page_begin = active ? split * chunk : 0;
   const int page_end = active ? min(n_seen, page_begin + chunk) : 0;
-  const int first = page_begin + warp;        // this warp's pages: first + 4 j, j < mine
-  const int mine = first < page_end ? (page_end - first + kWarps - 1) / kWarps : 0;
+  // This warp's pages: its page l is page page_begin + (kWarps j + warp) kPer + e
+  // of the sequence's, l = kPer j + e; groups j < mine, pages l < my_pages.
+  const int pages = page_end - page_begin;
+  const int rounds = pages / (kWarps * kPer);
+  const int my_pages =
+      rounds * kPer + min(max(pages - (rounds * kWarps + warp) * kPer, 0), kPer);
+  const int mine = (my_pages + kPer - 1) / kPer;
   const int new_slot = (len - 1) % kPage;     // slot of the appended token
-  // fused: which of this warp's pages is the sequence's last one
-  const int new_off = n_seen - 1 - first;
-  const int j_new = new_off >= 0 && new_off % kWarps == 0 && new_off / kWarps < mine
-                        ? new_off / kWarps
-                        : -1;
+  // the sequence's last page, if it is one of this warp's
+  const int new_off = n_seen - 1 - page_begin;
+  const bool has_new = new_off >= 0 && new_off < pages && new_off / kPer % kWarps == warp;
+  const int j_new = has_new ? new_off / (kPer * kWarps) : -1;
+  const int l_new = has_new ? j_new * kPer + new_off % kPer : -1;
 
   const int32_t* row = prm.table + static_cast<size_t>(b) * prm.table_stride;
-  auto logical = [&](int j) {
-    const int i = first + kWarps * j;
+  auto logical = [&](int l) {
+    const int i = page_begin + (l / kPer * kWarps + warp) * kPer + l % kPer;
     return i < sink_pages ? i : i - sink_pages + win_page;
   };
   // Physical ids of 32 of this warp's pages, one per lane; the next 32 are
   // fetched while these are in use.
   auto fetch_ids = [&](int base) {
-    const int j = base + lane;
-    return j < mine ? __ldg(row + logical(j)) : -1;
+    const int l = base + lane;
+    return l < my_pages ? __ldg(row + logical(l)) : -1;
   };
   int ids = fetch_ids(0);
-  int ids_next = mine > 32 ? fetch_ids(32) : -1;
+  int ids_next = my_pages > 32 ? fetch_ids(32) : -1;
   auto good_id = [&](int phys) { return phys >= 0 && phys < prm.num_pages; };
   float ang_c = 1.f, ang_s = 0.f;                        // the angle of pair `lane`
   if (kRope && !load_pair_angle(prm.rope, rope_pos, lane, ang_c, ang_s)) {
@@ -453,19 +462,30 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   if (kCluster && n_splits > 1) async_inbox_setup(inbox);
   __syncwarp();
 
-  // Copy engine: page j's tile into `stage`, its two parts from lanes 0 and 1.
-  // A page whose only token is the appended one (fused) is not copied.
-  uint32_t stage_ok = 0;                      // bit s: stage s holds a valid page
-  auto issue_copy = [&](int j, int stage, int phys) {
+  // Copy engine: the pages of group j into `stage`, one copy per lane. A page
+  // whose only token is the appended one (fused) is not copied.
+  uint32_t stage_ok = 0;                      // bit kPer s + e: stage s holds a valid page e
+  auto issue_copy = [&](int j, int stage) {
+    const int e = kPer == 1 ? 0 : min(lane, kPer - 1);
+    const int l = j * kPer + e;
+    const int phys = __shfl_sync(0xffffffffu, ids, l & 31);
+    const bool serves = lane < kPer * kParts && l < my_pages;
     const bool ok = good_id(phys);
-    stage_ok = ok ? stage_ok | (1u << stage) : stage_ok & ~(1u << stage);
-    if (lane > 1) return;
-    const bool rows = !(kFused && j == j_new && new_slot == 0);
-    if (!ok && lane == 0) set_error(prm.err, kErrPage);
-    if (ok && rows) {
-      if (lane == 0) mbar_arrive_expect_tx(&bars[stage], Tiles::kCopyBytes);
-      __syncwarp(0x3u);   // the expected bytes are set before either copy can land
-      Tiles::copy(ws, stage, src, lane, kvh, phys, &bars[stage]);
+    const bool rows = !(kFused && l == l_new && new_slot == 0);
+    uint32_t valid = ok ? 1u : 0u, copied = ok && rows ? 1u : 0u;
+    if constexpr (kPer > 1) {
+      valid = __ballot_sync(0xffffffffu, serves && ok);
+      copied = __ballot_sync(0xffffffffu, serves && ok && rows);
+    }
+    stage_ok = (stage_ok & ~(((1u << kPer) - 1u) << (kPer * stage))) | valid << (kPer * stage);
+    if (lane >= kPer * kParts) return;
+    if (serves && !ok && lane % kParts == 0) set_error(prm.err, kErrPage);
+    if (copied) {
+      if (lane == 0) mbar_arrive_expect_tx(&bars[stage], __popc(copied) * Tiles::kCopyBytes);
+      // the expected bytes are set before any copy can land
+      __syncwarp((1u << (kPer * kParts)) - 1u);
+      if (serves && ok && rows)
+        Tiles::copy(ws, stage, e, src, lane % kParts, kvh, phys, &bars[stage]);
     } else if (lane == 0) {
       mbar_arrive(&bars[stage]);
     }
@@ -482,38 +502,41 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
           (static_cast<size_t>(b) * kHkv + kvh) * kDim + (lane & 7) * 8));
     return val;
   };
-  // Prefetch: the first pages' tiles at once, lanes 2 j and 2 j + 1 serving the
-  // parts of page j. The unfused kernel defers the last page,
-  // whose newest row the kernel before this one may be writing.
+  // Prefetch: the first groups' tiles at once, a lane per copy. The unfused
+  // kernel defers the last page's group, whose newest row the kernel before this
+  // one may be writing.
   const int n_prefetch = min(mine, kStages);
   const bool deferred = !kFused && j_new >= 0 && j_new < n_prefetch;
   {
-    const int j = lane >> 1;
-    const int phys = __shfl_sync(0xffffffffu, ids, j);
+    const int l = lane / kParts;
+    const int j = l / kPer;
+    const int phys = __shfl_sync(0xffffffffu, ids, l);
     const bool ok = good_id(phys);
-    const bool serves = j < n_prefetch && (kFused || j != j_new);
-    const bool rows = !(kFused && j == j_new && new_slot == 0);
-    stage_ok = __ballot_sync(0xffffffffu, lane < n_prefetch && good_id(ids)) &
-               ((1u << kStages) - 1u);
-    if (serves && (lane & 1) == 0) {
-      if (!ok) set_error(prm.err, kErrPage);
-      if (ok && rows) {
-        mbar_arrive_expect_tx(&bars[j], Tiles::kCopyBytes);
+    const bool serves = j < n_prefetch && l < my_pages && (kFused || j != j_new);
+    const bool copies = serves && ok && !(kFused && l == l_new && new_slot == 0);
+    stage_ok = __ballot_sync(0xffffffffu, lane < min(my_pages, kStages * kPer) && good_id(ids));
+    const uint32_t all = __ballot_sync(0xffffffffu, copies && lane % kParts == 0);
+    if (serves && lane % kParts == 0 && !ok) set_error(prm.err, kErrPage);
+    if (j < n_prefetch && (kFused || j != j_new) && lane % (kPer * kParts) == 0) {
+      const int n = __popc(all >> lane & ((1u << (kPer * kParts)) - 1u));
+      if (n > 0) {
+        mbar_arrive_expect_tx(&bars[j], n * Tiles::kCopyBytes);
       } else {
         mbar_arrive(&bars[j]);
       }
     }
     __syncwarp();
-    if (serves && ok && rows) Tiles::copy(ws, j, src, lane & 1, kvh, phys, &bars[j]);
+    if (copies) Tiles::copy(ws, j, l % kPer, src, lane % kParts, kvh, phys, &bars[j]);
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (deferred) issue_copy(j_new, j_new, __shfl_sync(0xffffffffu, ids, j_new));
+  if (deferred) issue_copy(j_new, j_new);
   // the new row's load goes out before the queries', so their latencies overlap
   uint4 new_row = make_uint4(0u, 0u, 0u, 0u);
   if (kFused && j_new >= 0) new_row = load_new_row();
-  int new_page = kFused && j_new >= 0 && j_new < n_prefetch ? __shfl_sync(0xffffffffu, ids, j_new)
-                                                            : -1;
+  int new_page = kFused && j_new >= 0 && j_new < n_prefetch
+                     ? __shfl_sync(0xffffffffu, ids, l_new & 31)
+                     : -1;
   typename Tiles::Queries queries;
   Tiles::template load_queries<kRope>(
       prm.q + (static_cast<size_t>(b) * kHq + kvh * kGroup) * kDim, lane, ang_c, ang_s, queries);
@@ -531,21 +554,29 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
       break;
     }
     consumed = j + 1;
-    const int t0 = logical(j) * kPage;
-    uint32_t seen = 0xffffu;
-    // a page inside the window, or one of sinks alone, is seen whole
-    if (t0 + kPage > len || t0 < win_lo)
-      seen = low_bits(len - t0) & (low_bits(prm.sinks - t0) | (0xffffu & ~low_bits(win_lo - t0)));
-    if (!((stage_ok >> stage) & 1u)) seen = 0;
+    uint32_t seen = 0;                         // 16 bits a page
+    #pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int l = j * kPer + e;
+      const int t0 = logical(l) * kPage;
+      uint32_t bits = 0xffffu;
+      // a page inside the window, or one of sinks alone, is seen whole
+      if (t0 + kPage > len || t0 < win_lo)
+        bits = low_bits(len - t0) & (low_bits(prm.sinks - t0) | (0xffffu & ~low_bits(win_lo - t0)));
+      if (!((stage_ok >> (kPer * stage + e)) & 1u)) bits = 0;
+      seen |= bits << (kPage * e);
+    }
     const bool with_new = kFused && j == j_new;
-    if (seen != 0xffffu || with_new) {
+    if (seen != 0xffffffffu >> (32 - kPage * kPer) || with_new) {
       // V rows that do not count are zeroed (0 times what they hold must stay
       // 0), and the appended row goes over what the copy brought
       Tiles::hide_rows(ws, stage, seen, lane);
       __syncwarp();
       if (with_new)
-        Tiles::template put_row<kRope>(ws, stage, src, kvh, new_slot, new_page,
-                                       good_id(new_page), seen != 0, new_row, ang_c, ang_s, lane);
+        Tiles::template put_row<kRope>(ws, stage, l_new % kPer, src, kvh, new_slot, new_page,
+                                       good_id(new_page),
+                                       (seen >> (l_new % kPer * kPage) & 0xffffu) != 0, new_row,
+                                       ang_c, ang_s, lane);
       fence_proxy_async_smem();
       __syncwarp();
     }
@@ -553,13 +584,12 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
     __syncwarp();   // every lane's reads of the stage are done before it is refilled
     const int next = j + kStages;
     if (next < mine) {
-      if ((next & 31) == 0) {
+      if ((next * kPer & 31) == 0) {
         ids = ids_next;
-        ids_next = fetch_ids(next + 32);
+        ids_next = fetch_ids(next * kPer + 32);
       }
-      const int phys = __shfl_sync(0xffffffffu, ids, next & 31);
-      issue_copy(next, stage, phys);
-      if (kFused && next == j_new) new_page = phys;
+      issue_copy(next, stage);
+      if (kFused && next == j_new) new_page = __shfl_sync(0xffffffffu, ids, l_new & 31);
       issued = next + 1;
     }
     if (++stage == kStages) {
