@@ -51,22 +51,27 @@ __device__ __forceinline__ uint32_t float2_to_half2(float e0, float e1) {
   return w;
 }
 
-// x - (an FP16 half of the pair h), exact where h holds x rounded.
+// x + m (an FP16 half of the pair h), m an FP16 number: with m = -1 what h, x
+// rounded, leaves of x, exactly.
 template <int kUpper>
-__device__ __forceinline__ float rest_of_half(float x, uint32_t h) {
-  float f;
+__device__ __forceinline__ float plus_half(float x, uint32_t h, uint16_t m) {
+  float d;
   if (kUpper)
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, u;\n\t}" : "=f"(f) : "r"(h));
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tfma.rn.f32.f16 %0, u, %2, %3;\n\t}"
+        : "=f"(d)
+        : "r"(h), "h"(m), "f"(x));
   else
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-  return x - f;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tfma.rn.f32.f16 %0, l, %2, %3;\n\t}"
+        : "=f"(d)
+        : "r"(h), "h"(m), "f"(x));
+  return d;
 }
+constexpr uint16_t kMinusOne = 0xbc00;
 
-// The high parts (lanes 0..15) or the low ones (16..31) of two values.
-__device__ __forceinline__ uint32_t half_terms(float x0, float x1, int lane) {
+// The high parts (m = 0) or the low ones (m = -1) of two values.
+__device__ __forceinline__ uint32_t half_terms(float x0, float x1, uint16_t m) {
   const uint32_t hi = float2_to_half2(x0, x1);
-  const uint32_t lo = float2_to_half2(rest_of_half<0>(x0, hi), rest_of_half<1>(x1, hi));
-  return lane < 16 ? hi : lo;
+  return float2_to_half2(plus_half<0>(x0, hi, m), plus_half<1>(x1, hi, m));
 }
 
 // Largest over the four lanes of a row.
@@ -224,8 +229,7 @@ struct QuantTiles {
       // without rotation the high parts are the queries (8 bits)
       const float x0 = x[2 * i] * scale, x1 = x[2 * i + 1] * scale;
       q.a[i] = float2_to_half2(x0, x1);
-      q.l[i] = kRope ? float2_to_half2(rest_of_half<0>(x0, q.a[i]), rest_of_half<1>(x1, q.a[i]))
-                     : 0u;
+      q.l[i] = kRope ? half_terms(x0, x1, kMinusOne) : 0u;
     }
   }
 
@@ -311,11 +315,12 @@ struct QuantTiles {
       st.rescale(factor, lane);
     }
     const float2 unit = make_float2(st.unit, st.unit);
+    const uint16_t part = lane < 16 ? 0 : kMinusOne;   // high parts in lanes 0..15
     uint32_t pb[kTiles];
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
       const float2 x = __fmul2_rn(w[nt], unit);
-      pb[nt] = half_terms(x.x, x.y, lane);
+      pb[nt] = half_terms(x.x, x.y, part);
     }
     // lane L addresses token L % 16 of chunk 2 j (lanes 0..15) or 2 j + 1: a
     // transposed matrix of 16-bit pairs, dims 2 g and 2 g + 1 of tokens 2 q, 2 q + 1

@@ -465,26 +465,27 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   // Copy engine: the pages of group j into `stage`, one copy per lane. A page
   // whose only token is the appended one (fused) is not copied.
   uint32_t stage_ok = 0;                      // bit kPer s + e: stage s holds a valid page e
+  bool some_bad = false;                      // some page had an invalid id
   auto issue_copy = [&](int j, int stage) {
-    const int e = kPer == 1 ? 0 : min(lane, kPer - 1);
-    const int l = j * kPer + e;
-    const int phys = __shfl_sync(0xffffffffu, ids, l & 31);
-    const bool serves = lane < kPer * kParts && l < my_pages;
+    constexpr uint32_t kGroup1 = (1u << kPer) - 1u;
+    const int l0 = j * kPer;
+    const int there = min(my_pages - l0, kPer);
+    const int e = kPer == 1 ? 0 : lane;
+    const int phys = __shfl_sync(0xffffffffu, ids, (l0 + e) & 31);
     const bool ok = good_id(phys);
-    const bool rows = !(kFused && l == l_new && new_slot == 0);
-    uint32_t valid = ok ? 1u : 0u, copied = ok && rows ? 1u : 0u;
-    if constexpr (kPer > 1) {
-      valid = __ballot_sync(0xffffffffu, serves && ok);
-      copied = __ballot_sync(0xffffffffu, serves && ok && rows);
-    }
-    stage_ok = (stage_ok & ~(((1u << kPer) - 1u) << (kPer * stage))) | valid << (kPer * stage);
+    const uint32_t valid = kPer == 1 ? ok : __ballot_sync(0xffffffffu, e < there && ok);
+    stage_ok = (stage_ok & ~(kGroup1 << (kPer * stage))) | valid << (kPer * stage);
+    uint32_t copied = valid;
+    if (kFused && j == j_new && new_slot == 0) copied &= ~(1u << (l_new - l0));
+    const bool bad = valid != (1u << there) - 1u;
+    some_bad |= bad;
+    if (bad && lane == 0) set_error(prm.err, kErrPage);
     if (lane >= kPer * kParts) return;
-    if (serves && !ok && lane % kParts == 0) set_error(prm.err, kErrPage);
     if (copied) {
       if (lane == 0) mbar_arrive_expect_tx(&bars[stage], __popc(copied) * Tiles::kCopyBytes);
       // the expected bytes are set before any copy can land
       __syncwarp((1u << (kPer * kParts)) - 1u);
-      if (serves && ok && rows)
+      if (kPer == 1 || (copied >> e & 1u))
         Tiles::copy(ws, stage, e, src, lane % kParts, kvh, phys, &bars[stage]);
     } else if (lane == 0) {
       mbar_arrive(&bars[stage]);
@@ -514,7 +515,9 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
     const bool ok = good_id(phys);
     const bool serves = j < n_prefetch && l < my_pages && (kFused || j != j_new);
     const bool copies = serves && ok && !(kFused && l == l_new && new_slot == 0);
-    stage_ok = __ballot_sync(0xffffffffu, lane < min(my_pages, kStages * kPer) && good_id(ids));
+    const int held = min(my_pages, kStages * kPer);
+    stage_ok = __ballot_sync(0xffffffffu, lane < held && good_id(ids));
+    some_bad = stage_ok != (1u << held) - 1u;
     const uint32_t all = __ballot_sync(0xffffffffu, copies && lane % kParts == 0);
     if (serves && lane % kParts == 0 && !ok) set_error(prm.err, kErrPage);
     if (j < n_prefetch && (kFused || j != j_new) && lane % (kPer * kParts) == 0) {
@@ -543,31 +546,40 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
 
   typename Tiles::State st;
   st.reset();
+  // Groups seen whole: all their pages are there, inside the window (and valid);
+  // the first one is one of the sequence's [whole_from, whole_from + whole).
+  const int whole_from = sink_pages + (win_lo % kPage != 0 ? 1 : 0);
+  const unsigned whole = max(min(len / kPage - win_page + sink_pages, page_end) - kPer + 1 - whole_from, 0);
+  int at = page_begin + warp * kPer;          // the group's first page
   int issued = n_prefetch;
   int consumed = 0;
   bool timed_out = false;
   int stage = 0;
   uint32_t phase = 0;
-  for (int j = 0; j < mine; ++j) {
+  for (int j = 0; j < mine; ++j, at += kWarps * kPer) {
     if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], phase))) {
       timed_out = true;
       break;
     }
     consumed = j + 1;
-    uint32_t seen = 0;                         // 16 bits a page
-    #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int l = j * kPer + e;
-      const int t0 = logical(l) * kPage;
-      uint32_t bits = 0xffffu;
-      // a page inside the window, or one of sinks alone, is seen whole
-      if (t0 + kPage > len || t0 < win_lo)
-        bits = low_bits(len - t0) & (low_bits(prm.sinks - t0) | (0xffffu & ~low_bits(win_lo - t0)));
-      if (!((stage_ok >> (kPer * stage + e)) & 1u)) bits = 0;
-      seen |= bits << (kPage * e);
-    }
+    constexpr uint32_t kAll = 0xffffffffu >> (32 - kPage * kPer);   // 16 bits a page
+    uint32_t seen = kAll;
     const bool with_new = kFused && j == j_new;
-    if (seen != 0xffffffffu >> (32 - kPage * kPer) || with_new) {
+    if (static_cast<unsigned>(at - whole_from) >= whole || some_bad || with_new) {
+      seen = 0;
+      #pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int t0 = logical(j * kPer + e) * kPage;
+        uint32_t bits = 0xffffu;
+        // a page inside the window, or one of sinks alone, is seen whole
+        if (t0 + kPage > len || t0 < win_lo)
+          bits = low_bits(len - t0) &
+                 (low_bits(prm.sinks - t0) | (0xffffu & ~low_bits(win_lo - t0)));
+        if (!((stage_ok >> (kPer * stage + e)) & 1u)) bits = 0;
+        seen |= bits << (kPage * e);
+      }
+    }
+    if (seen != kAll || with_new) {
       // V rows that do not count are zeroed (0 times what they hold must stay
       // 0), and the appended row goes over what the copy brought
       Tiles::hide_rows(ws, stage, seen, lane);
