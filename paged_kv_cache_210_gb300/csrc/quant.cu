@@ -233,42 +233,57 @@ struct QuantTiles {
     }
   }
 
-  // A group of pages; bit t of `seen` = token t counts (at least one does). The
-  // scores of the others are dropped by select; their V rows and exponents are
-  // zero. Lanes L and L + 16 hold the same scores, maxima and sums.
+  static constexpr int kTiles = 2 * kStagePages;     // of 8 tokens
+  // Lane (g, q): products of head g % 4 with tokens 8 nt + 2 q, + 1.
+  struct Scores {
+    float2 s[kTiles];
+  };
+  // Their weights p 2^ev as FP16 pairs, high or low parts.
+  struct Weights {
+    uint32_t p[kTiles];
+  };
+
+  // A group's products with the queries, and its exponents unpacked, a token per
+  // lane, for all.
   template <bool kRope>
-  static __device__ __forceinline__ void attend(Ring& ws, int stage, uint32_t seen, int lane,
-                                                const Queries& q, State& st) {
-    constexpr int kTiles = 2 * kStagePages;          // of 8 tokens
+  static __device__ __forceinline__ void scores_of(Ring& ws, int stage, int lane,
+                                                   const Queries& q, Scores& out) {
     const int g8 = lane >> 2;
     const int qq = lane & 3;
-    {
-      // a lane unpacks one token's exponents for all
-      const uint8_t* t = ws.tile[stage][lane / kPage];
-      ws.scale[lane] = make_float2(scale_of(t[kKExp + lane % kPage]),
-                                   scale_of(t[kVExp + lane % kPage]));
-    }
-    float2 s[kTiles], scale_v[kTiles];
-    float d[kTiles][4];
+    const uint8_t* own = ws.tile[stage][lane / kPage];
+    const uint32_t ek = own[kKExp + lane % kPage], ev = own[kVExp + lane % kPage];
+    uint4 kw[kTiles];
+    #pragma unroll
+    for (int nt = 0; nt < kTiles; ++nt)
+      kw[nt] = *reinterpret_cast<const uint4*>(ws.tile[stage][nt / 2] +
+                                               k_at(8 * (nt % 2) + g8, 16 * qq));
+    ws.scale[lane] = make_float2(scale_of(ek), scale_of(ev));
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
-      const uint8_t* t = ws.tile[stage][nt / 2];
-      const uint4 kw = *reinterpret_cast<const uint4*>(t + k_at(8 * (nt % 2) + g8, 16 * qq));
-      const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
-      d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+      const uint32_t w[4] = {kw[nt].x, kw[nt].y, kw[nt].z, kw[nt].w};
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
       #pragma unroll
       for (int sl = 0; sl < 4; ++sl)
-        mma_f16(d[nt], q.a[2 * sl], kRope ? q.l[2 * sl] : 0u, q.a[2 * sl + 1],
+        mma_f16(d, q.a[2 * sl], kRope ? q.l[2 * sl] : 0u, q.a[2 * sl + 1],
                 kRope ? q.l[2 * sl + 1] : 0u, codes_to_half2<0>(w[sl]), codes_to_half2<1>(w[sl]));
+      out.s[nt] = make_float2(d[0], d[1]);
+      // rows g and g + 8: the two parts of head g's query
+      if (kRope) out.s[nt] = __fadd2_rn(out.s[nt], make_float2(d[2], d[3]));
     }
-    __syncwarp();
+  }
+
+  // The group's weights; bit t of `seen` = token t counts. The scores of the
+  // others are dropped by select; their V rows and exponents are zero. Lanes L and
+  // L + 16 hold the same scores, maxima and sums.
+  static __device__ __forceinline__ Weights weights_of(const Ring& ws, uint32_t seen, int lane,
+                                                       const Queries& q, const Scores& in,
+                                                       State& st) {
+    const int qq = lane & 3;
+    float2 s[kTiles], scale_v[kTiles], w[kTiles], sum;
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
       const float4 sc = *reinterpret_cast<const float4*>(&ws.scale[8 * nt + 2 * qq]);
-      float2 x = make_float2(d[nt][0], d[nt][1]);
-      // rows g and g + 8: the two parts of head g's query
-      if (kRope) x = __fadd2_rn(x, make_float2(d[nt][2], d[nt][3]));
-      s[nt] = __fmul2_rn(x, make_float2(sc.x, sc.z));
+      s[nt] = __fmul2_rn(in.s[nt], make_float2(sc.x, sc.z));
       scale_v[nt] = make_float2(sc.y, sc.w);
     }
     if (seen != 0xffffffffu) {
@@ -278,52 +293,59 @@ struct QuantTiles {
         if (!((seen >> (8 * nt + 2 * qq + 1)) & 1u)) s[nt].y = -INFINITY;
       }
     }
-    // p stays within 1: the exponent it is taken against moves 8 above the
-    // row's maximum whenever that passes it
-    const float lane_top = largest(s) * q.to_log2;
-    if (__any_sync(0xffffffffu, lane_top > st.m_run)) {
-      const float top = row_max(lane_top);
-      float alpha = 1.f;
-      if (top > st.m_run) {
-        alpha = fast_exp2(st.m_run - (top + kRescaleLog2));   // 0 on the first page
-        st.m_run = top + kRescaleLog2;
-        st.l_run *= alpha;
+    const float2 to_log2 = make_float2(q.to_log2, q.to_log2);
+    auto exponentials = [&]() {
+      const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
+      const float2 minus = make_float2(-mu, -mu);
+      sum = make_float2(0.f, 0.f);
+      #pragma unroll
+      for (int nt = 0; nt < kTiles; ++nt) {
+        const float2 x = __ffma2_rn(s[nt], to_log2, minus);
+        const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        sum = __fadd2_rn(sum, p);
+        w[nt] = __fmul2_rn(p, scale_v[nt]);
       }
-      st.rescale(alpha, lane);
-    }
-    const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
-    const float2 to_log2 = make_float2(q.to_log2, q.to_log2), minus = make_float2(-mu, -mu);
-    float2 w[kTiles], sum = make_float2(0.f, 0.f);
-    #pragma unroll
-    for (int nt = 0; nt < kTiles; ++nt) {
-      const float2 x = __ffma2_rn(s[nt], to_log2, minus);
-      const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      sum = __fadd2_rn(sum, p);
-      w[nt] = __fmul2_rn(p, scale_v[nt]);
-    }
-    st.l_run += sum.x + sum.y;
-    const float lane_most = largest(w);
-    if (__any_sync(0xffffffffu, lane_most * st.unit > 32768.f)) {
-      const float most = row_max(lane_most);
+    };
+    // Taken against the state as it is. Where a row's maximum passes the exponent
+    // that p is taken against (p would pass 1), that one moves to 8 above it; where
+    // its weighted rows pass 2^15 units, the unit moves. Both are rare.
+    const float lane_top = largest(s) * q.to_log2;
+    exponentials();
+    const float lane_most = largest(w) * st.unit;
+    if (__any_sync(0xffffffffu, lane_top > st.m_run || !(lane_most <= 32768.f))) {
+      const float top = row_max(lane_top);
       float factor = 1.f;
+      if (top > st.m_run) {
+        factor = fast_exp2(st.m_run - (top + kRescaleLog2));   // 0 on the first page
+        st.m_run = top + kRescaleLog2;
+        st.l_run *= factor;
+      }
+      exponentials();
+      const float most = row_max(largest(w));
       if (most * st.unit > 32768.f) {
         // 2^(7 - floor(log2 most)): the largest then lies in [2^7, 2^8)
         const float unit = scale_of(261u - (__float_as_uint(most) >> 23));
-        factor = unit * inverse_scale_of(__float_as_uint(st.unit) >> 23);
+        factor *= unit * inverse_scale_of(__float_as_uint(st.unit) >> 23);
         st.unit = unit;
       }
       st.rescale(factor, lane);
     }
+    st.l_run += sum.x + sum.y;
     const float2 unit = make_float2(st.unit, st.unit);
     const uint16_t part = lane < 16 ? 0 : kMinusOne;   // high parts in lanes 0..15
-    uint32_t pb[kTiles];
+    Weights out;
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
       const float2 x = __fmul2_rn(w[nt], unit);
-      pb[nt] = half_terms(x.x, x.y, part);
+      out.p[nt] = half_terms(x.x, x.y, part);
     }
-    // lane L addresses token L % 16 of chunk 2 j (lanes 0..15) or 2 j + 1: a
-    // transposed matrix of 16-bit pairs, dims 2 g and 2 g + 1 of tokens 2 q, 2 q + 1
+    return out;
+  }
+
+  // lane L addresses token L % 16 of chunk 2 j (lanes 0..15) or 2 j + 1: a
+  // transposed matrix of 16-bit pairs, dims 2 g and 2 g + 1 of tokens 2 q, 2 q + 1
+  static __device__ __forceinline__ void add_values(Ring& ws, int stage, int lane,
+                                                    const Weights& weights, State& st) {
     #pragma unroll
     for (int j = 0; j < 2; ++j) {
       // from zero, and added up in FP32: a tensor-core sum drops the bits below
@@ -338,7 +360,7 @@ struct QuantTiles {
           const uint32_t lo = __byte_perm(v[2 * h], 0u, 0x3120);       // tokens 0..7
           const uint32_t hi = __byte_perm(v[2 * h + 1], 0u, 0x3120);   // tokens 8..15
           mma_f16(o[h], codes_to_half2<0>(lo), codes_to_half2<1>(lo), codes_to_half2<0>(hi),
-                  codes_to_half2<1>(hi), pb[2 * e], pb[2 * e + 1]);
+                  codes_to_half2<1>(hi), weights.p[2 * e], weights.p[2 * e + 1]);
         }
       }
       #pragma unroll
@@ -353,10 +375,19 @@ struct QuantTiles {
       }
     }
   }
-  static __device__ __forceinline__ float largest(const float2 (&x)[2 * kStagePages]) {
+  // A group of pages; at least one token counts.
+  template <bool kRope>
+  static __device__ __forceinline__ void attend(Ring& ws, int stage, uint32_t seen, int lane,
+                                                const Queries& q, State& st) {
+    Scores scores;
+    scores_of<kRope>(ws, stage, lane, q, scores);
+    __syncwarp();
+    add_values(ws, stage, lane, weights_of(ws, seen, lane, q, scores, st), st);
+  }
+  static __device__ __forceinline__ float largest(const float2 (&x)[kTiles]) {
     float m = fmaxf(x[0].x, x[0].y);
     #pragma unroll
-    for (int i = 1; i < 2 * kStagePages; ++i) m = fmaxf(fmaxf(m, x[i].x), x[i].y);
+    for (int i = 1; i < kTiles; ++i) m = fmaxf(fmaxf(m, x[i].x), x[i].y);
     return m;
   }
 

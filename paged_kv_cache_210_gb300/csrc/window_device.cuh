@@ -556,13 +556,11 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   bool timed_out = false;
   int stage = 0;
   uint32_t phase = 0;
-  for (int j = 0; j < mine; ++j, at += kWarps * kPer) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], phase))) {
-      timed_out = true;
-      break;
-    }
-    consumed = j + 1;
-    constexpr uint32_t kAll = 0xffffffffu >> (32 - kPage * kPer);   // 16 bits a page
+  constexpr uint32_t kAll = 0xffffffffu >> (32 - kPage * kPer);   // 16 bits a page
+  // Group j has landed in `stage`: which of its tokens count. V rows that do not
+  // are cleared (0 times what they hold must stay 0), and the appended row goes
+  // over what the copy brought.
+  auto make_ready = [&](int j, int stage, int at) {
     uint32_t seen = kAll;
     const bool with_new = kFused && j == j_new;
     if (static_cast<unsigned>(at - whole_from) >= whole || some_bad || with_new) {
@@ -580,8 +578,6 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
       }
     }
     if (seen != kAll || with_new) {
-      // V rows that do not count are zeroed (0 times what they hold must stay
-      // 0), and the appended row goes over what the copy brought
       Tiles::hide_rows(ws, stage, seen, lane);
       __syncwarp();
       if (with_new)
@@ -592,18 +588,30 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
       fence_proxy_async_smem();
       __syncwarp();
     }
-    if (seen) Tiles::template attend<kRope>(ws, stage, seen, lane, queries, st);
-    __syncwarp();   // every lane's reads of the stage are done before it is refilled
+    return seen;
+  };
+  // Every lane's reads of the stage are done: the group after those in flight.
+  auto refill = [&](int j, int stage) {
     const int next = j + kStages;
-    if (next < mine) {
-      if ((next * kPer & 31) == 0) {
-        ids = ids_next;
-        ids_next = fetch_ids(next * kPer + 32);
-      }
-      issue_copy(next, stage);
-      if (kFused && next == j_new) new_page = __shfl_sync(0xffffffffu, ids, l_new & 31);
-      issued = next + 1;
+    if (next >= mine) return;
+    if ((next * kPer & 31) == 0) {
+      ids = ids_next;
+      ids_next = fetch_ids(next * kPer + 32);
     }
+    issue_copy(next, stage);
+    if (kFused && next == j_new) new_page = __shfl_sync(0xffffffffu, ids, l_new & 31);
+    issued = next + 1;
+  };
+  for (int j = 0; j < mine; ++j, at += kWarps * kPer) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], phase))) {
+      timed_out = true;
+      break;
+    }
+    consumed = j + 1;
+    const uint32_t seen = make_ready(j, stage, at);
+    if (seen) Tiles::template attend<kRope>(ws, stage, seen, lane, queries, st);
+    __syncwarp();
+    refill(j, stage);
     if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
