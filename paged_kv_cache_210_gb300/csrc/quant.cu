@@ -127,6 +127,19 @@ struct QuantTiles {
   };
 
   static const WindowResidency& residency(const pkv_pool* pool) { return pool->quant; }
+  // The largest of 16, 8 and 4 whose blocks are all resident at once. Measured (us),
+  // 2,048-token sequences: one, cluster of 16 4.7, of 12 5.2, of 8 4.9; 3, of 8 5.6,
+  // of 16 8.1; 6, of 8 6.4, of 4 7.0; 8, of 4 7.2, of 8 10.0; 12, of 4 8.3, units
+  // 10.0; 16, units 12.3, of 4 14.4. Longer ones: one of 8,192 tokens, cluster of 16
+  // 7.2, units 8.6; of 32,768, 17.8 and 12.9; 4 of 131,072, of 12 (all slots filled)
+  // 89.7, units 90.
+  static int cluster_size(long long rows, long long slots) {
+    return rows * 16 <= slots * 9 / 16 ? 16
+           : rows * 8 <= slots * 27 / 32 ? 8
+           : rows * 4 <= slots * 27 / 32 ? 4
+                                         : 0;
+  }
+  static bool fills(long long, long long) { return false; }
   static __device__ __forceinline__ void prefetch(const Source&) {}
 
   // One bulk copy moves the whole tile.
@@ -159,17 +172,21 @@ struct QuantTiles {
                                                  int kvh, int slot, int phys, bool to_pool, bool to_stage,
                                                  uint4 val, float ang_c, float ang_s, int lane) {
     const int c = lane & 7;
-    float x[8];
+    float2 x[4];
     unpack8(val, x);
     if (kRope) {
-      float cs[8], sn[8], partner[8];
+      float2 cs[4], sn[4], partner[4];
       unpack8(shfl_xor_uint4(val, 4), partner);
+      const float sign = c < 4 ? -1.f : 1.f;
       #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cs[e] = __shfl_sync(0xffffffffu, ang_c, 8 * (c & 3) + e);
-        sn[e] = __shfl_sync(0xffffffffu, ang_s, 8 * (c & 3) + e);
+      for (int e = 0; e < 4; ++e) {
+        const int pair = 8 * (c & 3) + 2 * e;
+        cs[e] = make_float2(__shfl_sync(0xffffffffu, ang_c, pair),
+                            __shfl_sync(0xffffffffu, ang_c, pair + 1));
+        sn[e] = make_float2(sign * __shfl_sync(0xffffffffu, ang_s, pair),
+                            sign * __shfl_sync(0xffffffffu, ang_s, pair + 1));
       }
-      if (lane < 8) rotate8(x, partner, c >= 4, cs, sn);
+      if (lane < 8) rotate8(x, partner, cs, sn);
     }
     uint2 codes;
     const uint32_t e = quantise_row(x, codes);

@@ -30,11 +30,6 @@ __host__ __device__ constexpr int v_at(int t, int d) {
 
 constexpr float kLargest = 0x1.ep127f;               // 240 x 2^120, the largest value stored
 
-// Values beyond the largest are taken as that; NaN stays.
-__device__ __forceinline__ float within_range(float x) {
-  return fabsf(x) > kLargest ? copysignf(kLargest, x) : x;
-}
-
 // The exponent byte of a row whose largest magnitude is `most` (clamped): the
 // least e >= -124 with most <= 448 x 2^e = 1.75 x 2^(e + 8), plus 127. Adding
 // 0x1fffff carries into the exponent where the fraction is above 1.75.
@@ -73,42 +68,50 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
 }
 
 // A row of 64 values held by 8 neighbouring lanes, 8 each: its exponent byte
-// and this lane's 8 codes. Called by a whole warp (four rows).
-__device__ __forceinline__ uint32_t quantise_row(float (&x)[8], uint2& codes) {
+// and this lane's 8 codes. Called by a whole warp (four rows). Arithmetic on pairs
+// where the hardware has it: each lane's instructions bound the fill.
+__device__ __forceinline__ uint32_t quantise_row(float2 (&x)[4], uint2& codes) {
   float most = 0.f;
   #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = within_range(x[i]);
-    most = fmaxf(most, fabsf(x[i]));                 // a NaN does not count
-  }
+  for (int i = 0; i < 4; ++i)
+    most = fmaxf(fmaxf(most, fabsf(x[i].x)), fabsf(x[i].y));   // a NaN does not count
   #pragma unroll
   for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (__any_sync(0xffffffffu, most > kLargest)) {
+    // values beyond the largest are taken as that; NaN stays
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (fabsf(x[i].x) > kLargest) x[i].x = copysignf(kLargest, x[i].x);
+      if (fabsf(x[i].y) > kLargest) x[i].y = copysignf(kLargest, x[i].y);
+    }
+    most = fminf(most, kLargest);
+  }
   const uint32_t e = exponent_byte(most);
-  const float inv = inverse_scale_of(e);
-  codes.x = codes_of(x[0] * inv, x[1] * inv) | codes_of(x[2] * inv, x[3] * inv) << 16;
-  codes.y = codes_of(x[4] * inv, x[5] * inv) | codes_of(x[6] * inv, x[7] * inv) << 16;
+  const float2 inv = make_float2(inverse_scale_of(e), inverse_scale_of(e));
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(x[i], inv);
+  codes.x = codes_of(x[0].x, x[0].y) | codes_of(x[1].x, x[1].y) << 16;
+  codes.y = codes_of(x[2].x, x[2].y) | codes_of(x[3].x, x[3].y) << 16;
   return e;
 }
 
 // BF16 chunk -> 8 FP32 values, exact.
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
 // 8 dims of a row rotated: own = dims 8 c .., partner = the other half's (c ^ 4),
-// with the angles of pairs 8 (c % 4) ..; products and sum each rounded in FP32.
-__device__ __forceinline__ void rotate8(float (&x)[8], const float (&partner)[8], bool high,
-                                        const float (&cs)[8], const float (&sn)[8]) {
+// cs and sn the angles of pairs 8 (c % 4) .., sn negated for the lower half (c <
+// 4: x cos - y sin); products and sum each rounded in FP32 (the
+// _rn intrinsics are never contracted).
+__device__ __forceinline__ void rotate8(float2 (&x)[4], const float2 (&partner)[4],
+                                        const float2 (&cs)[4], const float2 (&sn)[4]) {
   #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = __fmul_rn(x[i], cs[i]), b = __fmul_rn(partner[i], sn[i]);
-    x[i] = high ? __fadd_rn(a, b) : __fsub_rn(a, b);
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = __fadd2_rn(__fmul2_rn(x[i], cs[i]), __fmul2_rn(partner[i], sn[i]));
 }
 
 }  // namespace pkv_quant_dev

@@ -213,6 +213,11 @@ struct Bf16Tiles {
   };
 
   static const WindowResidency& residency(const pkv_pool* pool) { return pool->window; }
+  // Measured (us): one 2,048-token sequence, cluster of 12 5.7, units 6.8; 4
+  // sequences at a 1,024-token window 6.0 and 6.9, with 16 (not all resident at
+  // once) 9.4. One 131,072-token sequence, cluster of 12 120.6, units 48.0.
+  static int cluster_size(long long, long long) { return 12; }
+  static bool fills(long long blocks, long long slots) { return 2 * blocks >= slots; }
 
   static __device__ __forceinline__ void prefetch(const Source& src) {
     prefetch_tensormap(&src.k);

@@ -667,15 +667,14 @@ struct WindowPlan {
   int least_pages;
 };
 
-// Small batches take a cluster per (sequence, kv head): its merge is shorter
-// than the ticket's (us, one 2,048-token sequence: cluster of 12 5.7, units
-// 6.8; 4 sequences at a 1,024-token window: 6.0 and 6.9), as long as all blocks
-// are resident at once (4 sequences, cluster of 16: 9.4) and either fill half
-// of the slots or have few pages (one 131,072-token sequence: cluster of 12
-// 120.6, units 48.0). Everything else takes units.
-constexpr int kMostCluster = 12;
-
-inline WindowPlan plan_window(const pkv_pool* pool, const WindowResidency& res, int batch, int window, int sinks, int num_splits) {
+// Small batches take a cluster per (sequence, kv head), whose merge is shorter
+// than the ticket's, of the size that its tiles choose from the batch's rows (times
+// 8 KV heads) and the slots of resident cluster blocks, while the pages a sequence
+// can see are few for it or the blocks fill enough of the slots. Everything else
+// takes units.
+template <class Tiles>
+WindowPlan plan_window(const pkv_pool* pool, const WindowResidency& res, int batch, int window,
+                       int sinks, int num_splits) {
   const pkv_pool_config& c = pool->cfg;
   const int max_pages = c.max_seq_len / kPage;
   // the most pages a sequence can see
@@ -689,10 +688,11 @@ inline WindowPlan plan_window(const pkv_pool* pool, const WindowResidency& res, 
   const long long rows = static_cast<long long>(batch) * kHkv;
   const long long cluster_slots =
       static_cast<long long>(res.cluster_blocks_per_sm) * pool->num_sms;
-  const int s = std::min({kMostCluster, pool->max_cluster, c.max_splits,
-                          (seen + kWarps - 1) / kWarps});
+  constexpr int kBlockPages = kWarps * Tiles::kStagePages;      // of one turn of a block
+  const int s = std::min({Tiles::cluster_size(rows, cluster_slots), pool->max_cluster,
+                          c.max_splits, (seen + kBlockPages - 1) / kBlockPages});
   if (s >= 2 && rows * s <= cluster_slots &&
-      (seen <= 4 * kWarps * s || 2 * rows * s >= cluster_slots)) {
+      (seen <= 4 * kBlockPages * s || Tiles::fills(rows * s, cluster_slots))) {
     p.num_splits = s;
     p.cluster = true;
     return p;
@@ -710,8 +710,9 @@ inline WindowPlan plan_window(const pkv_pool* pool, const WindowResidency& res, 
 template <class Tiles, bool kFused, class MakeSource>
 pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* k, const void* v,
                          bool pools_good, const MakeSource& make_source,
-                         const int32_t* block_tables, const int32_t* seq_lens, float* out, int window, int sinks,
-                         const pkv_axes_rope* rope, const int32_t* rope_positions,
+                         const int32_t* block_tables, const int32_t* seq_lens, float* out,
+                         int window, int sinks, const pkv_axes_rope* rope,
+                         const int32_t* rope_positions,
                          int position_stride, int batch, int num_splits, void* stream) {
   if (!pool) return PKV_ERR_INVALID_ARG;
   const pkv_pool_config& c = pool->cfg;
@@ -752,7 +753,7 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
   prm.max_splits = c.max_splits;
   prm.window = std::min(window, c.max_seq_len);
   prm.sinks = std::min(sinks, c.max_seq_len);
-  const WindowPlan plan = plan_window(pool, Tiles::residency(pool), batch, prm.window, prm.sinks, num_splits);
+  const WindowPlan plan = plan_window<Tiles>(pool, Tiles::residency(pool), batch, prm.window, prm.sinks, num_splits);
   const bool cluster = plan.cluster;
   prm.num_splits = plan.num_splits;
   prm.batch = batch;
