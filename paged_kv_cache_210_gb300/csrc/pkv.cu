@@ -980,8 +980,6 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
   const size_t slots = pkv_tree_slots(pool);
   ok = ok && cudaMalloc(&pool->tree_part_o, slots * 128 * kDim * sizeof(float)) == cudaSuccess;
   ok = ok && cudaMalloc(&pool->tree_part_ml, slots * 128 * sizeof(float2)) == cudaSuccess;
-  ok = ok && cudaMalloc(&pool->tree_part_len,
-                        (1 + static_cast<size_t>(c.max_batch)) * sizeof(int)) == cudaSuccess;
   if (ok) pool->page_to = reinterpret_cast<int*>(pool->page_marks + c.num_pages);
 
   ok = ok && cudaMemset(pool->tickets, 0, 2 * static_cast<size_t>(c.max_batch) * kHkv * sizeof(int)) ==
@@ -1054,7 +1052,6 @@ pkv_status pkv_pool_destroy(pkv_pool_t pool) {
   cudaFree(pool->page_marks);
   cudaFree(pool->tree_part_o);
   cudaFree(pool->tree_part_ml);
-  cudaFree(pool->tree_part_len);
   cudaFree(pool->prefill_next);
   delete pool;
   return st;

@@ -39,7 +39,6 @@ struct pkv_pool {
                                     // launches)
   float* tree_part_o;               // [pkv_tree_slots][128][64] parts of drafted tokens' sums
   float2* tree_part_ml;             // [pkv_tree_slots][128]
-  int* tree_part_len;               // [1 + max_batch]
   WindowResidency window;           // the windowed decode over BF16 pages
   WindowResidency quant;            // ... and over 8-bit pages
   std::atomic<bool> pages_written{false};   // the handle's last page or fill call (pkv_pages.h,

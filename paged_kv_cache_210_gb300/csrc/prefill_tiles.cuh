@@ -47,7 +47,8 @@
 //                         (has_page, page, n_pages), steps (first_step, n_steps;
 //                         plain_from, plain_to and has_dead count from the first),
 //                         keys that no row sees (dead)
-//   Walk                  tile number -> Work, numbers ever larger
+//   Walk, kDrawn          tile number -> Work, numbers ever larger; drawn from a
+//                         counter by the launch's CTAs, or the walk shares them out
 //   Row                   what one row sees of a page
 //   kFewRows              tiles may leave whole softmax warps without rows
 //   kParts, is_whole, ... a tile may be a part of its rows' keys
@@ -203,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  // the kernel that joins the parts may be made ready (it waits for this one's end)
+  if constexpr (Job::kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // The n-th tile of this CTA, handed over by the K loader. One verdict per
   // warp: false if it never comes.
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           // few steps before they are used up: any earlier, and a CTA would
           // hold a tile back from those that run out of work.
           unsigned long long index = blockIdx.x;
-          if (!first) {
+          if (Job::kDrawn && !first) {
             if (lane == 0) index = gridDim.x + atomicAdd(prm.next_tile, 1ull);
             index = __shfl_sync(0xffffffffu, index, 0);
           }
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
         drain(sm.bar_k, issued, kKStages);
         drain(sm.bar_q, q_loads, kQBuffers);
         // the last CTA to stop drawing leaves the counters at zero
-        if (lane == 0) {
+        if (Job::kDrawn && lane == 0) {
           __threadfence();
           if (atomicAdd(prm.ctas_done, 1u) == gridDim.x - 1) {
             *prm.next_tile = 0;

@@ -25,17 +25,16 @@ using namespace pkv_tiles;
 namespace {
 
 constexpr int kMaxTree = PKV_MAX_TREE;
-constexpr int kTries = 8;         // part lengths tried for a launch of one wave
-constexpr int kHeld = 2;          // sequences per lane whose steps are kept for the tries
+// A tile's start and end cost a CTA about as much as two steps; a CTA is given no
+// less than kLeastCost.
+constexpr int kTileCost = 2;
+constexpr int kLeastCost = 4;
 
 struct TreeParams : TileParams {
   const unsigned long long* tree;   // [total] which drafted tokens each row sees
-  float* part_o;                    // [slots][128][64] sums of parts, not divided
-  float2* part_ml;                  // [slots][128] their exponent and sum of weights
-  int* part_len;                    // [1 + max_batch] steps per part; then each split
-                                    // sequence's first slot / 8
-  int wave;                         // units (of 8 KV heads) that one wave of CTAs takes
-  int slots;                        // 8 x the units that may be parts
+  float* part_o;                    // [2 wave][8][128][64] sums of parts, not divided
+  float2* part_ml;                  // [2 wave][8][128] their exponent and sum of weights
+  int wave;                         // CTAs of one wave, per KV head
 };
 
 struct TreeWork {
@@ -104,25 +103,34 @@ struct TreeView {
   }
 };
 
-// The launch's units (sequence, tile, part), sequence by sequence, 8 KV heads each.
-// Held by one warp that asks for ever larger numbers; lane i looks after the i-th
-// of 32 sequences.
+// How the launch's work is shared out. All tiles one after the other (sequence by
+// sequence, a tile kTileCost before its steps) make a line of `total` places; of
+// `ctas` CTAs per KV head number c takes [total c / ctas, total (c + 1) / ctas), so
+// all take equally long whatever the lengths are, and a tile may be cut anywhere.
+// (Parts of one length per launch left a fifth of the device idle: 8 trees of 64
+// over 20,000 to 32,700 tokens took 254 us, shared out 205.)
 //
-// Parts: with T the steps of all tiles, a batch whose tiles fit one wave of CTAs
-// takes the shortest of r0 (8 + k) / 8 steps, r0 = T / wave, k < 8, with which the
-// parts fit it too; others T / wave steps.
-struct TreeWalk {
-  int chunk = 0;                  // steps per part; 0: not known yet
-  int first = -32;                // the first of the 32 sequences
-  int row0, nodes, start, steps;  // this lane's sequence
-  int units, before_me;           // its units and those of earlier lanes
-  int slot_units;                 // ... of those that are parts
-  int base = 0, here = 0;         // units of earlier sequences, of these 32
-  int slot_base = 0, slots_here = 0;
+// A CTA has at most one part of a tile that began before it, kept in slot 2 c, and
+// one of a tile that goes on behind it, in slot 2 c + 1.
+struct TreeShares {
+  long long total;
+  int ctas;
+  __device__ void set(long long all, int wave) {
+    total = all;
+    ctas = static_cast<int>(min(max(total / kLeastCost, 1ll), static_cast<long long>(wave)));
+  }
+  __device__ long long begin(int c) const { return total * c / ctas; }
+  // the last CTA that begins at or before `place`
+  __device__ int owner(long long place) const {
+    return static_cast<int>(((place + 1) * ctas - 1) / total);
+  }
+};
 
-  __device__ __forceinline__ void fetch(const TreeParams&, int) {}
+// The sequences of 32 lanes: what each brings, and where on the line.
+struct TreeLane {
+  int row0, nodes, start, steps;
 
-  // Lane's sequence b: its data, steps 0 if it has none or they are bad.
+  // Sequence b: steps 0 if there is none or its data is bad.
   __device__ __forceinline__ void load(const TreeParams& prm, int b, bool report) {
     steps = nodes = row0 = start = 0;
     if (b >= prm.batch) return;
@@ -141,107 +149,126 @@ struct TreeWalk {
     steps = TreePages(start, nodes, prm.window, prm.sinks).steps();
   }
   __device__ __forceinline__ int tiles() const { return (nodes + kTileTokens - 1) / kTileTokens; }
+  __device__ __forceinline__ int cost() const { return tiles() * (steps + kTileCost); }
+};
 
-  __device__ __forceinline__ void plan(const TreeParams& prm, int lane) {
-    int held_steps[kHeld], held_tiles[kHeld];
-    long long total = 0;
-    for (int b = 0; b < prm.batch; b += 32) {
-      load(prm, b + lane, blockIdx.x == 0);
-      #pragma unroll
-      for (int e = 0; e < kHeld; ++e)
-        if (b == 32 * e) {
-          held_steps[e] = steps;
-          held_tiles[e] = tiles();
-        }
-      total += static_cast<long long>(steps) * tiles();
-    }
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int r0 = max(static_cast<int>((total + prm.wave - 1) / prm.wave), 1);
-    chunk = r0;
-    if (prm.batch <= 32 * kHeld) {
-      #pragma unroll
-      for (int k = kTries - 1; k >= 0; --k) {
-        const int r = (r0 * (kTries + k) + kTries - 1) / kTries;
-        int n = 0;
-        #pragma unroll
-        for (int e = 0; e < kHeld; ++e)
-          if (prm.batch > 32 * e) n += held_tiles[e] * ((held_steps[e] + r - 1) / r);
-        if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) <= prm.wave) chunk = r;
-      }
-    }
-    if (blockIdx.x == 0 && lane == 0) prm.part_len[0] = chunk;
+// The sum of x over the lanes.
+__device__ __forceinline__ long long warp_sum(long long x) {
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// This CTA's parts, in the line's order. Held by one warp; lane i looks after the
+// i-th of 32 sequences.
+struct TreeWalk {
+  TreeLane mine;
+  TreeShares shares;
+  bool planned = false;
+  int cta, first;                 // its number; the first of the 32 sequences
+  long long at, end;              // places that are left
+  long long base;                 // where the 32 sequences begin
+  int before_me, here;            // cost of earlier lanes' sequences; of all 32
+
+  __device__ __forceinline__ void fetch(const TreeParams& prm, int lane) {
+    mine.load(prm, lane, blockIdx.x == 0);
   }
 
-  // Unit `index` / 8 for KV head `index` % 8. False past the last one. Called by a
-  // whole warp.
-  __device__ __forceinline__ bool next(unsigned long long index, const TreeParams& prm, int lane,
-                                       TreeWork& work) {
-    if (chunk == 0) plan(prm, lane);
-    const long long u = static_cast<long long>(index / kHkv);
-    while (u >= base + here) {
-      base += here;
-      slot_base += slots_here;
-      first += 32;
-      if (first >= prm.batch) return false;
-      load(prm, first + lane, false);
-      const int parts = (steps + chunk - 1) / chunk;
-      units = tiles() * parts;
-      slot_units = parts > 1 ? units : 0;
-      before_me = scan(units, lane, here);
-      slot_units = scan(slot_units, lane, slots_here);    // those of earlier lanes
+  __device__ __forceinline__ void take(int lane) {
+    int incl = mine.cost();       // 32 x 2 x (2^14 + 3) at most
+    const int own = incl;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
     }
-    const int at = static_cast<int>(u - base);
-    const int from = __ffs(__ballot_sync(0xffffffffu, at >= before_me && at < before_me + units)) - 1;
-    const int parts = (__shfl_sync(0xffffffffu, steps, from) + chunk - 1) / chunk;
-    const int place = at - __shfl_sync(0xffffffffu, before_me, from);
-    const int tile = place / parts, part = place - tile * parts;
-    work.b = first + from;
-    work.g = static_cast<int>(index % kHkv);
-    work.start = __shfl_sync(0xffffffffu, start, from);
-    work.nodes = __shfl_sync(0xffffffffu, nodes, from);
-    const int r0 = __shfl_sync(0xffffffffu, row0, from);
-    const int all = __shfl_sync(0xffffffffu, steps, from);
-    const int slot0 = slot_base + __shfl_sync(0xffffffffu, slot_units, from);
-    work.first_node = tile * kTileTokens;
-    work.row = r0 + work.first_node;
-    work.count = min(kTileTokens, work.nodes - work.first_node);
-    work.step = part * chunk;
-    work.steps = min(chunk, all - work.step);
-    work.slot = parts > 1 ? (slot0 + place) * kHkv + work.g : -1;
-    if (place == 0 && work.g == 0 && parts > 1 && lane == 0) prm.part_len[1 + work.b] = slot0;
-    // the rows' positions, where the window hides committed tokens
-    work.lo = 0;
-    work.top = work.start + work.nodes - 1;
-    if (work.top >= prm.window) {
-      int least = kMaxTree, most = 0;
-      for (int i = lane; i < work.nodes; i += 32) {
-        const int n = __popcll(prm.tree[r0 + i] & low_nodes(work.nodes));
-        least = min(least, n);
-        most = max(most, n);
+    here = __shfl_sync(0xffffffffu, incl, 31);
+    before_me = incl - own;
+  }
+
+  __device__ __forceinline__ void plan(const TreeParams& prm, int lane) {
+    planned = true;
+    cta = blockIdx.x / kHkv;
+    first = 0;
+    base = 0;
+    take(lane);
+    long long total = here;
+    if (prm.batch > 32) {
+      long long rest = 0;
+      for (int b = 32; b < prm.batch; b += 32) {
+        TreeLane other;
+        other.load(prm, b + lane, blockIdx.x == 0);
+        rest += other.cost();
       }
-      least = __reduce_min_sync(0xffffffffu, least);
-      most = __reduce_max_sync(0xffffffffu, most);
-      work.lo = min(max(work.start + least - prm.window, 0), work.start);
-      work.top = work.start + most - 1;
+      total += warp_sum(rest);
     }
-    return true;
+    at = end = 0;
+    if (total == 0) return;
+    shares.set(total, prm.wave);
+    if (cta >= shares.ctas) return;
+    at = shares.begin(cta);
+    end = shares.begin(cta + 1);
+  }
+
+  // The next part, false when there is none. Called by a whole warp.
+  __device__ __forceinline__ bool next(unsigned long long, const TreeParams& prm, int lane,
+                                       TreeWork& work) {
+    if (!planned) plan(prm, lane);
+    while (at < end) {
+      if (at >= base + here) {
+        base += here;
+        first += 32;
+        mine.load(prm, first + lane, false);
+        take(lane);
+        continue;
+      }
+      const int place = static_cast<int>(at - base);
+      const int from = __ffs(__ballot_sync(0xffffffffu, place >= before_me &&
+                                                            place < before_me + mine.cost())) - 1;
+      const int steps = __shfl_sync(0xffffffffu, mine.steps, from);
+      const int in = place - __shfl_sync(0xffffffffu, before_me, from);
+      const int tile = in >= steps + kTileCost ? 1 : 0;
+      const long long tile_at = at - (in - tile * (steps + kTileCost));   // the tile's place
+      const int begin = max(static_cast<int>(at - tile_at) - kTileCost, 0);
+      const int stop = static_cast<int>(min(max(end - tile_at - kTileCost, 0ll),
+                                            static_cast<long long>(steps)));
+      at = tile_at + steps + kTileCost;
+      if (stop <= begin) continue;
+      work.b = first + from;
+      work.g = blockIdx.x % kHkv;
+      work.start = __shfl_sync(0xffffffffu, mine.start, from);
+      work.nodes = __shfl_sync(0xffffffffu, mine.nodes, from);
+      const int row0 = __shfl_sync(0xffffffffu, mine.row0, from);
+      work.first_node = tile * kTileTokens;
+      work.row = row0 + work.first_node;
+      work.count = min(kTileTokens, work.nodes - work.first_node);
+      work.step = begin;
+      work.steps = stop - begin;
+      work.slot = begin == 0 && stop == steps
+                      ? -1
+                      : (2 * cta + (begin == 0 ? 1 : 0)) * kHkv + work.g;
+      // the rows' positions, where the window hides committed tokens
+      work.lo = 0;
+      work.top = work.start + work.nodes - 1;
+      if (work.top >= prm.window) {
+        int least = kMaxTree, most = 0;
+        for (int i = lane; i < work.nodes; i += 32) {
+          const int n = __popcll(prm.tree[row0 + i] & low_nodes(work.nodes));
+          least = min(least, n);
+          most = max(most, n);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        work.lo = min(max(work.start + least - prm.window, 0), work.start);
+        work.top = work.start + most - 1;
+      }
+      return true;
+    }
+    return false;
   }
 
   static __device__ __forceinline__ unsigned long long low_nodes(int n) {
     return n >= 64 ? ~0ull : (1ull << n) - 1ull;
-  }
-
-  // The sum over earlier lanes, and over all.
-  static __device__ __forceinline__ int scan(int x, int lane, int& all) {
-    int incl = x;
-    #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    all = __shfl_sync(0xffffffffu, incl, 31);
-    return incl - x;
   }
 };
 
@@ -252,6 +279,7 @@ struct TreeJob {
   using Walk = TreeWalk;
   static constexpr bool kFewRows = true;
   static constexpr bool kParts = true;
+  static constexpr bool kDrawn = false;
   static __device__ __forceinline__ bool is_whole(const Work& work) { return work.slot < 0; }
   static __device__ __forceinline__ void put_sums(const Work& work, const Params& prm, int r,
                                                   float m, float l) {
@@ -288,25 +316,42 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 8;       // parts whose sums are loaded at once
 
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams prm) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.z, tile = blockIdx.y;
   const int g = blockIdx.x % kHkv, quarter = blockIdx.x / kHkv;
-  TreeWalk walk;
-  walk.load(prm, b, false);
+  // this launch must not complete before the one ahead of it, even if nothing is
+  // to be joined: the launch after it waits for this one alone
+  if (b == 0 && tile == 0 && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // where the tile lies on the line, from the lists alone
+  const int lane = threadIdx.x & 31;
+  long long all = 0, before = 0;
+  for (int s = 0; s < prm.batch; s += 32) {
+    TreeLane other;
+    other.load(prm, s + lane, false);
+    all += other.cost();
+    before += s + lane < b ? other.cost() : 0;
+  }
+  all = warp_sum(all);
+  before = warp_sum(before);
+  TreeLane seq;
+  seq.load(prm, b, false);
   const int first_token = tile * kTileTokens + quarter * 8;
-  if (walk.steps == 0 || first_token >= walk.nodes) return;
-  const int chunk = __ldcg(prm.part_len);
-  const int parts = (walk.steps + chunk - 1) / chunk;
+  if (first_token >= seq.nodes) return;
+  TreeShares shares;
+  shares.set(all, prm.wave);
+  const long long from = before + tile * (seq.steps + kTileCost) + kTileCost;
+  const int cta = shares.owner(from);
+  const int parts = shares.owner(from + seq.steps - 1) - cta + 1;
   if (parts <= 1) return;
   const int r = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
   const int token = first_token + (r >> 2);
-  if (token >= walk.nodes) return;
-  const size_t slot = static_cast<size_t>(__ldcg(prm.part_len + 1 + b) + tile * parts) * kHkv + g;
+  if (token >= seq.nodes) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int row = quarter * 32 + r;
-  const float4* o = reinterpret_cast<const float4*>(prm.part_o) +
-                    (slot * kRows + row) * (kDim / 4) + lane8;
-  const float2* ml = prm.part_ml + slot * kRows + row;
-  constexpr size_t kStep = static_cast<size_t>(kHkv) * kRows;
+  // part 0 in slot 2 cta + 1, part s in slot 2 (cta + s)
+  auto slot = [&](int s) {
+    return static_cast<size_t>((2 * (cta + s) + (s == 0 ? 1 : 0)) * kHkv + g) * kRows + row;
+  };
+  const float4* o = reinterpret_cast<const float4*>(prm.part_o) + lane8;
   float m = -INFINITY, l = 0.f;
   float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int s = 0; s < parts; s += kJoinAhead) {
@@ -315,10 +360,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
     #pragma unroll
     for (int e = 0; e < kJoinAhead; ++e) {
       const bool is = s + e < parts;
-      x[e] = is ? __ldcg(ml + (s + e) * kStep) : make_float2(-INFINITY, 0.f);
+      const size_t at = is ? slot(s + e) : 0;
+      x[e] = is ? __ldcg(prm.part_ml + at) : make_float2(-INFINITY, 0.f);
       #pragma unroll
       for (int h = 0; h < 2; ++h)
-        v[e][h] = is ? __ldcg(o + (s + e) * kStep * (kDim / 4) + 8 * h)
+        v[e][h] = is ? __ldcg(o + at * (kDim / 4) + 8 * h)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float m_new = m;
@@ -346,7 +392,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   float4* to = reinterpret_cast<float4*>(
-                   prm.out + ((static_cast<size_t>(walk.row0) + token) * kHq + g * kGroup +
+                   prm.out + ((static_cast<size_t>(seq.row0) + token) * kHq + g * kGroup +
                               (r & 3)) * kDim) + lane8;
   #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -472,13 +518,21 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   prm.tree = reinterpret_cast<const unsigned long long*>(tree);
   prm.part_o = pool->tree_part_o;
   prm.part_ml = pool->tree_part_ml;
-  prm.part_len = pool->tree_part_len;
   prm.wave = std::max(wave / kHkv, 1);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   tile_attention_kernel<TreeJob><<<wave, kThreads, kSmemBytes<TreeJob>, st>>>(tq, tk, tv, prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  const int tiles = total_tokens > kTileTokens ? 2 : 1;
-  tree_join_kernel<<<dim3(kHkv * (kTileTokens / 8), tiles, batch), kJoinThreads, 0, st>>>(prm);
+  // the join's blocks start as the attention's CTAs end, and wait for the last
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kHkv * (kTileTokens / 8), total_tokens > kTileTokens ? 2 : 1, batch);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tree_join_kernel, prm) != cudaSuccess) return PKV_ERR_CUDA;
   return pkv_check_launch();
 }
 

@@ -211,6 +211,7 @@ struct WindowJob {
   using Walk = WindowWalk;
   static constexpr bool kFewRows = false;
   static constexpr bool kParts = false;
+  static constexpr bool kDrawn = true;
   static __device__ constexpr bool is_whole(const Work&) { return true; }
   struct Row {
     int pos, window;
