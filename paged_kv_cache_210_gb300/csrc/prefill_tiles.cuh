@@ -240,25 +240,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
       // V only: a step with rows that no one sees lands on a barrier of its
       // own; the loader clears those rows and then completes the stage.
       int edges = 0;
-      auto load_tile = [&](const View& view, const Work& work, const CUtensorMap* map,
+      // this lane's page of 8 steps from step j on: past the pool's end if there is
+      // none, or an invalid one (bad)
+      auto page_id = [&](const View& view, int b, int j, bool& bad) {
+        int id = prm.num_pages;
+        const int i = (view.first_step() + j) * kStepPages + lane;
+        if (view.has_page(i)) {
+          id = __ldg(prm.table + static_cast<size_t>(b) * prm.table_stride + view.page(i));
+          if (id < 0 || id >= prm.num_pages) {
+            id = prm.num_pages;
+            bad = true;
+          }
+        }
+        return id;
+      };
+      auto load_tile = [&](const View& view, const Work& work, int ids, const CUtensorMap* map,
                            uint8_t* ring, unsigned long long* full, unsigned long long* free,
                            auto& at, int& issued, int stages, bool is_v) {
-        const int32_t* trow = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
-        auto page_of = [&](int j, int e) {      // the e-th page of step j, past the end if none
-          int id = prm.num_pages;
-          const int i = (view.first_step() + j) * kStepPages + e;
-          if (view.has_page(i)) {
-            id = __ldg(trow + view.page(i));
-            if (id < 0 || id >= prm.num_pages) id = prm.num_pages;
-          }
-          return id;
-        };
-        int ids = page_of(lane / kStepPages, lane % kStepPages);
-        int ids_next = page_of(8 + lane / kStepPages, lane % kStepPages);
+        bool bad;
+        int ids_next = page_id(view, work.b, 8, bad);
         for (int j = 0; j < view.n_steps; ++j) {
           if ((j & 7) == 0 && j > 0) {
             ids = ids_next;
-            ids_next = page_of(j + 8 + lane / kStepPages, lane % kStepPages);
+            ids_next = page_id(view, work.b, j + 8, bad);
           }
           const int page = __shfl_sync(0xffffffffu, ids, (j & 7) * kStepPages + lane % kStepPages);
           const bool edge = is_v && view.has_dead(j);
@@ -328,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           Work work;
           if (!walk.next(index, prm, lane, work)) break;
           const View view(work, prm);
-          const int32_t* trow = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
           const int buffer = n % kQBuffers;
+          bool bad = false;
+          const int ids = page_id(view, work.b, 0, bad);
           if (lane == 0) {
             if (n >= kQBuffers) ok = mbar_wait(&sm.q_free[buffer], (n / kQBuffers - 1) & 1);
             if (ok) {
@@ -341,19 +346,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           if (!ok) break;
           ++q_loads;
           // invalid ids among the pages that count
-          bool bad = false;
-          const int first_page = view.first_step() * kStepPages;
-          const int end_page = min(first_page + view.n_steps * kStepPages, view.n_pages);
-          for (int i = first_page + lane; i < end_page; i += 32) {
-            const int id = view.has_page(i) ? __ldg(trow + view.page(i)) : 0;
-            bad |= id < 0 || id >= prm.num_pages;
-          }
+          #pragma unroll 4
+          for (int j = 8; j < view.n_steps; j += 8) page_id(view, work.b, j, bad);
           work.bad_page = __any_sync(0xffffffffu, bad);
           if (work.bad_page && lane == 0) set_error(prm.err, PKV_DEV_ERR_PAGE);
           ok = hand_over(work);
           if (!ok) break;
           ++n;
-          ok = load_tile(view, work, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued, kKStages,
+          ok = load_tile(view, work, ids, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued, kKStages,
                          false);
           if (!ok) break;
         }
@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           ok = next_work(n, work);
           if (!ok || work.count == 0) break;
           const View view(work, prm);
-          ok = load_tile(view, work, &tmap_v, sm.v[0], sm.bar_v, sm.v_free, at, issued, kVStages,
-                         true);
+          bool bad;
+          ok = load_tile(view, work, page_id(view, work.b, 0, bad), &tmap_v, sm.v[0], sm.bar_v,
+                         sm.v_free, at, issued, kVStages, true);
           if (!ok) break;
         }
         if (!ok && lane == 0) give_up();

@@ -119,10 +119,16 @@ struct TreeShares {
     total = all;
     ctas = static_cast<int>(min(max(total / kLeastCost, 1ll), static_cast<long long>(wave)));
   }
-  __device__ long long begin(int c) const { return total * c / ctas; }
+  __device__ long long begin(int c) const { return quotient(total * c, ctas); }
   // the last CTA that begins at or before `place`
   __device__ int owner(long long place) const {
-    return static_cast<int>(((place + 1) * ctas - 1) / total);
+    return static_cast<int>(quotient((place + 1) * ctas - 1, total));
+  }
+  // x / y, in 32 bits where they fit: a division in 64 is some 100 instructions on
+  // the way to a CTA's first copy
+  static __device__ long long quotient(long long x, long long y) {
+    return (x | y) >> 32 ? x / y
+                         : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
   }
 };
 
