@@ -413,58 +413,66 @@ constexpr int kCommitThreads = 256;
 constexpr int kHeadVecs = 2 * kRowBytes / 16;                    // K and V of a token: 16
 constexpr int kCommitItems = kMaxTree * kHeadVecs / kCommitThreads;   // 4
 
-__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(
+__global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
     uint4* k_pool, uint4* v_pool, const int32_t* __restrict__ tables,
     const int32_t* __restrict__ start_pos, const int32_t* __restrict__ accepted,
     const int32_t* __restrict__ counts, int max_accepted, int max_batch, int table_stride,
     int num_pages, int max_seq_len, int heads, int* err) {
   const int b = blockIdx.y, layer = blockIdx.z;
   const int count = counts[b], start = start_pos[b];
+  // item i of this thread: accepted token k(i)'s vector `vec` of head g(i)
+  auto k_of = [&](int i) { return (threadIdx.x + i * kCommitThreads) / (heads * kHeadVecs); };
+  int j[kCommitItems];
+  #pragma unroll
+  for (int i = 0; i < kCommitItems; ++i)        // not waiting for the count
+    j[i] = k_of(i) < max_accepted ? accepted[static_cast<size_t>(b) * max_accepted + k_of(i)] : 0;
   if (count == 0) return;
   const bool reports = threadIdx.x == 0 && blockIdx.x == 0;
-  if (count < 0 || count > max_accepted) {
-    if (reports) set_error(err, PKV_DEV_ERR_SEQ_LEN);
+  if (count < 0 || count > max_accepted || start < 0 || start > max_seq_len - count) {
+    if (reports) set_error(err, count < 0 || count > max_accepted ? PKV_DEV_ERR_SEQ_LEN
+                                                                  : PKV_DEV_ERR_POSITION);
     return;
   }
   const int32_t* row = tables + (static_cast<size_t>(layer) * max_batch + b) * table_stride;
-  uint4 v[kCommitItems];
-  size_t to[kCommitItems];
-  bool good_place = start >= 0 && start <= max_seq_len - count, good_page = true;
+  int page[kCommitItems], dest[kCommitItems];
+  int bad = 0;
   #pragma unroll
   for (int i = 0; i < kCommitItems; ++i) {
-    const int item = threadIdx.x + i * kCommitThreads;
-    const int k = item / (heads * kHeadVecs);
-    const int g = blockIdx.x * heads + item / kHeadVecs % heads;
-    to[i] = 0;
+    page[i] = dest[i] = -1;
+    if (k_of(i) >= count) continue;
+    if (j[i] < 0 || j[i] >= kMaxTree || j[i] >= max_seq_len - start) {
+      bad = PKV_DEV_ERR_POSITION;
+      continue;
+    }
+    page[i] = row[(start + j[i]) / kPage];
+    dest[i] = row[(start + k_of(i)) / kPage];
+  }
+  uint4 v[kCommitItems];
+  #pragma unroll
+  for (int i = 0; i < kCommitItems; ++i) {
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (!good_place || k >= count) continue;
-    const int j = accepted[static_cast<size_t>(b) * max_accepted + k];
-    if (j < 0 || j >= kMaxTree || j >= max_seq_len - start) {
-      good_place = false;
+    if (k_of(i) >= count || bad) continue;
+    if (page[i] < 0 || page[i] >= num_pages || dest[i] < 0 || dest[i] >= num_pages) {
+      bad = PKV_DEV_ERR_PAGE;
       continue;
     }
-    const int from = start + j, dest = start + k;
-    const int page = row[from / kPage], dest_page = row[dest / kPage];
-    if (page < 0 || page >= num_pages || dest_page < 0 || dest_page >= num_pages) {
-      good_page = false;
-      continue;
-    }
-    const int chunk = item % 8;
+    const int item = threadIdx.x + i * kCommitThreads;
+    const int g = blockIdx.x * heads + item / kHeadVecs % heads;
     const uint4* pool = item / 8 % 2 ? v_pool : k_pool;
-    v[i] = pool[((static_cast<size_t>(page) * kHkv + g) * kPage + from % kPage) * 8 + chunk];
-    to[i] = ((static_cast<size_t>(dest_page) * kHkv + g) * kPage + dest % kPage) * 8 + chunk;
+    v[i] = pool[((static_cast<size_t>(page[i]) * kHkv + g) * kPage + (start + j[i]) % kPage) * 8 +
+                item % 8];
   }
   // every row is in registers, and the verdict is the block's
-  const bool bad_place = __syncthreads_or(!good_place);
-  const bool bad_page = __syncthreads_or(!good_page);
-  if (bad_place || bad_page) {
-    if (reports) set_error(err, bad_place ? PKV_DEV_ERR_POSITION : PKV_DEV_ERR_PAGE);
-    return;
-  }
+  if (bad) set_error(err, bad);
+  if (__syncthreads_or(bad)) return;
   #pragma unroll
   for (int i = 0; i < kCommitItems; ++i) {
+    if (k_of(i) >= count) continue;
     const int item = threadIdx.x + i * kCommitThreads;
-    if (item / (heads * kHeadVecs) < count) (item / 8 % 2 ? v_pool : k_pool)[to[i]] = v[i];
+    const int g = blockIdx.x * heads + item / kHeadVecs % heads;
+    uint4* pool = item / 8 % 2 ? v_pool : k_pool;
+    pool[((static_cast<size_t>(dest[i]) * kHkv + g) * kPage + (start + k_of(i)) % kPage) * 8 +
+         item % 8] = v[i];
   }
 }
 
