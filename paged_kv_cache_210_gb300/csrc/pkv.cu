@@ -1027,7 +1027,8 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
     cudaGetLastError();   // a size the device refuses is not an error here
   }
   ok = ok && pkv_layers_setup(pool);
-  ok = ok && pkv_window_setup(pool) && pkv_quant_setup(pool);
+  ok = ok && pkv_window_setup(pool) && pkv_quant_setup(pool) &&
+       pkv_tree_few_setup();
   if (ok && pool->blocks_per_sm < 1) pool->blocks_per_sm = 1;
   if (ok && pool->cluster_blocks_per_sm < 1) pool->cluster_blocks_per_sm = 1;
   if (ok && pool->wide_blocks_per_sm < 1) pool->wide_blocks_per_sm = 1;

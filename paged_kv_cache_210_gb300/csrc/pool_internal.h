@@ -89,6 +89,9 @@ bool pkv_layers_setup(pkv_pool* pool);
 bool pkv_window_setup(pkv_pool* pool);
 bool pkv_quant_setup(pkv_pool* pool);
 
+// tree_few.cu: its kernel's attributes.
+bool pkv_tree_few_setup();
+
 // tree.cu: parts of 128 rows whose sums one call may keep.
 size_t pkv_tree_slots(const pkv_pool* pool);
 

@@ -1,0 +1,436 @@
+// Attention of small drafted trees over the paged KV cache for GB300 (sm_103a):
+// pkv_tree_attention's kernel where a sequence brings few drafted tokens (declared
+// in include/pkv_tree.h; larger trees: tree.cu).
+//
+// out_i = sum_t p_it V_t / sum_t p_it, p_it = 2^(q_i.K_t log2(e) / 8 - m_i), over
+// the tokens that row i sees: one pass with a running maximum m_i and sum.
+//
+// A tile is up to 8 drafted tokens of a sequence and KV head: 32 rows. That fills a
+// quarter of a tcgen05 product's rows, and a CTA of that kernel takes 5 us before its
+// first scores (its roles, tensor memory and first instructions). Here a block is
+// four warps like the decode's: each takes every fourth page through its own ring of
+// tiles and does all 32 rows' products by warp-wide mma.sync, which needs no set-up.
+// The tiles' steps (four pages, one per warp) are shared out and joined as in tree.cu.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pkv.h"
+#include "pkv_tree.h"
+#include "decode_device.cuh"
+#include "device_common.cuh"
+#include "pool_internal.h"
+#include "tree.cuh"
+
+using namespace pkv_tree_dev;
+
+namespace {
+
+constexpr int kFewTokens = 8;                        // drafted tokens of a tile
+constexpr int kFewRowsN = kFewTokens * kGroup;       // 32
+constexpr int kFewWarps = 4;
+constexpr int kFewThreads = kFewWarps * 32;
+constexpr int kFewStages = 3;
+constexpr int kFewBlocksPerSm = 3;
+constexpr int kFewTileBytes = kPage * kRowBytes;     // K or V of a page: 2 KiB
+constexpr int kAccStride = kDim + 4;                 // floats of a merged row: no bank conflicts
+static_assert(kFewWarps == kStepPages, "a step's pages go to a warp each");
+
+struct alignas(1024) FewSmem {
+  pkv_decode::PageRing<kFewStages> warp[kFewWarps];  // at a part's end: the warp's sums
+  uint4 q[8][32];                                    // the rows as operand fragments, by lane
+  unsigned long long mask[kFewTokens];
+  unsigned long long bar[kFewWarps][kFewStages];
+  float m[kFewWarps][kFewRowsN];
+  float l[kFewWarps][kFewRowsN];
+  int abort;
+};
+constexpr size_t kFewSmemBytes = sizeof(FewSmem) + 1024;   // + room to align the base
+static_assert(sizeof(pkv_decode::PageRing<kFewStages>) >= kFewRowsN * kAccStride * sizeof(float),
+              "a warp's sums fit its ring");
+static_assert(kFewBlocksPerSm * (kFewSmemBytes + 1024) <= 228 * 1024, "blocks per SM");
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// A warp's sums over its pages. Lane (g, q) = (L / 4, L % 4) holds rows 16 t + g
+// (o[t][n][0, 1]) and 16 t + 8 + g ([2, 3]), dims 8 n + 2 q, + 1; row r is drafted
+// token r / 4 of the tile, head r % 4. m and l of row 16 t + 8 h + g in [2 t + h].
+struct FewState {
+  float o[2][8][4];
+  float m[4];      // base-2 exponent the row's weights are taken against, p <= 2^8
+  float l[4];      // this lane's share of the row's sum
+  __device__ __forceinline__ void reset() {
+    #pragma unroll
+    for (int t = 0; t < 2; ++t)
+      #pragma unroll
+      for (int n = 0; n < 8; ++n)
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][n][e] = 0.f;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+  }
+};
+
+// One page, K tile kt and V tile vt (swizzled). kTiles: 16-row halves that have
+// rows. seen: what each of this lane's rows sees of it, 16 bits, where not `whole`;
+// V rows that no row sees hold zeros.
+template <int kTiles>
+__device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt, bool whole,
+                                            const uint32_t (&seen)[4], const uint4 (*q)[32],
+                                            int lane, FewState& st) {
+  const int g8 = lane >> 2;
+  const int qq = lane & 3;
+  // scores; slice s of the contraction is dims 16 q + 4 s .. + 3 of lane q, so a
+  // lane's fragments of a K row are 32 contiguous bytes (as in decode_device.cuh)
+  float s[kTiles][2][4];
+  {
+    uint32_t kw[2][8];
+    #pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const uint8_t* row = kt + (8 * nt + g8) * kRowBytes;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(row + (((2 * qq) ^ g8) << 4));
+      const uint4 k1 = *reinterpret_cast<const uint4*>(row + (((2 * qq + 1) ^ g8) << 4));
+      kw[nt][0] = k0.x; kw[nt][1] = k0.y; kw[nt][2] = k0.z; kw[nt][3] = k0.w;
+      kw[nt][4] = k1.x; kw[nt][5] = k1.y; kw[nt][6] = k1.z; kw[nt][7] = k1.w;
+    }
+    #pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      #pragma unroll
+      for (int nt = 0; nt < 2; ++nt) s[t][nt][0] = s[t][nt][1] = s[t][nt][2] = s[t][nt][3] = 0.f;
+      #pragma unroll
+      for (int half = 0; half < 2; ++half) {       // dims 8 half .. + 7 of each lane's 16
+        const uint4 lo = q[4 * t + half][lane], hi = q[4 * t + 2 + half][lane];   // rows g, g + 8
+        const uint32_t a[2][4] = {{lo.x, hi.x, lo.y, hi.y}, {lo.z, hi.z, lo.w, hi.w}};
+        #pragma unroll
+        for (int e = 0; e < 2; ++e)
+          #pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+            mma_16816(s[t][nt], a[e], kw[nt][4 * half + 2 * e], kw[nt][4 * half + 2 * e + 1]);
+      }
+    }
+  }
+  if (!whole) {
+    #pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+      #pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!((seen[2 * t + e / 2] >> (8 * nt + 2 * qq + e % 2)) & 1u)) s[t][nt][e] = -INFINITY;
+  }
+  const float c = 1.4426950408889634f * 0.125f;   // log2(e) / sqrt(64)
+  float top[2 * kTiles];
+  bool grow = false;
+  #pragma unroll
+  for (int i = 0; i < 2 * kTiles; ++i) {
+    const int t = i / 2, h = 2 * (i % 2);
+    top[i] = fmaxf(fmaxf(s[t][0][h], s[t][0][h + 1]), fmaxf(s[t][1][h], s[t][1][h + 1])) * c;
+    grow |= top[i] > st.m[i] + pkv_decode::kRescaleLog2;
+  }
+  // a row's exponent moves only when its maximum grows by more than 2^8
+  if (__any_sync(0xffffffffu, grow)) {
+    #pragma unroll
+    for (int i = 0; i < 2 * kTiles; ++i) {
+      const float most = quad_max(top[i]);
+      if (most > st.m[i] + pkv_decode::kRescaleLog2) {
+        const float alpha = fast_exp2(st.m[i] - most);   // 0 on the first page
+        st.m[i] = most;
+        st.l[i] *= alpha;
+        #pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          st.o[i / 2][n][2 * (i % 2)] *= alpha;
+          st.o[i / 2][n][2 * (i % 2) + 1] *= alpha;
+        }
+      }
+    }
+  }
+  // weights as three BF16 terms (24 bits): A fragments of rows g, g + 8 and tokens
+  // 2 q, 2 q + 1, then 8 + 2 q, 9 + 2 q, where the scores' accumulators hold them
+  uint32_t p[kTiles][3][4];
+  const float2 c2 = make_float2(c, c);
+  #pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float mu = st.m[2 * t + h] == -INFINITY ? 0.f : st.m[2 * t + h];
+      const float2 minus = make_float2(-mu, -mu);
+      float2 sum = make_float2(0.f, 0.f);
+      #pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float2 x = __ffma2_rn(make_float2(s[t][nt][2 * h], s[t][nt][2 * h + 1]), c2, minus);
+        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        sum = __fadd2_rn(sum, pp);
+        split3(pp.x, pp.y, p[t][0][2 * nt + h], p[t][1][2 * nt + h], p[t][2][2 * nt + h]);
+      }
+      st.l[2 * t + h] += sum.x + sum.y;
+    }
+  // values: a page's products start from zero and are added up in FP32
+  const int mrow = lane & 7;
+  const int mat = lane >> 3;
+  const uint32_t vrow = smem_u32(vt) + (mrow + 8 * (mat & 1)) * kRowBytes;
+  #pragma unroll
+  for (int jj = 0; jj < 4; ++jj) {
+    uint32_t v[4];
+    pkv_decode::ldsm_x4_trans(v, vrow + (((2 * jj + (mat >> 1)) ^ mrow) << 4));
+    #pragma unroll
+    for (int h = 0; h < 2; ++h)
+      #pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        #pragma unroll
+        for (int part = 0; part < 3; ++part) mma_16816(d, p[t][part], v[2 * h], v[2 * h + 1]);
+        float* o = st.o[t][2 * jj + h];
+        const float2 a = __fadd2_rn(make_float2(o[0], o[1]), make_float2(d[0], d[1]));
+        const float2 b = __fadd2_rn(make_float2(o[2], o[3]), make_float2(d[2], d[3]));
+        o[0] = a.x;
+        o[1] = a.y;
+        o[2] = b.x;
+        o[3] = b.y;
+      }
+  }
+}
+
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
+    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+    const uint16_t* __restrict__ q, const TreeParams prm) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  FewSmem& sm = *reinterpret_cast<FewSmem*>(
+      smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g8 = lane >> 2;
+  const int qq = lane & 3;
+  const int kvh = blockIdx.x % kHkv;
+  pkv_decode::PageRing<kFewStages>& ring = sm.warp[warp];
+  unsigned long long* bars = sm.bar[warp];
+  // the kernel that joins the parts may be made ready (it waits for this one's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // every warp walks the line for itself
+  TreeWalk<kFewTokens> walk;
+  walk.fetch(prm, lane);
+  if (lane == 0) {
+    for (int s = 0; s < kFewStages; ++s) mbar_init(&bars[s], 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      pkv_decode::prefetch_tensormap(&tmap_k);
+      pkv_decode::prefetch_tensormap(&tmap_v);
+      sm.abort = 0;
+    }
+  }
+  __syncwarp();
+
+  uint32_t used = 0;                  // pages that went through the ring
+  TreeWork work;
+  while (walk.next(0, prm, lane, work)) {
+    const TreeView view(work, prm);
+    const int mine = work.steps;      // this warp's pages: one of every step
+    const int32_t* row = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
+    auto list_at = [&](int j) { return (work.step + j) * kStepPages + warp; };
+    // physical ids of 32 of this warp's pages, one per lane (the next 32 on their
+    // way): -1 invalid, -2 no such page or no token that counts
+    auto fetch_ids = [&](int base) {
+      int id = -2;
+      if (base + lane < mine && view.has_page(list_at(base + lane))) {
+        id = __ldg(row + view.page(list_at(base + lane)));
+        if (id < 0 || id >= prm.num_pages) id = -1;
+      }
+      return id;
+    };
+    int ids = fetch_ids(0);
+    int ids_next = fetch_ids(32);
+    // the rows and what they see, for all warps: fragment c of lane (g, q) holds dims
+    // 16 q + 8 (c % 2) .. + 7 of row 16 (c / 4) + 8 (c / 2 % 2) + g
+    #pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = 2 * warp + e;
+      const int r = 16 * (c >> 2) + 8 * (c >> 1 & 1) + g8;
+      const int token = work.row + min(r >> 2, work.count - 1);   // past the end: the last one's
+      sm.q[c][lane] = __ldg(reinterpret_cast<const uint4*>(
+          q + (static_cast<size_t>(token) * kHq + kvh * kGroup + (r & 3)) * kDim + 16 * qq +
+          8 * (c & 1)));
+    }
+    if (threadIdx.x < kFewTokens)
+      sm.mask[threadIdx.x] = prm.tree[work.row + min(static_cast<int>(threadIdx.x),
+                                                     work.count - 1)];
+    // Copy engine: K and V of page j into its stage, from lanes 0 and 1.
+    auto issue = [&](int j) {
+      const int stage = (used + j) % kFewStages;
+      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+      if (id == -1 && lane == 0) set_error(prm.err, PKV_DEV_ERR_PAGE);
+      if (lane > 1) return;
+      if (id >= 0) {
+        if (lane == 0) mbar_arrive_expect_tx(&bars[stage], 2 * kFewTileBytes);
+        __syncwarp(0x3u);   // the expected bytes are set before either copy can land
+        pkv_decode::tma_load_tile(lane == 0 ? ring.k[stage] : ring.v[stage],
+                                  lane == 0 ? &tmap_k : &tmap_v, kvh * kPage, id, &bars[stage]);
+      } else if (lane == 0) {
+        mbar_arrive(&bars[stage]);
+      }
+    };
+    int issued = min(mine, kFewStages);
+    uint32_t good = __ballot_sync(0xffffffffu, ids >= 0);   // of the 32 pages in `ids`
+    uint32_t good_now = good;                               // ... of the 32 being attended
+    for (int j = 0; j < issued; ++j) issue(j);
+    __syncthreads();
+
+    FewState st;
+    st.reset();
+    int landed = 0;
+    bool timed_out = sm.abort != 0;
+    for (int j = 0; j < mine && !timed_out; ++j) {
+      const uint32_t at = used + j;
+      const int stage = at % kFewStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[stage], at / kFewStages & 1u))) {
+        timed_out = true;
+        break;
+      }
+      landed = j + 1;
+      if ((j & 31) == 0) good_now = good;
+      if (good_now >> (j & 31) & 1u) {
+        const int i = list_at(j);
+        const bool whole = i >= view.whole_from && i < view.whole_to;
+        uint32_t seen[4] = {0xffffu, 0xffffu, 0xffffu, 0xffffu};
+        if (!whole) {
+          const int base = view.page(i) * kPage;
+          uint8_t* vt = ring.v[stage];
+          bool cleared = false;
+          for (int idx = lane; idx < kPage * 8; idx += 32)
+            if (view.dead(base + (idx >> 3))) {
+              *reinterpret_cast<uint4*>(vt + idx * 16) = make_uint4(0u, 0u, 0u, 0u);
+              cleared = true;
+            }
+          if (cleared) pkv_prefill_dev::fence_proxy_async_smem();
+          #pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int token = 4 * (r >> 1) + 2 * (r & 1) + (g8 >> 2);
+            seen[r] = TreeRow(work, prm, sm.mask[token]).seen(view, base);
+          }
+          __syncwarp();
+        }
+        if (work.count > kFewTokens / 2)
+          attend_rows<2>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
+        else
+          attend_rows<1>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
+      }
+      __syncwarp();   // every lane's reads of the stage are done before it is refilled
+      const int next = j + kFewStages;
+      if (next < mine) {
+        if ((next & 31) == 0) {
+          ids = ids_next;
+          good = __ballot_sync(0xffffffffu, ids >= 0);
+          ids_next = fetch_ids(next + 32);
+        }
+        issue(next);
+        issued = next + 1;
+      }
+    }
+    if (timed_out) {
+      // this warp's copies in flight land before the block goes on (each wait bounded)
+      for (int j = landed; j < issued; ++j)
+        mbar_wait(&bars[(used + j) % kFewStages], (used + j) / kFewStages & 1u);
+      if (lane == 0) {
+        set_error(prm.err, PKV_DEV_ERR_TIMEOUT);
+        sm.abort = 1;
+      }
+    }
+    used += mine;
+
+    // the warps' sums, each in its own ring (whose copies have all landed)
+    float* acc = reinterpret_cast<float*>(&ring);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + g8;
+      float l = st.l[i];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (qq == 0) {
+        sm.m[warp][r] = st.m[i];
+        sm.l[warp][r] = l;
+      }
+      #pragma unroll
+      for (int n = 0; n < 8; ++n)
+        *reinterpret_cast<float2*>(acc + r * kAccStride + 8 * n + 2 * qq) =
+            make_float2(st.o[i / 2][n][2 * (i % 2)], st.o[i / 2][n][2 * (i % 2) + 1]);
+    }
+    __syncthreads();
+    if (sm.abort) return;             // the same decision in every warp
+    // 8 threads a row, two float4 each, 16 rows at a time
+    #pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      const int r = 16 * pass + (threadIdx.x >> 3), at = threadIdx.x & 7;
+      if (r < work.count * kGroup) {
+        float M = -INFINITY, L = 0.f;
+        #pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, sm.m[w][r]);
+        float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        #pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          const float f = M == -INFINITY ? 0.f : fast_exp2(sm.m[w][r] - M);
+          L += f * sm.l[w][r];
+          const float4* o = reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(&sm.warp[w]) + r * kAccStride) + at;
+          #pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 x = o[8 * h];
+            sum[h].x += f * x.x;
+            sum[h].y += f * x.y;
+            sum[h].z += f * x.z;
+            sum[h].w += f * x.w;
+          }
+        }
+        float4* to;
+        if (work.slot < 0) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          #pragma unroll
+          for (int h = 0; h < 2; ++h)
+            sum[h] = make_float4(sum[h].x * inv, sum[h].y * inv, sum[h].z * inv, sum[h].w * inv);
+          to = reinterpret_cast<float4*>(
+              prm.out + ((static_cast<size_t>(work.row) + (r >> 2)) * kHq + kvh * kGroup +
+                         (r & 3)) * kDim);
+        } else {
+          const size_t at_row = static_cast<size_t>(work.slot) * kFewRowsN + r;
+          to = reinterpret_cast<float4*>(prm.part_o + at_row * kDim);
+          if (at == 0) prm.part_ml[at_row] = make_float2(M, L);
+        }
+        to[at] = sum[0];
+        to[at + 8] = sum[1];
+      }
+    }
+    // the rings are copied into again
+    pkv_prefill_dev::fence_proxy_async_smem();
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+bool pkv_tree_few_setup() {
+  return cudaFuncSetAttribute(tree_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kFewSmemBytes)) == cudaSuccess;
+}
+
+pkv_status pkv_tree_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
+                        const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
+  set_wave(&prm, kFewBlocksPerSm * pool->num_sms);
+  tree_few_kernel<<<prm.wave * kHkv, kFewThreads, kFewSmemBytes, st>>>(
+      tk, tv, static_cast<const uint16_t*>(q), prm);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  return launch_join<kFewTokens>(prm, st);
+}

@@ -94,6 +94,21 @@ def test_ragged_batches(starts, nodes):
     run_tree(starts, nodes, seed=len(starts))
 
 
+@pytest.mark.parametrize("starts,nodes", [
+    # few drafted tokens a sequence on average: one large tree among them, long contexts,
+    # batches of more than 32 sequences
+    ([700, 3, 0, 50] + [90] * 20, [64, 0, 5, 1] + [1] * 20), ([300 + i for i in range(45)], [3] * 45),
+    ([2000, 1, 16], [4, 4, 4]), ([0] * 70, [i % 3 for i in range(70)])])
+@pytest.mark.parametrize("window,sinks", [(2048, 0), (50, 5)])
+def test_few_rows(starts, nodes, window, sinks):
+    run_tree(starts, nodes, window=window, sinks=sinks, seed=len(starts))
+
+
+def test_few_rows_over_long_contexts():
+    run_tree([60000, 33333], [4, 3], max_seq_len=65536)
+    run_tree([60000, 33333], [4, 3], max_seq_len=65536, window=3000, sinks=20)
+
+
 @pytest.mark.parametrize("batch", [39, 65, 150])
 def test_many_sequences(batch):
     rng = np.random.RandomState(batch)
