@@ -105,13 +105,15 @@ __device__ __forceinline__ void unpack8(uint4 v, float2 (&x)[4]) {
 
 // 8 dims of a row rotated: own = dims 8 c .., partner = the other half's (c ^ 4),
 // cs and sn the angles of pairs 8 (c % 4) .., sn negated for the lower half (c <
-// 4: x cos - y sin); products and sum each rounded in FP32 (the
-// _rn intrinsics are never contracted).
+// 4: x cos - y sin); products and sum each rounded in FP32: the scalar _rn
+// intrinsics are never contracted, those on pairs were (one code in four million
+// came out different).
 __device__ __forceinline__ void rotate8(float2 (&x)[4], const float2 (&partner)[4],
                                         const float2 (&cs)[4], const float2 (&sn)[4]) {
   #pragma unroll
   for (int i = 0; i < 4; ++i)
-    x[i] = __fadd2_rn(__fmul2_rn(x[i], cs[i]), __fmul2_rn(partner[i], sn[i]));
+    x[i] = make_float2(__fadd_rn(__fmul_rn(x[i].x, cs[i].x), __fmul_rn(partner[i].x, sn[i].x)),
+                       __fadd_rn(__fmul_rn(x[i].y, cs[i].y), __fmul_rn(partner[i].y, sn[i].y)));
 }
 
 }  // namespace pkv_quant_dev

@@ -95,6 +95,40 @@ def test_rotated_fill_quantises_the_fp32_rotation(axes):
     assert np.array_equal(kv.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("chunk", [16384, 4000, 1])
+def test_rotated_codes_of_many_tokens(chunk):
+    # products and sum each rounded in FP32: a fused multiply-add would change about one
+    # code in a million (8 million here; the last case takes the fused append, 2 million)
+    total = 16384 if chunk > 1 else 4096
+    c = QuantCache([0] * (total if chunk == 1 else 1), max_seq_len=16 if chunk == 1 else 16384,
+                   spare=total // (1 if chunk == 1 else PAGE))
+    pages = c.table.shape[2]
+    c.tables = torch.randperm(c.num_pages, dtype=torch.int32)[:c.table.size].view(c.table.shape).cuda()
+    assert c.tables.numel() == c.num_pages and pages * PAGE == c.max_seq_len
+    pool, kv = handle(c), c.pool()
+    k = normal(1, total, HKV, DIM)
+    cos, sin = angles(20000)
+    pos = torch.randint(0, 20000, (3, total), dtype=torch.int32, device="cuda")
+    rope = pkv.pkv_axes_rope(cos, sin, AXES[3])
+    kb, vb = torch.empty_like(k), torch.empty_like(k)
+    if chunk > 1:
+        for at in range(0, total, chunk):
+            n = min(chunk, total - at)
+            pkv.pkv_quant_fill(pool, 0, k[at:at + n], k[at:at + n], kv, c.tables, int32([0, n]),
+                               int32([at]), n, rope=rope, rope_positions=pos[:, at:at + n].contiguous())
+        cu, start, most = int32([0, total]), int32([0]), total
+    else:
+        q, out = normal(2, total, HQ, DIM), torch.empty(total, HQ, DIM, device="cuda")
+        pkv.pkv_quant_append_attend(pool, 0, q, k, k, kv, c.tables, int32([1] * total), out, 16,
+                                    rope=rope, rope_positions=pos)
+        cu, start, most = int32(np.arange(total + 1)), int32([0] * total), 1
+    pkv.pkv_quant_read(pool, 0, kv, c.tables, cu, start, kb, vb, most)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    turned = rotate(k, cos, sin, pos, AXES[3], torch.float32).double().cpu()
+    assert int((kb.double().cpu() != quantise(turned)[2]).sum()) == 0
+    assert torch.equal(vb.double().cpu(), quantise(k.double().cpu())[2])
+
+
 def special_rows():
     """Rows at the edges of the rule: zeros, powers of two, 448 and its neighbours
     times powers, ties, subnormals, the largest values, one large among small."""
