@@ -53,11 +53,12 @@ constexpr int kCommitThreads = 256;
 constexpr int kHeadVecs = 2 * kRowBytes / 16;                    // K and V of a token: 16
 constexpr int kCommitItems = kMaxTree * kHeadVecs / kCommitThreads;   // 4
 
+template <int heads>
 __global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
     uint4* k_pool, uint4* v_pool, const int32_t* __restrict__ tables,
     const int32_t* __restrict__ start_pos, const int32_t* __restrict__ accepted,
     const int32_t* __restrict__ counts, int max_accepted, int max_batch, int table_stride,
-    int num_pages, int max_seq_len, int heads, int* err) {
+    int num_pages, int max_seq_len, int* err) {
   const int b = blockIdx.y, layer = blockIdx.z;
   const int count = counts[b], start = start_pos[b];
   // item i of this thread: accepted token k(i)'s vector `vec` of head g(i)
@@ -210,12 +211,16 @@ pkv_status pkv_tree_commit(pkv_pool_t pool, void* k_pool, void* v_pool,
   if (cudaGetDevice(&dev) != cudaSuccess || dev != pool->device) return PKV_ERR_INVALID_ARG;
   int heads = kHkv;
   while (heads > 1 && heads * max_accepted > kMaxTree) heads /= 2;
+  const auto kernel = heads == 8   ? tree_commit_kernel<8>
+                      : heads == 4 ? tree_commit_kernel<4>
+                      : heads == 2 ? tree_commit_kernel<2>
+                                   : tree_commit_kernel<1>;
   pool->pages_written = true;
-  tree_commit_kernel<<<dim3(kHkv / heads, batch, c.num_layers), kCommitThreads, 0,
-                       static_cast<cudaStream_t>(stream)>>>(
+  kernel<<<dim3(kHkv / heads, batch, c.num_layers), kCommitThreads, 0,
+           static_cast<cudaStream_t>(stream)>>>(
       static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), block_tables, start_pos, accepted,
       counts, max_accepted, c.max_batch, c.max_seq_len / kPage, c.num_pages, c.max_seq_len,
-      heads, pool->err);
+      pool->err);
   return pkv_check_launch();
 }
 
