@@ -202,31 +202,6 @@ __device__ __forceinline__ void arrive_lane0(unsigned long long* bar, int lane) 
       : "memory");
 }
 
-// One lane of a converged warp, always the same. The issuing warps run their
-// loops whole and only the tcgen05 instructions under this predicate, so the
-// operands stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-// The largest of three (the last two given as bits).
-__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;"
-      : "=f"(d)
-      : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-  return d;
-}
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
-  return max3(__uint_as_float(a), b, c);
-}
-
 // 16 consecutive columns, complete on return.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(

@@ -80,15 +80,21 @@ __device__ __forceinline__ float row_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
+// -FLT_MAX, no finite score lies below it: with it as the exponent of a row that saw
+// nothing yet, no test for -inf - -inf is needed.
+constexpr float kNone = -0x1.fffffep127f;
+
 struct QuantTiles {
-  static constexpr int kStages = 3;
+  // With 3, 4 sequences of 131,072 tokens take 92 us instead of 84.
+  static constexpr int kStages = 2;
   static constexpr int kStagePages = 2;
   static constexpr int kParts = 1;
   static constexpr uint32_t kCopyBytes = kQuantTile;
   static constexpr size_t kAlign = 128;
   struct alignas(16) Ring {
     uint8_t tile[kStages][kStagePages][kQuantTile];
-    float2 scale[kStagePages * kPage];   // 2^ek, 2^ev of the group's tokens
+    // 2^ek of two neighbouring tokens, then their 2^ev
+    float scale[kStagePages * kPage / 2][4];
   };
   struct Source {
     uint8_t* pool;               // [num_pages][8][kQuantTile]
@@ -102,12 +108,13 @@ struct QuantTiles {
   struct State {
     float o[4][4];   // chunk c: dims 16 c + 2 g (0, 1) and + 1 (2, 3), columns 2 q, 2 q + 1
     float m_run;     // the base-2 exponent p is taken against: p = 2^(x - m_run) <= 1
+                     // (kNone: nothing seen yet)
     float l_run;     // this lane's share of the head's sum
     float unit;      // the power of two that the weights p 2^ev are scaled by
     __device__ __forceinline__ void reset() {
       #pragma unroll
       for (int c = 0; c < 4; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
-      m_run = -INFINITY;
+      m_run = kNone;
       l_run = 0.f;
       unit = 0x1p126f;
     }
@@ -148,7 +155,8 @@ struct QuantTiles {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
         ::"r"(smem_u32(ws.tile[stage][e])),
-          "l"(src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile), "r"(kQuantTile),
+          "l"(src.pool + kvh * kQuantTile + static_cast<size_t>(phys) * (kHkv * kQuantTile)),
+          "r"(kQuantTile),
           "r"(smem_u32(bar))
         : "memory");
   }
@@ -274,7 +282,8 @@ struct QuantTiles {
     for (int nt = 0; nt < kTiles; ++nt)
       kw[nt] = *reinterpret_cast<const uint4*>(ws.tile[stage][nt / 2] +
                                                k_at(8 * (nt % 2) + g8, 16 * qq));
-    ws.scale[lane] = make_float2(scale_of(ek), scale_of(ev));
+    ws.scale[lane / 2][lane % 2] = scale_of(ek);
+    ws.scale[lane / 2][2 + lane % 2] = scale_of(ev);
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
       const uint32_t w[4] = {kw[nt].x, kw[nt].y, kw[nt].z, kw[nt].w};
@@ -299,9 +308,9 @@ struct QuantTiles {
     float2 s[kTiles], scale_v[kTiles], w[kTiles], sum;
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {
-      const float4 sc = *reinterpret_cast<const float4*>(&ws.scale[8 * nt + 2 * qq]);
-      s[nt] = __fmul2_rn(in.s[nt], make_float2(sc.x, sc.z));
-      scale_v[nt] = make_float2(sc.y, sc.w);
+      const float4 sc = *reinterpret_cast<const float4*>(ws.scale[4 * nt + qq]);
+      s[nt] = __fmul2_rn(in.s[nt], make_float2(sc.x, sc.y));
+      scale_v[nt] = make_float2(sc.z, sc.w);
     }
     if (seen != 0xffffffffu) {
       #pragma unroll
@@ -312,8 +321,7 @@ struct QuantTiles {
     }
     const float2 to_log2 = make_float2(q.to_log2, q.to_log2);
     auto exponentials = [&]() {
-      const float mu = st.m_run == -INFINITY ? 0.f : st.m_run;
-      const float2 minus = make_float2(-mu, -mu);
+      const float2 minus = make_float2(-st.m_run, -st.m_run);
       sum = make_float2(0.f, 0.f);
       #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt) {
@@ -404,7 +412,8 @@ struct QuantTiles {
   static __device__ __forceinline__ float largest(const float2 (&x)[kTiles]) {
     float m = fmaxf(x[0].x, x[0].y);
     #pragma unroll
-    for (int i = 1; i < kTiles; ++i) m = fmaxf(fmaxf(m, x[i].x), x[i].y);
+    for (int i = 1; i < kTiles; ++i)
+      m = max3(m, __float_as_uint(x[i].x), __float_as_uint(x[i].y));
     return m;
   }
 

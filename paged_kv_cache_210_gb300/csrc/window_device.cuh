@@ -451,7 +451,9 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   };
   int ids = fetch_ids(0);
   int ids_next = my_pages > 32 ? fetch_ids(32) : -1;
-  auto good_id = [&](int phys) { return phys >= 0 && phys < prm.num_pages; };
+  auto good_id = [&](int phys) {
+    return static_cast<unsigned>(phys) < static_cast<unsigned>(prm.num_pages);
+  };
   float ang_c = 1.f, ang_s = 0.f;                        // the angle of pair `lane`
   if (kRope && !load_pair_angle(prm.rope, rope_pos, lane, ang_c, ang_s)) {
     if (split == 0 && kvh == 0 && threadIdx.x == 0) set_error(prm.err, kErrPosition);
@@ -464,22 +466,38 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
 
   // Copy engine: the pages of group j into `stage`, one copy per lane. A page
   // whose only token is the appended one (fused) is not copied.
-  uint32_t stage_ok = 0;                      // bit kPer s + e: stage s holds a valid page e
+  uint32_t stage_bad = 0;                     // bit kPer s + e: page e of stage s is invalid
   bool some_bad = false;                      // some page had an invalid id
   auto issue_copy = [&](int j, int stage) {
     constexpr uint32_t kGroup1 = (1u << kPer) - 1u;
     const int l0 = j * kPer;
     const int there = min(my_pages - l0, kPer);
+    if constexpr (kPer == 2) {
+      // both pages there and nothing unusual: one lane issues both copies, all lanes
+      // compute their addresses (operands of a lane's own take a loop over the lanes)
+      const int p0 = __shfl_sync(0xffffffffu, ids, l0 & 31);
+      const int p1 = __shfl_sync(0xffffffffu, ids, (l0 + 1) & 31);
+      if (there == 2 && good_id(p0) && good_id(p1) && !some_bad &&
+          !(kFused && j == j_new && new_slot == 0)) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bars[stage], 2 * Tiles::kCopyBytes);
+          Tiles::copy(ws, stage, 0, src, 0, kvh, p0, &bars[stage]);
+          Tiles::copy(ws, stage, 1, src, 0, kvh, p1, &bars[stage]);
+        }
+        __syncwarp();
+        return;
+      }
+    }
     const int e = kPer == 1 ? 0 : lane;
     const int phys = __shfl_sync(0xffffffffu, ids, (l0 + e) & 31);
     const bool ok = good_id(phys);
     const uint32_t valid = kPer == 1 ? ok : __ballot_sync(0xffffffffu, e < there && ok);
-    stage_ok = (stage_ok & ~(kGroup1 << (kPer * stage))) | valid << (kPer * stage);
+    const uint32_t all = (1u << there) - 1u;
+    stage_bad = (stage_bad & ~(kGroup1 << (kPer * stage))) | (all & ~valid) << (kPer * stage);
     uint32_t copied = valid;
     if (kFused && j == j_new && new_slot == 0) copied &= ~(1u << (l_new - l0));
-    const bool bad = valid != (1u << there) - 1u;
-    some_bad |= bad;
-    if (bad && lane == 0) set_error(prm.err, kErrPage);
+    some_bad |= valid != all;
+    if (valid != all && lane == 0) set_error(prm.err, kErrPage);
     if (lane >= kPer * kParts) return;
     if (copied) {
       if (lane == 0) mbar_arrive_expect_tx(&bars[stage], __popc(copied) * Tiles::kCopyBytes);
@@ -516,8 +534,8 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
     const bool serves = j < n_prefetch && l < my_pages && (kFused || j != j_new);
     const bool copies = serves && ok && !(kFused && l == l_new && new_slot == 0);
     const int held = min(my_pages, kStages * kPer);
-    stage_ok = __ballot_sync(0xffffffffu, lane < held && good_id(ids));
-    some_bad = stage_ok != (1u << held) - 1u;
+    stage_bad = __ballot_sync(0xffffffffu, lane < held && !good_id(ids));
+    some_bad = stage_bad != 0;
     const uint32_t all = __ballot_sync(0xffffffffu, copies && lane % kParts == 0);
     if (serves && lane % kParts == 0 && !ok) set_error(prm.err, kErrPage);
     if (j < n_prefetch && (kFused || j != j_new) && lane % (kPer * kParts) == 0) {
@@ -573,7 +591,8 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
         if (t0 + kPage > len || t0 < win_lo)
           bits = low_bits(len - t0) &
                  (low_bits(prm.sinks - t0) | (0xffffu & ~low_bits(win_lo - t0)));
-        if (!((stage_ok >> (kPer * stage + e)) & 1u)) bits = 0;
+        if ((stage_bad >> (kPer * stage + e)) & 1u) bits = 0;
+        if (kPer > 1 && j * kPer + e >= my_pages) bits = 0;     // no page of this warp's
         seen |= bits << (kPage * e);
       }
     }
