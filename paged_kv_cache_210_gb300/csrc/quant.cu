@@ -6,6 +6,23 @@
 // A tile's codes c stand for c 2^e, e one exponent a token (K_t = c_t 2^ek_t, V_t
 // = d_t 2^ev_t), so with the codes as exact FP16 operands
 //   score_t = 2^ek_t (q . c_t),   out = sum_t (p_t 2^ev_t) d_t / sum_t p_t.
+//
+// What bounds it: the bytes of the visible tiles, 2,080 per (page, KV head), while
+// a warp's instructions keep up: a tile takes half as long to arrive as a BF16 one
+// and its codes have to be widened, so the arithmetic per page had to come down.
+// Four sequences of 120,000 to 131,072 tokens, step by step: 131 us with one page
+// at a time; 95.5 with two (one barrier, one vote and one set of unpacked exponents
+// for 32 tokens, arithmetic on pairs of FP32 values); 93.7 with groups seen whole
+// told by one comparison and the weights split by mixed-precision multiply-adds; 90
+// with one vote per group instead of two, exponentials taken before it; 84 (6.2 TB/s,
+// 93 % of the measured copy rate, 2 us more than the copies alone) with copies issued
+// by one lane from uniform operands and two stages a warp instead of three. 256 ragged
+// sequences behind 4,096 tokens, append and rotation included, take 68 us (77 %; the
+// short sequences' blocks are latency), 64 of up to 2,048 tokens 11.6 us, of which the
+// unit search, page ids, the first copies and the merge are 8, one of 2,048 4.5 us.
+// (Inputs larger than L2 in total, launches in a graph.) Slower: five blocks an SM (by
+// 7 to 20 %), scores computed ahead beside the products before them (2 % faster over
+// long contexts, 3 to 6 % slower in ragged batches).
 
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -11,6 +11,13 @@
 // four warps like the decode's: each takes every fourth page through its own ring of
 // tiles and does all 32 rows' products by warp-wide mma.sync, which needs no set-up.
 // The tiles' steps (four pages, one per warp) are shared out and joined as in tree.cu.
+//
+// What bounds it: mma.sync, 64 products a page for 32 rows and 32 for up to 16 (three
+// BF16 terms of the weights), 8 cycles each on a quarter of an SM: three warps there
+// take a page each in about 2,000 cycles, 1,536 of them products, where the decode's
+// four rows hide under the copies. So it serves few tokens: one tree of 8 over 2,000
+// tokens 9.7 us (tcgen05 11.7), 128 trees of 4 over 2,000 123 us (140; the bytes alone
+// 80); which calls it takes is decided in tree.cu.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
