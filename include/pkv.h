@@ -106,9 +106,10 @@ typedef struct {
  * between them or leave this flag off.) The handle's own calls that write
  * pages or tables between steps, pkv_copy_pages, pkv_compact_pages,
  * pkv_prefill_fill_axes, pkv_quant_fill and pkv_tree_commit, may come immediately
- * before a decode launch: the first one called after them waits for the kernel before it to complete. (That
- * goes by the order of the calls: where a graph's replay puts a decode launch
- * right behind such a call captured elsewhere, the contract is the caller's.)
+ * before a decode launch: the first one called after them waits for the kernel
+ * before it to complete. (That goes by the order of the calls: where a graph's
+ * replay puts a decode launch right behind such a call captured elsewhere, the
+ * contract is the caller's.)
  * Off by default. */
 #define PKV_FLAG_PDL 1
 
@@ -116,8 +117,9 @@ typedef struct {
  * PKV_MAX_LONG_CONTEXT. Where max_seq_len exceeds 2,048 it serves the calls
  * without a context limit of their own: pkv_append, pkv_append_rope,
  * pkv_prefill_fill, and those of pkv_window.h, pkv_axes.h, pkv_pages.h,
- * pkv_quant.h and pkv_tree.h; the other attention calls return PKV_ERR_UNSUPPORTED (pkv_plan_decode INVALID_ARG),
- * and pkv_prefill does so before it fills. */
+ * pkv_quant.h and pkv_tree.h; the other attention calls return
+ * PKV_ERR_UNSUPPORTED (pkv_plan_decode INVALID_ARG), and pkv_prefill does so before
+ * it fills. */
 #define PKV_FLAG_LONG_CONTEXT 2
 #define PKV_MAX_LONG_CONTEXT 1048576
 
