@@ -140,11 +140,19 @@ struct TreeLane {
 
   // Sequence b: steps 0 if there is none or its data is bad.
   __device__ __forceinline__ void load(const TreeParams& prm, int b, bool report) {
-    steps = nodes = row0 = start = 0;
-    if (b >= prm.batch) return;
-    row0 = prm.cu_tokens[b];
-    const int rows = prm.cu_tokens[b + 1] - row0;
-    start = prm.start_pos[b];
+    set(prm, lists(prm, b), report);
+  }
+  // The same in two parts, to have several sequences' lists on their way: its first
+  // row, the row after its last, and its committed tokens.
+  static __device__ __forceinline__ int3 lists(const TreeParams& prm, int b) {
+    return b < prm.batch ? make_int3(prm.cu_tokens[b], prm.cu_tokens[b + 1], prm.start_pos[b])
+                         : make_int3(0, 0, 0);
+  }
+  __device__ __forceinline__ void set(const TreeParams& prm, int3 lists, bool report) {
+    steps = nodes = 0;
+    row0 = lists.x;
+    start = lists.z;
+    const int rows = lists.y - row0;
     const bool bad_rows = row0 < 0 || rows < 0 || rows > prm.total_tokens - row0 || rows > kMaxTree;
     const bool bad_start = !bad_rows && rows > 0 &&
                            (start < 0 || start > prm.max_seq_len || rows > prm.max_seq_len - start);
@@ -202,20 +210,48 @@ struct TreeWalk {
     base = 0;
     take(lane);
     long long total = here;
+    int group = lane == 0 ? here : 0;     // cost of the lane-th 32 sequences (of the first 1,024)
     if (prm.batch > 32) {
+      constexpr int kAhead = 4;
       long long rest = 0;
-      for (int b = 32; b < prm.batch; b += 32) {
-        TreeLane<kTile> other;
-        other.load(prm, b + lane, blockIdx.x == 0);
-        rest += other.cost();
+      for (int g = 1; g * 32 < prm.batch; g += kAhead) {
+        int3 lists[kAhead];
+        #pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          lists[e] = TreeLane<kTile>::lists(prm, (g + e) * 32 + lane);
+        #pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          TreeLane<kTile> other;
+          other.set(prm, lists[e], blockIdx.x == 0);
+          const int cost = __reduce_add_sync(0xffffffffu, other.cost());
+          if (lane == g + e) group = cost;
+          rest += cost;
+        }
       }
-      total += warp_sum(rest);
+      total += rest;
     }
     at = end = 0;
     shares.set(total, prm);
     if (cta >= prm.wave) return;
     at = shares.begin(cta, prm);
     end = min(shares.begin(cta + 1, prm), total);
+    if (prm.batch > 32) {
+      // on to the 32 sequences that hold the first place (or to the last of the 1,024)
+      int incl = group;                   // 1,024 x 8 x (2^14 + 3) at most
+      #pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const uint32_t behind = __ballot_sync(0xffffffffu, at < incl);
+      const int g = behind ? __ffs(behind) - 1 : 31;
+      if (g > 0) {
+        first = 32 * g;
+        base = __shfl_sync(0xffffffffu, incl - group, g);
+        mine.load(prm, first + lane, false);
+        take(lane);
+      }
+    }
   }
 
   // The next part, false when there is none. Called by a whole warp.
@@ -317,21 +353,32 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
   // this launch must not complete before the one ahead of it, even if nothing is
   // to be joined: the launch after it waits for this one alone
   if (b == 0 && tile == 0 && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // where the tile lies on the line, from the lists alone
-  const int lane = threadIdx.x & 31;
-  long long all = 0, before = 0;
-  for (int s = 0; s < prm.batch; s += 32) {
-    TreeLane<kTile> other;
-    other.load(prm, s + lane, false);
-    all += other.cost();
-    before += s + lane < b ? other.cost() : 0;
-  }
-  all = warp_sum(all);
-  before = warp_sum(before);
   TreeLane<kTile> seq;
   seq.load(prm, b, false);
   const int first_token = tile * kTile + quarter * 8;
   if (first_token >= seq.nodes) return;
+  // where the tile lies on the line, from the lists alone
+  __shared__ long long sums[2][kJoinThreads / 32];
+  long long all = 0, before = 0;
+  for (int s = threadIdx.x; s < prm.batch; s += kJoinThreads) {
+    TreeLane<kTile> other;
+    other.load(prm, s, false);
+    all += other.cost();
+    before += s < b ? other.cost() : 0;
+  }
+  all = warp_sum(all);
+  before = warp_sum(before);
+  if ((threadIdx.x & 31) == 0) {
+    sums[0][threadIdx.x >> 5] = all;
+    sums[1][threadIdx.x >> 5] = before;
+  }
+  __syncthreads();
+  all = before = 0;
+  #pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    all += sums[0][w];
+    before += sums[1][w];
+  }
   TreeShares shares;
   shares.set(all, prm);
   const long long from = before + tile * (seq.steps + kTileCost) + kTileCost;

@@ -104,6 +104,16 @@ def test_few_rows(starts, nodes, window, sinks):
     run_tree(starts, nodes, window=window, sinks=sinks, seed=len(starts))
 
 
+@pytest.mark.parametrize("most", [1, 12])
+def test_batches_past_1024_sequences(most):
+    rng = np.random.RandomState(most)
+    starts = [int(x) for x in rng.randint(0, 40, 1300)]
+    starts[1290], starts[1100], starts[40] = 900, 0, 500
+    nodes = [int(x) for x in rng.randint(0, most + 1, 1300)]
+    nodes[1290] = nodes[1] = 20
+    run_tree(starts, nodes, max_seq_len=1024, seed=most)
+
+
 def test_few_rows_over_long_contexts():
     run_tree([60000, 33333], [4, 3], max_seq_len=65536)
     run_tree([60000, 33333], [4, 3], max_seq_len=65536, window=3000, sinks=20)
