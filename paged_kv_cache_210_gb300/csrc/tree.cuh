@@ -341,105 +341,139 @@ struct TreeRow {
 };
 
 // ---------------------------------------------------------------- parts joined
-// 8 drafted tokens of a tile and KV head (32 rows) per block, 8 threads a row, two
-// float4 each: sum_s 2^(m_s - M) o_s over the parts, divided by the same of l_s.
+// There are fewer cut tiles than CTAs: a block per CTA c and KV head looks where c
+// begins and, if that is the first cut in its tile, joins the tile's rows, 8 threads a
+// row, two float4 each: sum_s 2^(m_s - M) o_s over the parts, divided by the same of
+// l_s. (With a block per sequence and tile, most of them without work, 4,096 trees
+// of 2 took 1,018 us instead of 392, 128 of 4 over 2,000 tokens 102 instead of 93.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 8;       // parts whose sums are loaded at once
 
 template <int kTile>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams prm) {
-  const int b = blockIdx.z, tile = blockIdx.y;
-  const int g = blockIdx.x % kHkv, quarter = blockIdx.x / kHkv;
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams prm,
+                                                                 int split) {
+  constexpr int kWarps = kJoinThreads / 32;
+  const int g = blockIdx.x % kHkv, c = blockIdx.x / (kHkv * split);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this launch must not complete before the one ahead of it, even if nothing is
   // to be joined: the launch after it waits for this one alone
-  if (b == 0 && tile == 0 && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c == 0) {
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  // the line's length, a thread's sequences being threadIdx.x, + 256, ...
+  __shared__ long long sums[kWarps];
+  __shared__ int scan[2][kWarps];
+  __shared__ int4 found;              // row0, nodes, steps, place in the sequence
   TreeLane<kTile> seq;
-  seq.load(prm, b, false);
-  const int first_token = tile * kTile + quarter * 8;
-  if (first_token >= seq.nodes) return;
-  // where the tile lies on the line, from the lists alone
-  __shared__ long long sums[2][kJoinThreads / 32];
-  long long all = 0, before = 0;
-  for (int s = threadIdx.x; s < prm.batch; s += kJoinThreads) {
+  seq.load(prm, threadIdx.x, false);
+  long long total = seq.cost();
+  for (int s = threadIdx.x + kJoinThreads; s < prm.batch; s += kJoinThreads) {
     TreeLane<kTile> other;
     other.load(prm, s, false);
-    all += other.cost();
-    before += s < b ? other.cost() : 0;
+    total += other.cost();
   }
-  all = warp_sum(all);
-  before = warp_sum(before);
-  if ((threadIdx.x & 31) == 0) {
-    sums[0][threadIdx.x >> 5] = all;
-    sums[1][threadIdx.x >> 5] = before;
-  }
+  total = warp_sum(total);
+  if (lane == 0) sums[warp] = total;
   __syncthreads();
-  all = before = 0;
+  total = 0;
   #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    all += sums[0][w];
-    before += sums[1][w];
-  }
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
   TreeShares shares;
-  shares.set(all, prm);
-  const long long from = before + tile * (seq.steps + kTileCost) + kTileCost;
-  const int cta = shares.owner(from, prm);
-  const int parts = shares.owner(from + seq.steps - 1, prm) - cta + 1;
-  if (parts <= 1) return;
-  const int r = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
-  const int token = first_token + (r >> 2);
-  if (token >= seq.nodes) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int row = quarter * 32 + r;
-  // part 0 in slot 2 cta + 1, part s in slot 2 (cta + s)
-  auto slot = [&](int s) {
-    return static_cast<size_t>((2 * (cta + s) + (s == 0 ? 1 : 0)) * kHkv + g) * (kTile * kGroup) + row;
-  };
-  const float4* o = reinterpret_cast<const float4*>(prm.part_o) + lane8;
-  float m = -INFINITY, l = 0.f;
-  float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int s = 0; s < parts; s += kJoinAhead) {
-    float2 x[kJoinAhead];
-    float4 v[kJoinAhead][2];
+  shares.set(total, prm);
+  const long long place = shares.begin(c, prm);
+  if (place >= total) return;
+  // the sequence that holds the place
+  long long base = 0;
+  for (int s0 = 0, turn = 0;; s0 += kJoinThreads, turn ^= 1) {
+    if (s0 > 0) seq.load(prm, s0 + threadIdx.x, false);
+    const int own = seq.cost();
+    int incl = own;                   // 256 x 8 x (2^14 + 3) at most
     #pragma unroll
-    for (int e = 0; e < kJoinAhead; ++e) {
-      const bool is = s + e < parts;
-      const size_t at = is ? slot(s + e) : 0;
-      x[e] = is ? __ldcg(prm.part_ml + at) : make_float2(-INFINITY, 0.f);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) scan[turn][warp] = incl;
+    __syncthreads();
+    int group = 0;
+    #pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += scan[turn][w];
+      group += scan[turn][w];
+    }
+    if (place < base + group) {       // the same decision in every thread
+      const int in = static_cast<int>(place - base);
+      if (in >= incl - own && in < incl)
+        found = make_int4(seq.row0, seq.nodes, seq.steps, in - (incl - own));
+      __syncthreads();
+      break;
+    }
+    base += group;
+  }
+  const int row0 = found.x, nodes = found.y, steps = found.z;
+  const int tile = found.w / (steps + kTileCost);
+  const long long from = place - found.w + tile * (steps + kTileCost) + kTileCost;   // its steps
+  // inside the tile's steps, and CTA c - 1 began at or before them
+  if (place - from < 1 || place - from >= steps || shares.begin(c - 1, prm) - from >= 1) return;
+  const int cta = c - 1;
+  const int parts = shares.owner(from + steps - 1, prm) - cta + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane8 = threadIdx.x & 7;
+  const int rows = min(kTile, nodes - tile * kTile) * kGroup;
+  for (int row = blockIdx.x / kHkv % split * (kJoinThreads / 8) + (threadIdx.x >> 3); row < rows;
+       row += split * (kJoinThreads / 8)) {
+    // part 0 in slot 2 cta + 1, part s in slot 2 (cta + s)
+    auto slot = [&](int s) {
+      return static_cast<size_t>((2 * (cta + s) + (s == 0 ? 1 : 0)) * kHkv + g) * (kTile * kGroup) + row;
+    };
+    const float4* o = reinterpret_cast<const float4*>(prm.part_o) + lane8;
+    float m = -INFINITY, l = 0.f;
+    float4 sum[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int s = 0; s < parts; s += kJoinAhead) {
+      float2 x[kJoinAhead];
+      float4 v[kJoinAhead][2];
+      #pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const bool is = s + e < parts;
+        const size_t at = is ? slot(s + e) : 0;
+        x[e] = is ? __ldcg(prm.part_ml + at) : make_float2(-INFINITY, 0.f);
+        #pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[e][h] = is ? __ldcg(o + at * (kDim / 4) + 8 * h)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float m_new = m;
+      #pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) m_new = fmaxf(m_new, x[e].x);
+      if (m_new == -INFINITY) continue;
+      const float a = fast_exp2(m - m_new);            // 0 while nothing was joined
+      l *= a;
       #pragma unroll
       for (int h = 0; h < 2; ++h)
-        v[e][h] = is ? __ldcg(o + at * (kDim / 4) + 8 * h)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        sum[h] = make_float4(sum[h].x * a, sum[h].y * a, sum[h].z * a, sum[h].w * a);
+      #pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float w = fast_exp2(x[e].x - m_new);     // 0 for an absent part
+        l += w * x[e].y;
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sum[h].x += w * v[e][h].x;
+          sum[h].y += w * v[e][h].y;
+          sum[h].z += w * v[e][h].z;
+          sum[h].w += w * v[e][h].w;
+        }
+      }
+      m = m_new;
     }
-    float m_new = m;
-    #pragma unroll
-    for (int e = 0; e < kJoinAhead; ++e) m_new = fmaxf(m_new, x[e].x);
-    if (m_new == -INFINITY) continue;
-    const float a = fast_exp2(m - m_new);            // 0 while nothing was joined
-    l *= a;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    float4* to = reinterpret_cast<float4*>(
+                     prm.out + ((static_cast<size_t>(row0) + tile * kTile + (row >> 2)) * kHq + g * kGroup +
+                                (row & 3)) * kDim) + lane8;
     #pragma unroll
     for (int h = 0; h < 2; ++h)
-      sum[h] = make_float4(sum[h].x * a, sum[h].y * a, sum[h].z * a, sum[h].w * a);
-    #pragma unroll
-    for (int e = 0; e < kJoinAhead; ++e) {
-      const float w = fast_exp2(x[e].x - m_new);     // 0 for an absent part
-      l += w * x[e].y;
-      #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sum[h].x += w * v[e][h].x;
-        sum[h].y += w * v[e][h].y;
-        sum[h].z += w * v[e][h].z;
-        sum[h].w += w * v[e][h].w;
-      }
-    }
-    m = m_new;
+      to[8 * h] = make_float4(sum[h].x * inv, sum[h].y * inv, sum[h].z * inv, sum[h].w * inv);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  float4* to = reinterpret_cast<float4*>(
-                   prm.out + ((static_cast<size_t>(seq.row0) + token) * kHq + g * kGroup +
-                              (r & 3)) * kDim) + lane8;
-  #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    to[8 * h] = make_float4(sum[h].x * inv, sum[h].y * inv, sum[h].z * inv, sum[h].w * inv);
 }
 
 // ---------------------------------------------------------------- host
@@ -447,8 +481,10 @@ template <int kTile>
 pkv_status launch_join(const TreeParams& prm, cudaStream_t st) {
   // the join's blocks start as the attention's CTAs end, and wait for the last
   cudaLaunchConfig_t cfg = {};
-  const int tiles = std::min((prm.total_tokens + kTile - 1) / kTile, kMaxTree / kTile);
-  cfg.gridDim = dim3(kHkv * (kTile / 8), tiles, prm.batch);
+  // blocks that share a cut tile's rows: more where there are few tiles (one sequence
+  // of 64, us: 4 blocks 15.6, 2 16.8, 1 21.3; 32 of up to 16: 21.4, 20.8, 21.1)
+  const int split = kTile == 8 ? 1 : prm.batch <= 2 ? 4 : 2;
+  cfg.gridDim = dim3(prm.wave * kHkv * split);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -456,7 +492,7 @@ pkv_status launch_join(const TreeParams& prm, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<kTile>, prm) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<kTile>, prm, split) != cudaSuccess) return PKV_ERR_CUDA;
   return pkv_check_launch();
 }
 
