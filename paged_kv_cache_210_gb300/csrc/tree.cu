@@ -9,12 +9,12 @@
 //
 // What bounds it: over long contexts the softmax warps, as in windowed prefill: a
 // step of two CTAs takes about 2,000 cycles. Eight trees of 49 to 64 tokens over
-// 20,000 to 32,700: 203 us, 464 TFLOP/s of score and value products counted once (254
+// 20,000 to 32,700: 205 us, 460 TFLOP/s of score and value products counted once (254
 // with parts of one length for a launch, a fifth of the CTAs idle at the end; 217 with
 // the parts joined by the last of a tile, in the same launch). A small call is latency:
-// of 32 trees of up to 16 tokens over up to 2,000, 23 us, a CTA needs 4.4 before its
+// of 32 trees of up to 16 tokens over up to 2,000, 21 us, a CTA needs 4.4 before its
 // first scores (set-up, its share of the line, page ids, copies), 0.7 a step, 2 at a
-// tile's end; the join 2.5.
+// tile's end; the join 2.
 //
 // The commit moves 128-byte rows: 256 sequences of up to 8 tokens in 16 layers 19.8 us
 // (3.8 TB/s of scattered rows; 21.8 with divisions by a launch's number of heads), one
@@ -131,14 +131,14 @@ __global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
 }
 
 // Whether the kernel for few rows takes the call. Measured (us, this and the other
-// kernel; sequences x drafted tokens, 2,000 committed): 1 x 1 8.0 and 10.6, 1 x 4 8.2
-// and 11.0, 8 x 4 13.1 and 17.0, 128 x 4 123 and 140; 1 x 8 9.6 and 11.7, 8 x 8 16.8
-// and 17.5, 16 x 8 25.7 and 24.6, 32 x 8 43.7 and 39.9, at 16,000 committed 1 x 8
-// 21.6 and 19.7; 32 x 16 26.6 and 23.0.
+// kernel; sequences x drafted tokens, 2,000 committed): 1 x 1 7.2 and 11.1, 1 x 4 7.5
+// and 11.6, 8 x 4 13.0 and 17.1, 128 x 4 93 and 119; 1 x 8 8.9 and 12.3, 8 x 8 16.1
+// and 17.7, 32 x 8 39.2 and 40.1; 1 x 16 9.8 and 13.2, 4 x 16 15.7 and 15.1. Over
+// 16,000 committed tokens 1 x 8 takes 21.7 and 19.6.
 bool few_rows(int max_seq_len, int batch, int total_tokens) {
   const long long mean4 = 4ll * batch;
   return total_tokens <= mean4 ||
-         (total_tokens <= 2 * mean4 && total_tokens <= kMaxTree && max_seq_len <= 2048);
+         (max_seq_len <= 2048 && total_tokens <= std::max(2 * mean4, 16ll));
 }
 
 }  // namespace

@@ -192,7 +192,7 @@ struct TreeWalk {
   }
 
   __device__ __forceinline__ void take(int lane) {
-    int incl = mine.cost();       // 32 x 8 x (2^14 + 3) at most
+    int incl = mine.cost();       // 32 x 16 x (2^14 + 3) at most
     const int own = incl;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -237,7 +237,7 @@ struct TreeWalk {
     end = min(shares.begin(cta + 1, prm), total);
     if (prm.batch > 32) {
       // on to the 32 sequences that hold the first place (or to the last of the 1,024)
-      int incl = group;                   // 1,024 x 8 x (2^14 + 3) at most
+      int incl = group;                   // 1,024 x 16 x (2^14 + 3) at most
       #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -271,8 +271,8 @@ struct TreeWalk {
                                                             place < before_me + mine.cost())) - 1;
       const int steps = __shfl_sync(0xffffffffu, mine.steps, from);
       const int in = place - __shfl_sync(0xffffffffu, before_me, from);
-      // in / (steps + kTileCost), below 8: (in + 1/2) / d is 1 / (2 d) > 2^-16 away from
-      // an integer, the error below 2^-19
+      // in / (steps + kTileCost), below 16: (in + 1/2) / d is 1 / (2 d) > 2^-16 away from
+      // an integer, the error below 2^-18
       const int tile = static_cast<int>(__fdividef(static_cast<float>(in) + 0.5f,
                                                    static_cast<float>(steps + kTileCost)));
       const long long tile_at = at - (in - tile * (steps + kTileCost));   // the tile's place
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
   for (int s0 = 0, turn = 0;; s0 += kJoinThreads, turn ^= 1) {
     if (s0 > 0) seq.load(prm, s0 + threadIdx.x, false);
     const int own = seq.cost();
-    int incl = own;                   // 256 x 8 x (2^14 + 3) at most
+    int incl = own;                   // 256 x 16 x (2^14 + 3) at most
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -483,7 +483,7 @@ pkv_status launch_join(const TreeParams& prm, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   // blocks that share a cut tile's rows: more where there are few tiles (one sequence
   // of 64, us: 4 blocks 15.6, 2 16.8, 1 21.3; 32 of up to 16: 21.4, 20.8, 21.1)
-  const int split = kTile == 8 ? 1 : prm.batch <= 2 ? 4 : 2;
+  const int split = kTile <= 8 ? 1 : prm.batch <= 2 ? 4 : 2;
   cfg.gridDim = dim3(prm.wave * kHkv * split);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;

@@ -5,8 +5,8 @@
 // out_i = sum_t p_it V_t / sum_t p_it, p_it = 2^(q_i.K_t log2(e) / 8 - m_i), over
 // the tokens that row i sees: one pass with a running maximum m_i and sum.
 //
-// A tile is up to 8 drafted tokens of a sequence and KV head: 32 rows. That fills a
-// quarter of a tcgen05 product's rows, and a CTA of that kernel takes 5 us before its
+// A tile is up to 4 or 8 drafted tokens of a sequence and KV head: 16 or 32 rows. That
+// fills a quarter of a tcgen05 product's rows at most, and a CTA of that kernel takes 5 us before its
 // first scores (its roles, tensor memory and first instructions). Here a block is
 // four warps like the decode's: each takes every fourth page through its own ring of
 // tiles and does all 32 rows' products by warp-wide mma.sync, which needs no set-up.
@@ -16,8 +16,10 @@
 // BF16 terms of the weights), 8 cycles each on a quarter of an SM: three warps there
 // take a page each in about 2,000 cycles, 1,536 of them products, where the decode's
 // four rows hide under the copies. So it serves few tokens: one tree of 8 over 2,000
-// tokens 9.7 us (tcgen05 11.7), 128 trees of 4 over 2,000 123 us (140; the bytes alone
-// 80); which calls it takes is decided in tree.cu.
+// tokens 8.9 us (tcgen05 12.3), 128 trees of 4 over 2,000 93 us (119; the bytes alone
+// 80); which calls it takes is decided in tree.cu. Many short sequences are bound by the
+// start and the end of their tiles, some 5 us each for a block: 1,024 trees of 4 over
+// 300 tokens 136 us (the bytes 103), 4,096 of 2 over 64 321 (98).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -36,29 +38,38 @@ using namespace pkv_tree_dev;
 
 namespace {
 
-constexpr int kFewTokens = 8;                        // drafted tokens of a tile
-constexpr int kFewRowsN = kFewTokens * kGroup;       // 32
+// A tile of kHalves x 16 rows: 4 or 8 drafted tokens.
+template <int kHalves>
+constexpr int kFewTokens = 16 * kHalves / kGroup;
+template <int kHalves>
+constexpr int kFewRowsN = 16 * kHalves;
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewStages = 3;
-constexpr int kFewBlocksPerSm = 3;
+template <int kHalves>
+constexpr int kFewBlocksPerSm = kHalves == 1 ? 4 : 3;   // by their registers
 constexpr int kFewTileBytes = kPage * kRowBytes;     // K or V of a page: 2 KiB
 constexpr int kAccStride = kDim + 4;                 // floats of a merged row: no bank conflicts
 static_assert(kFewWarps == kStepPages, "a step's pages go to a warp each");
 
+template <int kHalves>
 struct alignas(1024) FewSmem {
   pkv_decode::PageRing<kFewStages> warp[kFewWarps];  // at a part's end: the warp's sums
-  uint4 q[8][32];                                    // the rows as operand fragments, by lane
-  unsigned long long mask[kFewTokens];
+  uint4 q[4 * kHalves][32];                          // the rows as operand fragments, by lane
+  unsigned long long mask[kFewTokens<kHalves>];
   unsigned long long bar[kFewWarps][kFewStages];
-  float m[kFewWarps][kFewRowsN];
-  float l[kFewWarps][kFewRowsN];
+  float m[kFewWarps][kFewRowsN<kHalves>];
+  float l[kFewWarps][kFewRowsN<kHalves>];
   int abort;
 };
-constexpr size_t kFewSmemBytes = sizeof(FewSmem) + 1024;   // + room to align the base
-static_assert(sizeof(pkv_decode::PageRing<kFewStages>) >= kFewRowsN * kAccStride * sizeof(float),
+template <int kHalves>
+constexpr size_t kFewSmemBytes = sizeof(FewSmem<kHalves>) + 1024;   // + room to align the base
+static_assert(sizeof(pkv_decode::PageRing<kFewStages>) >=
+                  kFewRowsN<2> * kAccStride * sizeof(float),
               "a warp's sums fit its ring");
-static_assert(kFewBlocksPerSm * (kFewSmemBytes + 1024) <= 228 * 1024, "blocks per SM");
+static_assert(kFewBlocksPerSm<1> * (kFewSmemBytes<1> + 1024) <= 228 * 1024 &&
+                  kFewBlocksPerSm<2> * (kFewSmemBytes<2> + 1024) <= 228 * 1024,
+              "blocks per SM");
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
@@ -76,32 +87,33 @@ __device__ __forceinline__ float quad_max(float x) {
 // A warp's sums over its pages. Lane (g, q) = (L / 4, L % 4) holds rows 16 t + g
 // (o[t][n][0, 1]) and 16 t + 8 + g ([2, 3]), dims 8 n + 2 q, + 1; row r is drafted
 // token r / 4 of the tile, head r % 4. m and l of row 16 t + 8 h + g in [2 t + h].
+template <int kHalves>
 struct FewState {
-  float o[2][8][4];
-  float m[4];      // base-2 exponent the row's weights are taken against, p <= 2^8
-  float l[4];      // this lane's share of the row's sum
+  float o[kHalves][8][4];
+  float m[2 * kHalves];   // base-2 exponent the row's weights are taken against, p <= 2^8
+  float l[2 * kHalves];   // this lane's share of the row's sum
   __device__ __forceinline__ void reset() {
     #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kHalves; ++t)
       #pragma unroll
       for (int n = 0; n < 8; ++n)
         #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][n][e] = 0.f;
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * kHalves; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
   }
 };
 
-// One page, K tile kt and V tile vt (swizzled). kTiles: 16-row halves that have
-// rows. seen: what each of this lane's rows sees of it, 16 bits, where not `whole`;
+// One page, K tile kt and V tile vt (swizzled). kTiles: halves that have rows. seen: what each of this lane's rows sees of it, 16 bits, where not `whole`;
 // V rows that no row sees hold zeros.
-template <int kTiles>
+template <int kTiles, int kHalves>
 __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt, bool whole,
-                                            const uint32_t (&seen)[4], const uint4 (*q)[32],
-                                            int lane, FewState& st) {
+                                            const uint32_t (&seen)[2 * kHalves],
+                                            const uint4 (*q)[32], int lane,
+                                            FewState<kHalves>& st) {
   const int g8 = lane >> 2;
   const int qq = lane & 3;
   // scores; slice s of the contraction is dims 16 q + 4 s .. + 3 of lane q, so a
@@ -214,11 +226,14 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
   }
 }
 
-__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
+template <int kHalves>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_few_kernel(
     const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
     const uint16_t* __restrict__ q, const TreeParams prm) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  FewSmem& sm = *reinterpret_cast<FewSmem*>(
+  constexpr int kTokens = kFewTokens<kHalves>, kRowsN = kFewRowsN<kHalves>;
+  using Smem = FewSmem<kHalves>;
+  Smem& sm = *reinterpret_cast<Smem*>(
       smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -230,7 +245,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
   // the kernel that joins the parts may be made ready (it waits for this one's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // every warp walks the line for itself
-  TreeWalk<kFewTokens> walk;
+  TreeWalk<kTokens> walk;
   walk.fetch(prm, lane);
   if (lane == 0) {
     for (int s = 0; s < kFewStages; ++s) mbar_init(&bars[s], 1);
@@ -265,15 +280,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
     // the rows and what they see, for all warps: fragment c of lane (g, q) holds dims
     // 16 q + 8 (c % 2) .. + 7 of row 16 (c / 4) + 8 (c / 2 % 2) + g
     #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = 2 * warp + e;
+    for (int e = 0; e < kHalves; ++e) {
+      const int c = kHalves * warp + e;
       const int r = 16 * (c >> 2) + 8 * (c >> 1 & 1) + g8;
       const int token = work.row + min(r >> 2, work.count - 1);   // past the end: the last one's
       sm.q[c][lane] = __ldg(reinterpret_cast<const uint4*>(
           q + (static_cast<size_t>(token) * kHq + kvh * kGroup + (r & 3)) * kDim + 16 * qq +
           8 * (c & 1)));
     }
-    if (threadIdx.x < kFewTokens)
+    if (threadIdx.x < kTokens)
       sm.mask[threadIdx.x] = prm.tree[work.row + min(static_cast<int>(threadIdx.x),
                                                      work.count - 1)];
     // Copy engine: K and V of page j into its stage, from lanes 0 and 1.
@@ -297,7 +312,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
     for (int j = 0; j < issued; ++j) issue(j);
     __syncthreads();
 
-    FewState st;
+    FewState<kHalves> st;
     st.reset();
     int landed = 0;
     bool timed_out = sm.abort != 0;
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
       if (good_now >> (j & 31) & 1u) {
         const int i = list_at(j);
         const bool whole = i >= view.whole_from && i < view.whole_to;
-        uint32_t seen[4] = {0xffffu, 0xffffu, 0xffffu, 0xffffu};
+        uint32_t seen[2 * kHalves];
         if (!whole) {
           const int base = view.page(i) * kPage;
           uint8_t* vt = ring.v[stage];
@@ -325,14 +340,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
             }
           if (cleared) pkv_prefill_dev::fence_proxy_async_smem();
           #pragma unroll
-          for (int r = 0; r < 4; ++r) {
+          for (int r = 0; r < 2 * kHalves; ++r) {
             const int token = 4 * (r >> 1) + 2 * (r & 1) + (g8 >> 2);
             seen[r] = TreeRow(work, prm, sm.mask[token]).seen(view, base);
           }
           __syncwarp();
         }
-        if (work.count > kFewTokens / 2)
-          attend_rows<2>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
+        if (kHalves == 2 && work.count > kTokens / 2)
+          attend_rows<kHalves>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
         else
           attend_rows<1>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
       }
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
     // the warps' sums, each in its own ring (whose copies have all landed)
     float* acc = reinterpret_cast<float*>(&ring);
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * kHalves; ++i) {
       const int r = 8 * i + g8;
       float l = st.l[i];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
     if (sm.abort) return;             // the same decision in every warp
     // 8 threads a row, two float4 each, 16 rows at a time
     #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < kHalves; ++pass) {
       const int r = 16 * pass + (threadIdx.x >> 3), at = threadIdx.x & 7;
       if (r < work.count * kGroup) {
         float M = -INFINITY, L = 0.f;
@@ -412,7 +427,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
               prm.out + ((static_cast<size_t>(work.row) + (r >> 2)) * kHq + kvh * kGroup +
                          (r & 3)) * kDim);
         } else {
-          const size_t at_row = static_cast<size_t>(work.slot) * kFewRowsN + r;
+          const size_t at_row = static_cast<size_t>(work.slot) * kRowsN + r;
           to = reinterpret_cast<float4*>(prm.part_o + at_row * kDim);
           if (at == 0) prm.part_ml[at_row] = make_float2(M, L);
         }
@@ -429,15 +444,31 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) tree_few_kernel(
 }  // namespace
 
 bool pkv_tree_few_setup() {
-  return cudaFuncSetAttribute(tree_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kFewSmemBytes)) == cudaSuccess;
+  return cudaFuncSetAttribute(tree_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kFewSmemBytes<1>)) == cudaSuccess &&
+         cudaFuncSetAttribute(tree_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kFewSmemBytes<2>)) == cudaSuccess;
+}
+
+template <int kHalves>
+static pkv_status launch_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
+                             const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
+  set_wave(&prm, kFewBlocksPerSm<kHalves> * pool->num_sms);
+  tree_few_kernel<kHalves><<<prm.wave * kHkv, kFewThreads, kFewSmemBytes<kHalves>, st>>>(
+      tk, tv, static_cast<const uint16_t*>(q), prm);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  return launch_join<kFewTokens<kHalves>>(prm, st);
 }
 
 pkv_status pkv_tree_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
                         const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
-  set_wave(&prm, kFewBlocksPerSm * pool->num_sms);
-  tree_few_kernel<<<prm.wave * kHkv, kFewThreads, kFewSmemBytes, st>>>(
-      tk, tv, static_cast<const uint16_t*>(q), prm);
-  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
-  return launch_join<kFewTokens>(prm, st);
+  // Tiles of 4 tokens, and a block more per SM, where sequences bring no more on
+  // average and there are several for each block (us, with tiles of 4 and of 8: 4,096
+  // sequences x 2 over 64 committed tokens 321 and 392, 1,024 x 4 over 300 136 and 158,
+  // 256 x 4 over 1,000 94.7 and 99.6; 128 x 4 over 2,000 94.1 and 93.2, 8 x 4 13.7 and
+  // 13.0).
+  const int wave = kFewBlocksPerSm<1> * pool->num_sms / kHkv;
+  return prm.total_tokens <= 4ll * prm.batch && prm.batch >= 2 * wave
+             ? launch_few<1>(pool, q, tk, tv, prm, st)
+             : launch_few<2>(pool, q, tk, tv, prm, st);
 }
