@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           ok = hand_over(work);
           if (!ok) break;
           ++n;
-          ok = load_tile(view, work, ids, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued, kKStages,
-                         false);
+          ok = load_tile(view, work, ids, &tmap_k, sm.k[0], sm.bar_k, sm.k_free, at, issued,
+                         kKStages, false);
           if (!ok) break;
         }
         if (ok) {
@@ -725,7 +725,8 @@ bool set_smem_attribute(int device) {
   if (device < 0 || device >= kMaxDevices) return false;
   std::lock_guard<std::mutex> guard(lock);
   if (!done[device]) {
-    if (cudaFuncSetAttribute(tile_attention_kernel<Job>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(tile_attention_kernel<Job>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes<Job>)) != cudaSuccess)
       return false;
     done[device] = true;

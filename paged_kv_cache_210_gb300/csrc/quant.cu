@@ -38,7 +38,8 @@ using namespace pkv_quant_dev;
 namespace {
 
 // ---------------------------------------------------------------- page math
-// A warp takes two pages at a time. Their products are warp-wide mma.sync m16n8k16 of FP16 operands.
+// A warp takes two pages at a time. Their products are warp-wide mma.sync m16n8k16
+// of FP16 operands.
 //   scores: S = Q K^T, rows = the 4 heads' queries, their high parts in rows 0..3
 //           (again in 4..7) and with rotation their low ones in 8..11 (12..15),
 //           columns = 8 tokens;
@@ -107,7 +108,6 @@ struct QuantTiles {
   static constexpr int kStagePages = 2;
   static constexpr int kParts = 1;
   static constexpr uint32_t kCopyBytes = kQuantTile;
-  static constexpr size_t kAlign = 128;
   struct alignas(16) Ring {
     uint8_t tile[kStages][kStagePages][kQuantTile];
     // 2^ek of two neighbouring tokens, then their 2^ev
@@ -194,8 +194,9 @@ struct QuantTiles {
   // rotated, quantised, into its slot of the pool and of the stage.
   template <bool kRope>
   static __device__ __forceinline__ void put_row(Ring& ws, int stage, int page, const Source& src,
-                                                 int kvh, int slot, int phys, bool to_pool, bool to_stage,
-                                                 uint4 val, float ang_c, float ang_s, int lane) {
+                                                 int kvh, int slot, int phys, bool to_pool,
+                                                 bool to_stage, uint4 val, float ang_c,
+                                                 float ang_s, int lane) {
     const int c = lane & 7;
     float2 x[4];
     unpack8(val, x);
@@ -396,7 +397,8 @@ struct QuantTiles {
       #pragma unroll
       for (int e = 0; e < kStagePages; ++e) {
         uint32_t v[4];
-        ldsm_x4_trans(v, smem_u32(ws.tile[stage][e]) + kCodeBytes + lane * 16 + 2 * j * kChunkBytes);
+        ldsm_x4_trans(v, smem_u32(ws.tile[stage][e]) + kCodeBytes + lane * 16 +
+                             2 * j * kChunkBytes);
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t lo = __byte_perm(v[2 * h], 0u, 0x3120);       // tokens 0..7

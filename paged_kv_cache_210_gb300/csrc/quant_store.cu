@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
   const int head0 = blockIdx.x % kGroups * kFillHeads;
   const int slot = warp * kWarpTokens + lane / 8, c = lane % 8;
   bool valid = slot >= w.first && slot < w.first + w.count;
-  const size_t from = static_cast<size_t>(w.row + slot - w.first) * (kHkv * kDim / 8) + head0 * 8 + c;
+  const size_t from =
+      static_cast<size_t>(w.row + slot - w.first) * (kHkv * kDim / 8) + head0 * 8 + c;
   uint4 kv[2][kFillHeads];
   #pragma unroll
   for (int h = 0; h < kFillHeads; ++h) {
@@ -138,7 +139,8 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
     __syncwarp();
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float4 a = *reinterpret_cast<const float4*>(&angles[warp][lane / 8][8 * (c & 3) + 2 * e]);
+      const float4 a =
+          *reinterpret_cast<const float4*>(&angles[warp][lane / 8][8 * (c & 3) + 2 * e]);
       cs[e] = make_float2(a.x, a.z);
       sn[e] = c < 4 ? make_float2(-a.y, -a.w) : make_float2(a.y, a.w);
     }
@@ -170,7 +172,8 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
       uint2 codes;
       const uint32_t e = quantise_row(x, codes);
       if (!valid) continue;
-      *reinterpret_cast<uint2*>(tile + (which == 0 ? k_at(slot, 8 * c) : v_at(slot, 8 * c))) = codes;
+      const int at = which == 0 ? k_at(slot, 8 * c) : v_at(slot, 8 * c);
+      *reinterpret_cast<uint2*>(tile + at) = codes;
       if (c == 0) tile[(which == 0 ? kKExp : kVExp) + slot] = static_cast<uint8_t>(e);
     }
   }

@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
        row += split * (kJoinThreads / 8)) {
     // part 0 in slot 2 cta + 1, part s in slot 2 (cta + s)
     auto slot = [&](int s) {
-      return static_cast<size_t>((2 * (cta + s) + (s == 0 ? 1 : 0)) * kHkv + g) * (kTile * kGroup) + row;
+      const size_t at = (2 * (cta + s) + (s == 0 ? 1 : 0)) * kHkv + g;
+      return at * (kTile * kGroup) + row;
     };
     const float4* o = reinterpret_cast<const float4*>(prm.part_o) + lane8;
     float m = -INFINITY, l = 0.f;
@@ -468,8 +469,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     float4* to = reinterpret_cast<float4*>(
-                     prm.out + ((static_cast<size_t>(row0) + tile * kTile + (row >> 2)) * kHq + g * kGroup +
-                                (row & 3)) * kDim) + lane8;
+                     prm.out + ((static_cast<size_t>(row0) + tile * kTile + (row >> 2)) * kHq +
+                                g * kGroup + (row & 3)) * kDim) + lane8;
     #pragma unroll
     for (int h = 0; h < 2; ++h)
       to[8 * h] = make_float4(sum[h].x * inv, sum[h].y * inv, sum[h].z * inv, sum[h].w * inv);
@@ -492,7 +493,8 @@ pkv_status launch_join(const TreeParams& prm, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<kTile>, prm, split) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<kTile>, prm, split) != cudaSuccess)
+    return PKV_ERR_CUDA;
   return pkv_check_launch();
 }
 

@@ -6,11 +6,12 @@
 // the tokens that row i sees: one pass with a running maximum m_i and sum.
 //
 // A tile is up to 4 or 8 drafted tokens of a sequence and KV head: 16 or 32 rows. That
-// fills a quarter of a tcgen05 product's rows at most, and a CTA of that kernel takes 5 us before its
-// first scores (its roles, tensor memory and first instructions). Here a block is
-// four warps like the decode's: each takes every fourth page through its own ring of
-// tiles and does all 32 rows' products by warp-wide mma.sync, which needs no set-up.
-// The tiles' steps (four pages, one per warp) are shared out and joined as in tree.cu.
+// fills a quarter of a tcgen05 product's rows at most, and a CTA of that kernel takes
+// 4 us before its first scores (its roles, tensor memory and first instructions). Here a
+// block is four warps like the decode's: each takes every fourth page through its own
+// ring of tiles and does all rows' products by warp-wide mma.sync, which needs no
+// set-up. The tiles' steps (four pages, one per warp) are shared out and joined as in
+// tree.cu.
 //
 // What bounds it: mma.sync, 64 products a page for 32 rows and 32 for up to 16 (three
 // BF16 terms of the weights), 8 cycles each on a quarter of an SM: three warps there
@@ -107,8 +108,9 @@ struct FewState {
   }
 };
 
-// One page, K tile kt and V tile vt (swizzled). kTiles: halves that have rows. seen: what each of this lane's rows sees of it, 16 bits, where not `whole`;
-// V rows that no row sees hold zeros.
+// One page, K tile kt and V tile vt (swizzled). kTiles: halves that have rows. seen:
+// what each of this lane's rows sees of it, 16 bits, where not `whole`; V rows that no
+// row sees hold zeros.
 template <int kTiles, int kHalves>
 __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt, bool whole,
                                             const uint32_t (&seen)[2 * kHalves],

@@ -200,7 +200,6 @@ struct Bf16Tiles {
   static constexpr int kStagePages = 1;
   static constexpr int kParts = 2;              // K and V
   static constexpr uint32_t kCopyBytes = 2 * kTileBytes;
-  static constexpr size_t kAlign = 1024;        // swizzled tiles
   using Ring = PageRing<kStages>;
   using State = PageState;
   struct Source {
@@ -237,9 +236,9 @@ struct Bf16Tiles {
   // The appended row (a 16-byte chunk per lane: K in lanes 0..7, V in 8..15):
   // rotated, into its slot of the pool and of the stage.
   template <bool kRope>
-  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int, const Source& src, int kvh,
-                                                 int slot, int phys, bool to_pool, bool to_stage,
-                                                 uint4 val, float ang_c, float ang_s, int lane) {
+  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int, const Source& src,
+                                                 int kvh, int slot, int phys, bool to_pool,
+                                                 bool to_stage, uint4 val, float ang_c, float ang_s, int lane) {
     const int c = lane & 7;
     if (kRope) {
       const uint4 partner = shfl_xor_uint4(val, 4);

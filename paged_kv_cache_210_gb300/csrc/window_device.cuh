@@ -52,7 +52,7 @@ struct UnitSearch {
 };
 
 template <class Tiles>
-struct alignas(Tiles::kAlign) WindowSmem {
+struct WindowSmem {
   typename Tiles::Ring warp[kWarps];
   unsigned long long bar[kWarps][Tiles::kStages];
   float m[kWarps][kGroup];
@@ -567,7 +567,8 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   // Groups seen whole: all their pages are there, inside the window (and valid);
   // the first one is one of the sequence's [whole_from, whole_from + whole).
   const int whole_from = sink_pages + (win_lo % kPage != 0 ? 1 : 0);
-  const unsigned whole = max(min(len / kPage - win_page + sink_pages, page_end) - kPer + 1 - whole_from, 0);
+  const int whole_to = min(len / kPage - win_page + sink_pages, page_end);
+  const unsigned whole = max(whole_to - kPer + 1 - whole_from, 0);
   int at = page_begin + warp * kPer;          // the group's first page
   int issued = n_prefetch;
   int consumed = 0;
@@ -772,7 +773,8 @@ pkv_status launch_window(pkv_pool_t pool, int layer, const void* q, const void* 
   prm.max_splits = c.max_splits;
   prm.window = std::min(window, c.max_seq_len);
   prm.sinks = std::min(sinks, c.max_seq_len);
-  const WindowPlan plan = plan_window<Tiles>(pool, Tiles::residency(pool), batch, prm.window, prm.sinks, num_splits);
+  const WindowPlan plan = plan_window<Tiles>(pool, Tiles::residency(pool), batch, prm.window,
+                                             prm.sinks, num_splits);
   const bool cluster = plan.cluster;
   prm.num_splits = plan.num_splits;
   prm.batch = batch;
