@@ -74,7 +74,8 @@ pkv_status pkv_quant_read(pkv_pool_t pool, int layer, const void* kv_pool,
  * (pkv_window.h: window, sinks, padding rows, invalid pages, num_splits, rope).
  * q is BF16, out FP32; queries, scores, softmax statistics, probabilities and
  * sums keep FP32's precision, so the result is that of FP32 arithmetic on the
- * cache's values. */
+ * cache's values: keys below 2^122 in magnitude, scores and the sums of a
+ * sequence's |V| inside FP32's range. */
 pkv_status pkv_quant_attention(pkv_pool_t pool, int layer, const void* q, const void* kv_pool,
                                const int32_t* block_tables, const int32_t* seq_lens, float* out,
                                int window, int sinks, const pkv_axes_rope* rope,

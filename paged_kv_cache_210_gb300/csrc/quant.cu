@@ -102,6 +102,12 @@ __device__ __forceinline__ float row_max(float x) {
 // nothing yet, no test for -inf - -inf is needed.
 constexpr float kNone = -0x1.fffffep127f;
 
+// Products of scaled queries and codes reach 2^30 and exponents 2^120: a score is held
+// in units of 2^16 of theirs, so that it does not pass FP32's range before the query's
+// scaling is taken back out of it (with any |K| below 2^122; without the unit 2^106).
+// Exact: 2^-16 2^ek is a power of two >= 2^-140.
+constexpr float kScoreUnit = 0x1p-16f;
+
 struct QuantTiles {
   // With 3, 4 sequences of 131,072 tokens take 92 us instead of 84.
   static constexpr int kStages = 2;
@@ -110,7 +116,7 @@ struct QuantTiles {
   static constexpr uint32_t kCopyBytes = kQuantTile;
   struct alignas(16) Ring {
     uint8_t tile[kStages][kStagePages][kQuantTile];
-    // 2^ek of two neighbouring tokens, then their 2^ev
+    // kScoreUnit 2^ek of two neighbouring tokens, then their 2^ev
     float scale[kStagePages * kPage / 2][4];
   };
   struct Source {
@@ -266,7 +272,8 @@ struct QuantTiles {
     // 2^(14 - floor(log2 most)), at most 2^125
     const uint32_t up = 268u - max(__float_as_uint(most) >> 23, 16u);
     const float scale = scale_of(up);
-    q.to_log2 = 1.4426950408889634f * 0.125f * inverse_scale_of(up);   // log2(e) / sqrt(64)
+    // log2(e) / sqrt(64), at most 0.18 x 2^(113 + 16)
+    q.to_log2 = 1.4426950408889634f * 0.125f / kScoreUnit * inverse_scale_of(up);
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // without rotation the high parts are the queries (8 bits)
@@ -300,7 +307,7 @@ struct QuantTiles {
     for (int nt = 0; nt < kTiles; ++nt)
       kw[nt] = *reinterpret_cast<const uint4*>(ws.tile[stage][nt / 2] +
                                                k_at(8 * (nt % 2) + g8, 16 * qq));
-    ws.scale[lane / 2][lane % 2] = scale_of(ek);
+    ws.scale[lane / 2][lane % 2] = scale_of(ek) * kScoreUnit;
     ws.scale[lane / 2][2 + lane % 2] = scale_of(ev);
     #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt) {

@@ -361,6 +361,14 @@ def test_scales(k_scale, q_scale):
     run_decode(c, 2048, 0, 1, False, q_scale=q_scale)
 
 
+@pytest.mark.parametrize("axes", [0, 1])
+@pytest.mark.parametrize("k_scale", [1e34, 1e30, 1e-34])
+def test_keys_near_the_ends_of_the_range(k_scale, axes):
+    # scores of ordinary size from factors whose product with the other's scaling is not
+    c = QuantCache([300, 45], seed=3, k_scale=k_scale)
+    run_decode(c, 2048, 0, axes, False, q_scale=2 / k_scale)
+
+
 @pytest.mark.parametrize("spread", [4, 18, 60])
 def test_values_of_very_different_sizes(spread):
     # rows of V from 2^-spread to 2^spread, some zero, in any order
