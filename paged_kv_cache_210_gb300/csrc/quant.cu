@@ -204,8 +204,8 @@ struct QuantTiles {
                                                  bool to_stage, uint4 val, float ang_c,
                                                  float ang_s, int lane) {
     const int c = lane & 7;
-    float2 x[4];
-    unpack8(val, x);
+    float2 x[1][4];
+    unpack8(val, x[0]);
     if (kRope) {
       float2 cs[4], sn[4], partner[4];
       unpack8(shfl_xor_uint4(val, 4), partner);
@@ -218,22 +218,23 @@ struct QuantTiles {
         sn[e] = make_float2(sign * __shfl_sync(0xffffffffu, ang_s, pair),
                             sign * __shfl_sync(0xffffffffu, ang_s, pair + 1));
       }
-      if (lane < 8) rotate8(x, partner, cs, sn);
+      if (lane < 8) rotate8(x[0], partner, cs, sn);
     }
-    uint2 codes;
-    const uint32_t e = quantise_row(x, codes);
+    uint2 codes[1];
+    uint32_t e[1];
+    quantise_rows(x, codes, e);
     if (lane >= 16) return;
     const int at = lane < 8 ? k_at(slot, 8 * c) : v_at(slot, 8 * c);
     const int exp_at = (lane < 8 ? kKExp : kVExp) + slot;
     if (to_pool) {
       uint8_t* t = src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile;
-      *reinterpret_cast<uint2*>(t + at) = codes;
-      if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
+      *reinterpret_cast<uint2*>(t + at) = codes[0];
+      if (c == 0) t[exp_at] = static_cast<uint8_t>(e[0]);
     }
     if (to_stage) {
       uint8_t* t = ws.tile[stage][page];
-      *reinterpret_cast<uint2*>(t + at) = codes;
-      if (c == 0) t[exp_at] = static_cast<uint8_t>(e);
+      *reinterpret_cast<uint2*>(t + at) = codes[0];
+      if (c == 0) t[exp_at] = static_cast<uint8_t>(e[0]);
     }
   }
 

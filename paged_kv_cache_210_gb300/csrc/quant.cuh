@@ -22,7 +22,7 @@ constexpr int kKExp = 2 * kCodeBytes;                // exponent bytes of K ...
 constexpr int kVExp = kKExp + kPage;                 // ... and of V
 static_assert(kVExp + kPage == kQuantTile && kQuantTile % 16 == 0, "the documented tile");
 
-// Where dims d .. of token t start in a tile (d a multiple of 8).
+// Where dims d .. of token t start in a tile (of V: d a multiple of 8).
 __host__ __device__ constexpr int k_at(int t, int d) { return t * kDim + d; }
 __host__ __device__ constexpr int v_at(int t, int d) {
   return kCodeBytes + d / kChunkDims * kChunkBytes + t * kChunkDims + d % kChunkDims;
@@ -67,25 +67,20 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t w) {
   return h;
 }
 
-// A row of 64 values held by 8 neighbouring lanes, 8 each: its exponent byte
-// and this lane's 8 codes. Called by a whole warp (four rows). Arithmetic on pairs
-// where the hardware has it: each lane's instructions bound the fill.
-__device__ __forceinline__ uint32_t quantise_row(float2 (&x)[4], uint2& codes) {
-  float most = 0.f;
+// Rows of 64 values, each held by 8 neighbouring lanes, 8 values each (four rows a
+// warp): exponent bytes and this lane's 8 codes of each. Called by a whole warp.
+// Arithmetic on pairs where the hardware has it, and one branch for all rows: each
+// lane's instructions, and how many rows are under way at once, bound the fill.
+__device__ __forceinline__ float row_most(const float2 (&x)[4]) {
+  float most = 0.f;                                            // a NaN does not count
   #pragma unroll
   for (int i = 0; i < 4; ++i)
-    most = fmaxf(fmaxf(most, fabsf(x[i].x)), fabsf(x[i].y));   // a NaN does not count
+    most = max3(most, __float_as_uint(fabsf(x[i].x)), __float_as_uint(fabsf(x[i].y)));
   #pragma unroll
   for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (__any_sync(0xffffffffu, most > kLargest)) {
-    // values beyond the largest are taken as that; NaN stays
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (fabsf(x[i].x) > kLargest) x[i].x = copysignf(kLargest, x[i].x);
-      if (fabsf(x[i].y) > kLargest) x[i].y = copysignf(kLargest, x[i].y);
-    }
-    most = fminf(most, kLargest);
-  }
+  return most;
+}
+__device__ __forceinline__ uint32_t row_codes(float2 (&x)[4], float most, uint2& codes) {
   const uint32_t e = exponent_byte(most);
   const float2 inv = make_float2(inverse_scale_of(e), inverse_scale_of(e));
   #pragma unroll
@@ -93,6 +88,30 @@ __device__ __forceinline__ uint32_t quantise_row(float2 (&x)[4], uint2& codes) {
   codes.x = codes_of(x[0].x, x[0].y) | codes_of(x[1].x, x[1].y) << 16;
   codes.y = codes_of(x[2].x, x[2].y) | codes_of(x[3].x, x[3].y) << 16;
   return e;
+}
+template <int kRows>
+__device__ __forceinline__ void quantise_rows(float2 (&x)[kRows][4], uint2 (&codes)[kRows],
+                                              uint32_t (&exps)[kRows]) {
+  float most[kRows], top = 0.f;
+  #pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    most[r] = row_most(x[r]);
+    top = fmaxf(top, most[r]);
+  }
+  if (__any_sync(0xffffffffu, top > kLargest)) {
+    // values beyond the largest are taken as that; NaN stays
+    #pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (fabsf(x[r][i].x) > kLargest) x[r][i].x = copysignf(kLargest, x[r][i].x);
+        if (fabsf(x[r][i].y) > kLargest) x[r][i].y = copysignf(kLargest, x[r][i].y);
+      }
+      most[r] = fminf(most[r], kLargest);
+    }
+  }
+  #pragma unroll
+  for (int r = 0; r < kRows; ++r) exps[r] = row_codes(x[r], most[r], codes[r]);
 }
 
 // BF16 chunk -> 8 FP32 values, exact.
@@ -114,6 +133,20 @@ __device__ __forceinline__ void rotate8(float2 (&x)[4], const float2 (&partner)[
   for (int i = 0; i < 4; ++i)
     x[i] = make_float2(__fadd_rn(__fmul_rn(x[i].x, cs[i].x), __fmul_rn(partner[i].x, sn[i].x)),
                        __fadd_rn(__fmul_rn(x[i].y, cs[i].y), __fmul_rn(partner[i].y, sn[i].y)));
+}
+
+// 8 dims of a row rotated, the 4 in x[0], x[1] being the partners of those in x[2],
+// x[3]; cs and sn the angles of their 4 pairs; rounded as above.
+__device__ __forceinline__ void rotate_halves(float2 (&x)[4], const float2 (&cs)[2],
+                                              const float2 (&sn)[2]) {
+  #pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = x[i], b = x[i + 2];
+    x[i] = make_float2(__fsub_rn(__fmul_rn(a.x, cs[i].x), __fmul_rn(b.x, sn[i].x)),
+                       __fsub_rn(__fmul_rn(a.y, cs[i].y), __fmul_rn(b.y, sn[i].y)));
+    x[i + 2] = make_float2(__fadd_rn(__fmul_rn(b.x, cs[i].x), __fmul_rn(a.x, sn[i].x)),
+                           __fadd_rn(__fmul_rn(b.y, cs[i].y), __fmul_rn(a.y, sn[i].y)));
+  }
 }
 
 }  // namespace pkv_quant_dev

@@ -3,12 +3,12 @@
 // Both are memory traffic: 2,048 + 1,040 bytes a token either way (K and V of 8
 // heads in BF16, and as codes with their exponents). Reading 120,500 tokens back takes
 // 58 us (6.4 TB/s, 96 % of the measured copy rate), 14,200 8.9 us; filling 14,200
-// rotated tokens 11.8 us, of which three dependent loads (the lists, the page id and
-// the rotary positions, the angles) are 2.5 and a warp's arithmetic (107 instructions
-// a row of 8 lanes, 8 values each) about 5; 77 tokens 3.2 and 2.0 us, all latency. A
-// block per whole page whose tiles are put together in shared memory took 15.2 us for
-// the fill, one whose threads held 16 codes 83 us for the long read (it wrote half
-// sectors).
+// rotated tokens 9.4 us (4.7 TB/s), of which three dependent loads (the lists, the page
+// id and the rotary positions, the angles) are 2; 77 tokens 2.2 and 2.0 us, all
+// latency. The fill took 11.6 us with a branch on each row's clamp and on each token's
+// angle before the next one's load, 10.7 with the latter alone; a block per whole page
+// whose tiles are put together in shared memory 15.2. A reading block whose threads held
+// 16 codes took 83 us for the long read (it wrote half sectors).
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,14 +27,14 @@ using namespace pkv_quant_dev;
 namespace {
 
 // A block takes the tokens of a page, 4 per warp, and some of the KV heads: 8 lanes
-// hold a row, 8 dims each. Of one head a warp then moves 256 contiguous bytes of K's
+// hold a row, 8 dims each (of a key to be rotated, 4 dims and their 4 partners). Of one head a warp then moves 256 contiguous bytes of K's
 // codes, four pieces of 64 bytes of V's and four of 128 bytes on the BF16 side.
 constexpr int kThreads = 128;
 constexpr int kWarpTokens = 32 / 8;
 constexpr int kReadHeads = 2;                        // of a block
-// KV heads of a fill block: 2 shorten a small call (77 tokens 3.2 us, with 4 3.7),
-// 4 have more loads in flight and the angles for more (14,200 tokens 11.9 us, with 2
-// 12.4).
+// KV heads of a fill block: 2 shorten a small call (77 tokens 2.2 us, with 4 2.5; 2,048
+// 3.1 and 3.2), 4 have more loads in flight and the angles for more (6,144 tokens 5.1
+// us, with 2 5.7; 16,384 10.5 and 11.1).
 constexpr int kFewFillHeads = 2, kManyFillHeads = 4;
 constexpr int kManyTokens = 4096;
 static_assert(kThreads / 32 * kWarpTokens == kPage, "a block's warps cover a page");
@@ -92,7 +92,8 @@ __device__ __forceinline__ PageWork page_work(const StoreParams& prm, int index)
   return w;
 }
 
-// The rows' loads and the rotary positions' go out before the page id is waited for.
+// The rows' loads and the rotary positions' go out before the page id is waited for,
+// the angles' all at once.
 template <bool kRope, int kFillHeads>
 __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, uint8_t* pool,
@@ -105,18 +106,23 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
   const int head0 = blockIdx.x % kGroups * kFillHeads;
   const int slot = warp * kWarpTokens + lane / 8, c = lane % 8;
   bool valid = slot >= w.first && slot < w.first + w.count;
-  const size_t from =
-      static_cast<size_t>(w.row + slot - w.first) * (kHkv * kDim / 8) + head0 * 8 + c;
+  const size_t from = static_cast<size_t>(w.row + slot - w.first) * (kHkv * kDim) + head0 * kDim;
   uint4 kv[2][kFillHeads];
   #pragma unroll
   for (int h = 0; h < kFillHeads; ++h) {
     kv[0][h] = kv[1][h] = make_uint4(0u, 0u, 0u, 0u);
     if (valid) {
-      kv[0][h] = __ldcs(reinterpret_cast<const uint4*>(k) + from + 8 * h);
-      kv[1][h] = __ldcs(reinterpret_cast<const uint4*>(v) + from + 8 * h);
+      if constexpr (kRope) {
+        const uint2* row = reinterpret_cast<const uint2*>(k + from + kDim * h);
+        const uint2 lo = __ldcs(row + c), hi = __ldcs(row + 8 + c);
+        kv[0][h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        kv[0][h] = __ldcs(reinterpret_cast<const uint4*>(k + from + kDim * h) + c);
+      }
+      kv[1][h] = __ldcs(reinterpret_cast<const uint4*>(v + from + kDim * h) + c);
     }
   }
-  float2 cs[4], sn[4];
+  float2 cs[2], sn[2];
   if constexpr (kRope) {
     // lane i fetches pair i's angle of each of the warp's tokens; a token whose
     // position is outside the tables is left out
@@ -126,23 +132,30 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
       const int s = warp * kWarpTokens + t - w.first;
       pos[t] = s >= 0 && s < w.count ? pair_position(rope, w.row + s, lane) : 0;
     }
+    bool all_good = true;
     #pragma unroll
     for (int t = 0; t < kWarpTokens; ++t) {
-      float2 a = make_float2(1.f, 0.f);
-      const bool ok = load_pair_angle(rope, pos[t], lane, a.x, a.y);
-      angles[warp][t][lane] = a;
-      if (!ok) {
-        if (lane == 0) set_error(prm.err, PKV_DEV_ERR_POSITION);
+      if (!__all_sync(0xffffffffu, pos[t] >= 0 && pos[t] < rope.rows)) {
+        all_good = false;
+        pos[t] = 0;
         if (lane / 8 == t) valid = false;
       }
     }
+    if (!all_good && lane == 0) set_error(prm.err, PKV_DEV_ERR_POSITION);
+    float2 mine[kWarpTokens];
+    #pragma unroll
+    for (int t = 0; t < kWarpTokens; ++t) {
+      const size_t at = static_cast<size_t>(pos[t]) * kPairs + lane;
+      mine[t] = make_float2(__ldg(rope.cos + at), __ldg(rope.sin + at));
+    }
+    #pragma unroll
+    for (int t = 0; t < kWarpTokens; ++t) angles[warp][t][lane] = mine[t];
     __syncwarp();
     #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float4 a =
-          *reinterpret_cast<const float4*>(&angles[warp][lane / 8][8 * (c & 3) + 2 * e]);
+    for (int e = 0; e < 2; ++e) {
+      const float4 a = *reinterpret_cast<const float4*>(&angles[warp][lane / 8][4 * c + 2 * e]);
       cs[e] = make_float2(a.x, a.z);
-      sn[e] = c < 4 ? make_float2(-a.y, -a.w) : make_float2(a.y, a.w);
+      sn[e] = make_float2(a.y, a.w);
     }
   }
   const bool good_page = w.page >= 0 && w.page < prm.num_pages;
@@ -152,29 +165,29 @@ __global__ void __launch_bounds__(kThreads) quant_fill_kernel(
   }
   uint8_t* tile = pool + (static_cast<size_t>(w.page) * kHkv + head0) * kQuantTile;
   #pragma unroll
-  for (int h = 0; h < kFillHeads; ++h, tile += kQuantTile) {
+  for (int which = 0; which < 2; ++which) {
+    float2 x[kFillHeads][4];
     #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float2 x[4];
-      unpack8(kv[which][h], x);
-      if constexpr (kRope) {
-        if (which == 0) {
-          const uint4 own = kv[0][h];
-          float2 partner[4];
-          unpack8(make_uint4(__shfl_xor_sync(0xffffffffu, own.x, 4),
-                             __shfl_xor_sync(0xffffffffu, own.y, 4),
-                             __shfl_xor_sync(0xffffffffu, own.z, 4),
-                             __shfl_xor_sync(0xffffffffu, own.w, 4)),
-                  partner);
-          rotate8(x, partner, cs, sn);
+    for (int h = 0; h < kFillHeads; ++h) {
+      unpack8(kv[which][h], x[h]);
+      if (kRope && which == 0) rotate_halves(x[h], cs, sn);
+    }
+    uint2 codes[kFillHeads];
+    uint32_t exps[kFillHeads];
+    quantise_rows(x, codes, exps);
+    if (valid) {
+      #pragma unroll
+      for (int h = 0; h < kFillHeads; ++h) {
+        uint8_t* to = tile + h * kQuantTile;
+        if (kRope && which == 0) {
+          *reinterpret_cast<uint32_t*>(to + k_at(slot, 4 * c)) = codes[h].x;
+          *reinterpret_cast<uint32_t*>(to + k_at(slot, kDim / 2 + 4 * c)) = codes[h].y;
+        } else {
+          *reinterpret_cast<uint2*>(to + (which == 0 ? k_at(slot, 8 * c) : v_at(slot, 8 * c))) =
+              codes[h];
         }
+        if (c == 0) to[(which == 0 ? kKExp : kVExp) + slot] = static_cast<uint8_t>(exps[h]);
       }
-      uint2 codes;
-      const uint32_t e = quantise_row(x, codes);
-      if (!valid) continue;
-      const int at = which == 0 ? k_at(slot, 8 * c) : v_at(slot, 8 * c);
-      *reinterpret_cast<uint2*>(tile + at) = codes;
-      if (c == 0) tile[(which == 0 ? kKExp : kVExp) + slot] = static_cast<uint8_t>(e);
     }
   }
 }
