@@ -197,12 +197,17 @@ struct QuantTiles {
   }
 
   // The appended row (a 16-byte chunk per lane: K in lanes 0..7, V in 8..15):
-  // rotated, quantised, into its slot of the pool and of the stage.
+  // rotated, quantised and put into the pool while the first pages are on their way
+  // (256 sequences behind 4,096 tokens: 0.2 us less than at its page's turn, and three
+  // registers are kept instead of seven), into the stage at its page's turn.
+  struct NewRow {
+    uint2 codes;
+    uint32_t e;
+  };
   template <bool kRope>
-  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int page, const Source& src,
-                                                 int kvh, int slot, int phys, bool to_pool,
-                                                 bool to_stage, uint4 val, float ang_c,
-                                                 float ang_s, int lane) {
+  static __device__ __forceinline__ NewRow make_row(const Source& src, int kvh, int slot, int phys,
+                                                    bool to_pool, uint4 val, float ang_c,
+                                                    float ang_s, int lane) {
     const int c = lane & 7;
     float2 x[1][4];
     unpack8(val, x[0]);
@@ -223,19 +228,24 @@ struct QuantTiles {
     uint2 codes[1];
     uint32_t e[1];
     quantise_rows(x, codes, e);
+    const NewRow made = {codes[0], e[0]};
+    if (to_pool)
+      store_row(src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile, slot, made, lane);
+    return made;
+  }
+  static __device__ __forceinline__ void store_row(uint8_t* tile, int slot, const NewRow& made,
+                                                   int lane) {
+    const int c = lane & 7;
     if (lane >= 16) return;
-    const int at = lane < 8 ? k_at(slot, 8 * c) : v_at(slot, 8 * c);
-    const int exp_at = (lane < 8 ? kKExp : kVExp) + slot;
-    if (to_pool) {
-      uint8_t* t = src.pool + (static_cast<size_t>(phys) * kHkv + kvh) * kQuantTile;
-      *reinterpret_cast<uint2*>(t + at) = codes[0];
-      if (c == 0) t[exp_at] = static_cast<uint8_t>(e[0]);
-    }
-    if (to_stage) {
-      uint8_t* t = ws.tile[stage][page];
-      *reinterpret_cast<uint2*>(t + at) = codes[0];
-      if (c == 0) t[exp_at] = static_cast<uint8_t>(e[0]);
-    }
+    *reinterpret_cast<uint2*>(tile + (lane < 8 ? k_at(slot, 8 * c) : v_at(slot, 8 * c))) =
+        made.codes;
+    if (c == 0) tile[(lane < 8 ? kKExp : kVExp) + slot] = static_cast<uint8_t>(made.e);
+  }
+  template <bool kRope>
+  static __device__ __forceinline__ void put_row(Ring& ws, int stage, int page, const Source&, int,
+                                                 int slot, int, bool, bool to_stage,
+                                                 const NewRow& made, int lane) {
+    if (to_stage) store_row(ws.tile[stage][page], slot, made, lane);
   }
 
   template <bool kRope>

@@ -510,9 +510,9 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
     }
   };
   // Fused: the appended row, one 16-byte chunk per lane (K in lanes 0..7, V
-  // in 8..15). Loaded ahead of the pages; rotated, written to the pool and
-  // patched into the stage at its page's turn, when the load has long arrived
-  // (64 ragged sequences behind 1,024 tokens: 15.6 us; done ahead, 15.9).
+  // in 8..15). Loaded ahead of the pages and patched into the stage at its page's
+  // turn; what comes before that (rotation, quantisation, the pool's copy) is done
+  // there as well or, where the Tiles say so, while the first pages are on their way.
   auto load_new_row = [&]() {
     uint4 val = make_uint4(0u, 0u, 0u, 0u);
     if (lane < 16)
@@ -554,13 +554,19 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
   if (deferred) issue_copy(j_new, j_new);
   // the new row's load goes out before the queries', so their latencies overlap
   uint4 new_row = make_uint4(0u, 0u, 0u, 0u);
-  if (kFused && j_new >= 0) new_row = load_new_row();
-  int new_page = kFused && j_new >= 0 && j_new < n_prefetch
-                     ? __shfl_sync(0xffffffffu, ids, l_new & 31)
-                     : -1;
+  int new_page = -1;
+  if (kFused && j_new >= 0) {
+    new_row = load_new_row();
+    new_page = __ldg(row + (len - 1) / kPage);
+  }
   typename Tiles::Queries queries;
   Tiles::template load_queries<kRope>(
       prm.q + (static_cast<size_t>(b) * kHq + kvh * kGroup) * kDim, lane, ang_c, ang_s, queries);
+
+  typename Tiles::NewRow made;
+  if (kFused && j_new >= 0)
+    made = Tiles::template make_row<kRope>(src, kvh, new_slot, new_page, good_id(new_page), new_row,
+                                           ang_c, ang_s, lane);
 
   typename Tiles::State st;
   st.reset();
@@ -603,8 +609,7 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
       if (with_new)
         Tiles::template put_row<kRope>(ws, stage, l_new % kPer, src, kvh, new_slot, new_page,
                                        good_id(new_page),
-                                       (seen >> (l_new % kPer * kPage) & 0xffffu) != 0, new_row,
-                                       ang_c, ang_s, lane);
+                                       (seen >> (l_new % kPer * kPage) & 0xffffu) != 0, made, lane);
       fence_proxy_async_smem();
       __syncwarp();
     }
@@ -619,7 +624,6 @@ window_decode_kernel(const __grid_constant__ typename Tiles::Source src,
       ids_next = fetch_ids(next * kPer + 32);
     }
     issue_copy(next, stage);
-    if (kFused && next == j_new) new_page = __shfl_sync(0xffffffffu, ids, l_new & 31);
     issued = next + 1;
   };
   for (int j = 0; j < mine; ++j, at += kWarps * kPer) {
