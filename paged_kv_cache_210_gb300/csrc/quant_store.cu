@@ -27,8 +27,9 @@ using namespace pkv_quant_dev;
 namespace {
 
 // A block takes the tokens of a page, 4 per warp, and some of the KV heads: 8 lanes
-// hold a row, 8 dims each (of a key to be rotated, 4 dims and their 4 partners). Of one head a warp then moves 256 contiguous bytes of K's
-// codes, four pieces of 64 bytes of V's and four of 128 bytes on the BF16 side.
+// hold a row, 8 dims each (of a key to be rotated, 4 dims and their 4 partners). Of one
+// head a warp then moves 256 contiguous bytes of K's codes, four pieces of 64 bytes of
+// V's and four of 128 bytes on the BF16 side.
 constexpr int kThreads = 128;
 constexpr int kWarpTokens = 32 / 8;
 constexpr int kReadHeads = 2;                        // of a block

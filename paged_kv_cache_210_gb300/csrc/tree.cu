@@ -130,15 +130,16 @@ __global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
   }
 }
 
-// Whether the kernel for few rows takes the call. Measured (us, this and the other
-// kernel; sequences x drafted tokens, 2,000 committed): 1 x 1 7.2 and 11.1, 1 x 4 7.5
-// and 11.6, 8 x 4 13.0 and 17.1, 128 x 4 93 and 119; 1 x 8 8.9 and 12.3, 8 x 8 16.1
-// and 17.7, 32 x 8 39.2 and 40.1; 1 x 16 9.8 and 13.2, 4 x 16 15.7 and 15.1. Over
-// 16,000 committed tokens 1 x 8 takes 21.7 and 19.6.
-bool few_rows(int max_seq_len, int batch, int total_tokens) {
-  const long long mean4 = 4ll * batch;
-  return total_tokens <= mean4 ||
-         (max_seq_len <= 2048 && total_tokens <= std::max(2 * mean4, 16ll));
+// Whether the kernel for few rows takes the call: where clusters of 8 or 16 blocks do,
+// or for up to 4 drafted tokens a sequence on average, 8 in short contexts. Measured (us,
+// this and the other kernel; sequences x drafted tokens, 2,000 committed): with clusters
+// 1 x 8 7.7 and 12.9, 1 x 48 12.1 and 14.8, 3 x 16 12.0 and 14.1; 1 x 8 over 8,000 14.8
+// and 17.3; on the line, or in clusters of 4, 8 x 4 12.8 and 17.1, 128 x 4 93 and 119, 32
+// x 8 39.2 and 40.1, 2 x 32 15.1 and 15.3, 1 x 64 15.4 and 15.3, 1 x 8 over 16,000 (line)
+// 21.7 and 19.6.
+bool few_rows(int max_seq_len, int batch, int total_tokens, int parts) {
+  return parts >= 8 || total_tokens <= 4ll * batch ||
+         (max_seq_len <= 2048 && total_tokens <= 8ll * batch);
 }
 
 }  // namespace
@@ -170,7 +171,11 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   if (!set_smem_attribute<TreeJob>(pool->device)) return PKV_ERR_CUDA;
 
   CUtensorMap tq, tk, tv;
-  const bool few = few_rows(c.max_seq_len, batch, total_tokens);
+  // what a row sees: the context, or the sinks, the window and whole pages around them
+  const long long seen = std::min<long long>(c.max_seq_len, static_cast<long long>(window) + sinks +
+                                                                kMaxTree + 2 * kPage);
+  const int parts = pkv_tree_cluster(pool, batch, total_tokens, static_cast<int>(seen));
+  const bool few = few_rows(c.max_seq_len, batch, total_tokens, parts);
   const cuuint64_t dims[3] = {kDim, kHq, static_cast<cuuint64_t>(total_tokens)};
   const cuuint64_t strides[2] = {kRowBytes, static_cast<cuuint64_t>(kHq) * kRowBytes};
   const cuuint32_t box[3] = {kDim, kGroup, kTileTokens};
@@ -200,7 +205,7 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   prm.part_ml = pool->tree_part_ml;
   set_wave(&prm, wave);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (few) return pkv_tree_few(pool, q, tk, tv, prm, st);
+  if (few) return pkv_tree_few(pool, q, tk, tv, prm, parts, st);
   tile_attention_kernel<TreeJob><<<wave, kThreads, kSmemBytes<TreeJob>, st>>>(tq, tk, tv, prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   return launch_join<kTileTokens>(prm, st);

@@ -175,6 +175,24 @@ __device__ __forceinline__ long long warp_sum(long long x) {
   return x;
 }
 
+// The positions of a sequence's rows, where the window hides committed tokens.
+__device__ __forceinline__ void span_of_rows(const TreeParams& prm, int row0, int lane,
+                                             TreeWork& work) {
+  work.lo = 0;
+  work.top = work.start + work.nodes - 1;
+  if (work.top < prm.window) return;
+  int least = kMaxTree, most = 0;
+  for (int i = lane; i < work.nodes; i += 32) {
+    const int n = __popcll(prm.tree[row0 + i] & low_nodes(work.nodes));
+    least = min(least, n);
+    most = max(most, n);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  work.lo = min(max(work.start + least - prm.window, 0), work.start);
+  work.top = work.start + most - 1;
+}
+
 // This CTA's parts, in the line's order. Held by one warp; lane i looks after the
 // i-th of 32 sequences.
 template <int kTile>
@@ -294,27 +312,43 @@ struct TreeWalk {
       work.slot = begin == 0 && stop == steps
                       ? -1
                       : (2 * cta + (begin == 0 ? 1 : 0)) * kHkv + work.g;
-      // the rows' positions, where the window hides committed tokens
-      work.lo = 0;
-      work.top = work.start + work.nodes - 1;
-      if (work.top >= prm.window) {
-        int least = kMaxTree, most = 0;
-        for (int i = lane; i < work.nodes; i += 32) {
-          const int n = __popcll(prm.tree[row0 + i] & low_nodes(work.nodes));
-          least = min(least, n);
-          most = max(most, n);
-        }
-        least = __reduce_min_sync(0xffffffffu, least);
-        most = __reduce_max_sync(0xffffffffu, most);
-        work.lo = min(max(work.start + least - prm.window, 0), work.start);
-        work.top = work.start + most - 1;
-      }
+      span_of_rows(prm, row0, lane, work);
       return true;
     }
     return false;
   }
-
 };
+
+// Part `rank` of `parts` of the launch's tile number `tile`, of up to 32 sequences;
+// false if there are fewer tiles. A part may have no steps. Called by a whole warp.
+template <int kTile>
+__device__ __forceinline__ bool part_of_tile(const TreeParams& prm, const TreeLane<kTile>& mine,
+                                             int tile, int rank, int parts, int lane,
+                                             TreeWork& work) {
+  int incl = mine.tiles();
+  #pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  const uint32_t holds = __ballot_sync(0xffffffffu, tile < incl);
+  if (holds == 0) return false;
+  const int from = __ffs(holds) - 1;
+  const int in = tile - __shfl_sync(0xffffffffu, incl - mine.tiles(), from);
+  const int steps = __shfl_sync(0xffffffffu, mine.steps, from);
+  const int row0 = __shfl_sync(0xffffffffu, mine.row0, from);
+  work.b = from;
+  work.start = __shfl_sync(0xffffffffu, mine.start, from);
+  work.nodes = __shfl_sync(0xffffffffu, mine.nodes, from);
+  work.first_node = in * kTile;
+  work.row = row0 + work.first_node;
+  work.count = min(kTile, work.nodes - work.first_node);
+  work.step = steps * rank / parts;
+  work.steps = steps * (rank + 1) / parts - work.step;
+  work.slot = -1;
+  span_of_rows(prm, row0, lane, work);
+  return true;
+}
 
 // What one row sees.
 struct TreeRow {
@@ -506,8 +540,12 @@ inline void set_wave(TreeParams* prm, int ctas) {
 
 }  // namespace pkv_tree_dev
 
-// tree_few.cu: the attention of few rows per sequence (prm as tree.cu fills it).
+// tree_few.cu: the attention of few rows per sequence (prm as tree.cu fills it), by
+// clusters of so many blocks (0: none), as pkv_tree_cluster finds for a call whose
+// sequences see up to seen_tokens.
+int pkv_tree_cluster(const pkv_pool* pool, int batch, int total_tokens, int seen_tokens);
 pkv_status pkv_tree_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
-                        const CUtensorMap& tv, pkv_tree_dev::TreeParams prm, cudaStream_t st);
+                        const CUtensorMap& tv, pkv_tree_dev::TreeParams prm, int parts,
+                        cudaStream_t st);
 
 #endif  // PKV_TREE_CUH

@@ -11,16 +11,18 @@
 // block is four warps like the decode's: each takes every fourth page through its own
 // ring of tiles and does all rows' products by warp-wide mma.sync, which needs no
 // set-up. The tiles' steps (four pages, one per warp) are shared out and joined as in
-// tree.cu.
+// tree.cu, or, where the tiles are few and short, by a cluster of blocks per tile that
+// joins its parts through shared memory, without a second launch.
 //
 // What bounds it: mma.sync, 64 products a page for 32 rows and 32 for up to 16 (three
 // BF16 terms of the weights), 8 cycles each on a quarter of an SM: three warps there
 // take a page each in about 2,000 cycles, 1,536 of them products, where the decode's
 // four rows hide under the copies. So it serves few tokens: one tree of 8 over 2,000
-// tokens 8.9 us (tcgen05 12.3), 128 trees of 4 over 2,000 93 us (119; the bytes alone
+// tokens 7.7 us (tcgen05 12.9), 128 trees of 4 over 2,000 93 us (119; the bytes alone
 // 80); which calls it takes is decided in tree.cu. Many short sequences are bound by the
 // start and the end of their tiles, some 5 us each for a block: 1,024 trees of 4 over
-// 300 tokens 136 us (the bytes 103), 4,096 of 2 over 64 321 (98).
+// 300 tokens 136 us (the bytes 103), 4,096 of 2 over 64 321 (98). One tree of 8 over 2,000
+// tokens is latency: on the line 8.8 us, the join 2 of them, in clusters of 16 7.7.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -78,6 +80,66 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Parts of a cluster's rows, each at the block that ends the row: block r % S ends row
+// r, which finds part p of it in slot r / S * S + p.
+struct alignas(16) RowInbox {
+  float o[kFewRowsN<2>][kDim];
+  float2 ml[kFewRowsN<2>];
+  unsigned long long bar;
+};
+constexpr int kMaxParts = 16;
+constexpr uint32_t kRowPartBytes = (kDim + 2) * sizeof(float);
+constexpr int kPartTokens = 512;
+constexpr size_t kClusterSmemBytes = kFewSmemBytes<2> + sizeof(RowInbox);
+static_assert(kFewBlocksPerSm<2> * (kClusterSmemBytes + 1024) <= 228 * 1024, "blocks per SM");
+static_assert(sizeof(FewSmem<2>) % 16 == 0 && kFewRowsN<2> % kMaxParts == 0, "the inbox's place");
+
+// Asynchronous store of four floats into another block's shared memory, completing 16
+// transaction bytes on that block's mbarrier `rbar`.
+__device__ __forceinline__ void st_async4(uint32_t raddr, float4 v, uint32_t rbar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+      ::"r"(raddr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(rbar)
+      : "memory");
+}
+
+// The rows of a tile (count of them) that this block ends, once all parts have landed
+// (a bounded wait): a warp a row, two dims a lane.
+__device__ __forceinline__ void end_rows(RowInbox& inbox, const TreeWork& work, float* out,
+                                         int* err, int warp, int lane) {
+  const int S = gridDim.x, rank = blockIdx.x;
+  const int rows = work.count * kGroup;
+  if (rank + warp * S >= rows) return;
+  if (!__all_sync(0xffffffffu, pkv_decode::mbar_wait_cluster(&inbox.bar, 0))) {
+    if (lane == 0) set_error(err, PKV_DEV_ERR_TIMEOUT);
+    return;
+  }
+  for (int i = warp; rank + i * S < rows; i += kFewWarps) {
+    const float2 part = lane < S ? inbox.ml[i * S + lane] : make_float2(-INFINITY, 0.f);
+    float most = part.x;
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float w = part.x == -INFINITY ? 0.f : fast_exp2(part.x - most);
+    float l = w * part.y;
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float2 sum = make_float2(0.f, 0.f);
+    #pragma unroll
+    for (int p = 0; p < kMaxParts; ++p)
+      if (p < S) {
+        const float wp = __shfl_sync(0xffffffffu, w, p);
+        const float2 x = *reinterpret_cast<const float2*>(&inbox.o[i * S + p][2 * lane]);
+        sum.x += wp * x.x;
+        sum.y += wp * x.y;
+      }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int r = rank + i * S;
+    *reinterpret_cast<float2*>(
+        out + ((static_cast<size_t>(work.row) + (r >> 2)) * kHq + work.g * kGroup + (r & 3)) * kDim +
+        2 * lane) = make_float2(sum.x * inv, sum.y * inv);
+  }
 }
 
 __device__ __forceinline__ float quad_max(float x) {
@@ -228,7 +290,9 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
   }
 }
 
-template <int kHalves>
+// kCluster: grid (parts, KV heads, tiles), a tile's parts in a cluster; otherwise the
+// blocks share the line.
+template <int kHalves, bool kCluster>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_few_kernel(
     const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
     const uint16_t* __restrict__ q, const TreeParams prm) {
@@ -237,18 +301,23 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
   using Smem = FewSmem<kHalves>;
   Smem& sm = *reinterpret_cast<Smem*>(
       smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  RowInbox& inbox = *reinterpret_cast<RowInbox*>(&sm + 1);     // kCluster
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int g8 = lane >> 2;
   const int qq = lane & 3;
-  const int kvh = blockIdx.x % kHkv;
+  const int kvh = kCluster ? blockIdx.y : blockIdx.x % kHkv;
   pkv_decode::PageRing<kFewStages>& ring = sm.warp[warp];
   unsigned long long* bars = sm.bar[warp];
   // the kernel that joins the parts may be made ready (it waits for this one's end)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!kCluster) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // every warp walks the line for itself
   TreeWalk<kTokens> walk;
-  walk.fetch(prm, lane);
+  TreeLane<kTokens> lists;
+  if constexpr (kCluster)
+    lists.load(prm, lane, blockIdx.x + blockIdx.y + blockIdx.z == 0);
+  else
+    walk.fetch(prm, lane);
   if (lane == 0) {
     for (int s = 0; s < kFewStages; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
@@ -262,7 +331,24 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
 
   uint32_t used = 0;                  // pages that went through the ring
   TreeWork work;
-  while (walk.next(0, prm, lane, work)) {
+  auto next = [&]() {
+    if constexpr (!kCluster) return walk.next(0, prm, lane, work);
+    work.g = kvh;
+    // the same decision in every block of the cluster; returns after its one part
+    return part_of_tile<kTokens>(prm, lists, blockIdx.z, blockIdx.x, gridDim.x, lane, work);
+  };
+  while (next()) {
+    if constexpr (kCluster) {
+      const int S = gridDim.x, rank = blockIdx.x;
+      const int ends = max(work.count * kGroup - rank + S - 1, 0) / S;     // rows
+      if (threadIdx.x == 0 && ends > 0) {
+        mbar_init(&inbox.bar, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&inbox.bar, ends * S * kRowPartBytes);
+      }
+      __syncwarp();
+      pkv_decode::cluster_arrive_release();
+    }
     const TreeView view(work, prm);
     const int mine = work.steps;      // this warp's pages: one of every step
     const int32_t* row = prm.table + static_cast<size_t>(work.b) * prm.table_stride;
@@ -394,7 +480,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
             make_float2(st.o[i / 2][n][2 * (i % 2)], st.o[i / 2][n][2 * (i % 2) + 1]);
     }
     __syncthreads();
-    if (sm.abort) return;             // the same decision in every warp
+    // the same decision in every warp; a cluster's other blocks expect their parts
+    if (!kCluster && sm.abort) return;
+    // every block's inbox is ready
+    if constexpr (kCluster) pkv_decode::cluster_wait_acquire();
     // 8 threads a row, two float4 each, 16 rows at a time
     #pragma unroll
     for (int pass = 0; pass < kHalves; ++pass) {
@@ -419,6 +508,19 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
             sum[h].w += f * x.w;
           }
         }
+        if constexpr (kCluster) {
+          const int S = gridDim.x;
+          const uint32_t end = r % S;
+          const int slot = r / S * S + blockIdx.x;
+          const uint32_t rbar = pkv_decode::cluster_addr(&inbox.bar, end);
+          #pragma unroll
+          for (int h = 0; h < 2; ++h)
+            st_async4(pkv_decode::cluster_addr(&inbox.o[slot][4 * at + 32 * h], end), sum[h], rbar);
+          if (at == 0)
+            pkv_decode::st_async2(pkv_decode::cluster_addr(&inbox.ml[slot], end),
+                                  make_float2(M, L), rbar);
+          continue;
+        }
         float4* to;
         if (work.slot < 0) {
           const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -437,6 +539,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
         to[at + 8] = sum[1];
       }
     }
+    if constexpr (kCluster) {
+      end_rows(inbox, work, prm.out, prm.err, warp, lane);
+      return;
+    }
     // the rings are copied into again
     pkv_prefill_dev::fence_proxy_async_smem();
     __syncthreads();
@@ -446,24 +552,75 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
 }  // namespace
 
 bool pkv_tree_few_setup() {
-  return cudaFuncSetAttribute(tree_few_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(tree_few_kernel<1, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(kFewSmemBytes<1>)) == cudaSuccess &&
-         cudaFuncSetAttribute(tree_few_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kFewSmemBytes<2>)) == cudaSuccess;
+         cudaFuncSetAttribute(tree_few_kernel<2, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kFewSmemBytes<2>)) == cudaSuccess &&
+         cudaFuncSetAttribute(tree_few_kernel<2, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kClusterSmemBytes)) == cudaSuccess &&
+         cudaFuncSetAttribute(tree_few_kernel<2, true>,
+                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
 }
 
 template <int kHalves>
-static pkv_status launch_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
-                             const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
+static pkv_status launch_line(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
+                              const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
   set_wave(&prm, kFewBlocksPerSm<kHalves> * pool->num_sms);
-  tree_few_kernel<kHalves><<<prm.wave * kHkv, kFewThreads, kFewSmemBytes<kHalves>, st>>>(
+  tree_few_kernel<kHalves, false><<<prm.wave * kHkv, kFewThreads, kFewSmemBytes<kHalves>, st>>>(
       tk, tv, static_cast<const uint16_t*>(q), prm);
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   return launch_join<kFewTokens<kHalves>>(prm, st);
 }
 
+static pkv_status launch_cluster(const void* q, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const TreeParams& prm, int parts, cudaStream_t st) {
+  // no sequences of so many tokens have more tiles
+  const int sequences = std::min(prm.batch, prm.total_tokens);
+  const int tiles = (prm.total_tokens + (kFewTokens<2> - 1) * sequences) / kFewTokens<2>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts, kHkv, tiles);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kClusterSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = parts;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tree_few_kernel<2, true>, tk, tv, static_cast<const uint16_t*>(q),
+                         prm) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  return pkv_check_launch();
+}
+
+// The blocks of a tile's cluster: the largest of 16, 8 and 4 whose blocks are all
+// resident at once if the sequences bring equally many tokens, while it leaves a block
+// no more than 512 committed tokens; 0: the line. Measured (us, clusters and the line;
+// sequences x drafted tokens over committed ones): of 16 1 x 8 over 2,000 7.7 and 8.8, 1
+// x 4 over 8,000 12.2 and 13.3, over 16,000 19.5 and 16.2; of 8 4 x 8 over 2,000 10.3 and
+// 12.6, 6 x 8 12.2 and 14.7, 4 x 4 over 8,000 19.9 and 19.0; of 4 8 x 8 over 2,000 15.9
+// and 16.4, 12 x 4 14.8 and 16.6, 8 x 4 over 300 6.7 and 7.7. Too large ones: of 16 3 x 8
+// over 2,000 11.6 (of 8 10.3).
+int pkv_tree_cluster(const pkv_pool* pool, int batch, int total_tokens, int seen_tokens) {
+  const long long sequences = std::min(batch, total_tokens);
+  const long long each = sequences * kFewTokens<2>;
+  const long long blocks = sequences * ((total_tokens + each - 1) / each) * kHkv;
+  const long long slots = static_cast<long long>(kFewBlocksPerSm<2>) * pool->num_sms;
+  const int parts = batch > 32                          ? 0
+                    : blocks * 16 <= slots * 9 / 16     ? 16
+                    : blocks * 8 <= slots * 27 / 32     ? 8
+                    : blocks * 4 <= slots * 27 / 32     ? 4
+                                                        : 0;
+  return parts <= pool->max_cluster && seen_tokens <= kPartTokens * parts ? parts : 0;
+}
+
 pkv_status pkv_tree_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
-                        const CUtensorMap& tv, TreeParams prm, cudaStream_t st) {
+                        const CUtensorMap& tv, TreeParams prm, int parts, cudaStream_t st) {
+  if (parts > 0) return launch_cluster(q, tk, tv, prm, parts, st);
   // Tiles of 4 tokens, and a block more per SM, where sequences bring no more on
   // average and there are several for each block (us, with tiles of 4 and of 8: 4,096
   // sequences x 2 over 64 committed tokens 321 and 392, 1,024 x 4 over 300 136 and 158,
@@ -471,6 +628,6 @@ pkv_status pkv_tree_few(pkv_pool_t pool, const void* q, const CUtensorMap& tk,
   // 13.0).
   const int wave = kFewBlocksPerSm<1> * pool->num_sms / kHkv;
   return prm.total_tokens <= 4ll * prm.batch && prm.batch >= 2 * wave
-             ? launch_few<1>(pool, q, tk, tv, prm, st)
-             : launch_few<2>(pool, q, tk, tv, prm, st);
+             ? launch_line<1>(pool, q, tk, tv, prm, st)
+             : launch_line<2>(pool, q, tk, tv, prm, st);
 }

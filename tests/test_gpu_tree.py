@@ -119,6 +119,24 @@ def test_few_rows_over_long_contexts():
     run_tree([60000, 33333], [4, 3], max_seq_len=65536, window=3000, sinks=20)
 
 
+@pytest.mark.parametrize("starts,nodes,max_seq_len", [
+    # parts of a tile in clusters of 16, 8 and 4; sequences without tokens, tiles that are
+    # not there, more parts than steps
+    ([1999], [8], 2048), ([0], [16], 2048), ([700], [41], 2048), ([1000, 3], [25, 3], 2048),
+    ([1900, 0, 40, 7, 333], [1, 8, 9, 2, 5], 2048),
+    ([50 * i for i in range(32)], [[0, 0, 5, 0, 1, 0, 0, 2][i % 8] // (1 + i // 8) for i in range(32)],
+     2048),
+    ([200 * i for i in range(8)], [3, 1, 9, 0, 1, 4, 3, 5], 2048), ([90, 2], [9, 7], 2048),
+    ([0, 64, 1990], [0, 12, 0], 2048), ([8000], [5], 8192), ([4000, 100], [20, 7], 4096)])
+@pytest.mark.parametrize("window,sinks", [(1 << 20, 0), (37, 4)])
+def test_clusters(starts, nodes, max_seq_len, window, sinks):
+    run_tree(starts, nodes, window=window, sinks=sinks, max_seq_len=max_seq_len, seed=sum(nodes))
+
+
+def test_a_window_makes_clusters_of_a_long_context():
+    run_tree([60000], [8], max_seq_len=65536, window=3000, sinks=20)
+
+
 @pytest.mark.parametrize("batch", [39, 65, 150])
 def test_many_sequences(batch):
     rng = np.random.RandomState(batch)
@@ -289,6 +307,50 @@ def test_captured_with_changing_lengths():
         start.copy_(int32(starts))
         flat = pack(sum(masks, []))
         tree[:flat.numel()].copy_(flat)
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        row = 0
+        for b, n in enumerate(nodes):
+            if n:
+                ref, tol = attend(q[row:row + n].double(), c.k[b][:starts[b] + n].double(),
+                                  c.v[b][:starts[b] + n].double(),
+                                  seen_matrix(starts[b], masks[b], 2048, 0))
+                check(out[row:row + n], ref, tol)
+            row += n
+        assert bool((out[row:] == 3.0).all())
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+
+
+def test_captured_clusters_with_changing_lengths():
+    c = Cache([1900, 700, 64], seed=17)
+    k_pool, v_pool = c.pools(lambda b: np.ones(c.lens[b], bool))
+    total = 24
+    q = normal(2, total, HQ, DIM)
+    out = torch.zeros(total, HQ, DIM, device="cuda")
+    pool = handle(c)
+    rng = np.random.RandomState(17)
+    cu, start = int32([0, 8, 16, 24]), int32([0, 0, 0])
+    tree = torch.zeros(total, dtype=torch.int64, device="cuda")
+
+    def call():
+        pkv.pkv_tree_attention(pool, 0, q, k_pool, v_pool, c.tables, cu, start, tree, out, 2048)
+
+    call()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            call()
+    for starts, nodes in (([1880, 680, 44], [8, 8, 8]), ([0, 3, 40], [1, 23, 0]),
+                          ([1800, 1, 0], [0, 0, 2]), ([5, 600, 9], [0, 0, 0]),
+                          ([1892, 0, 0], [6, 9, 9])):
+        masks = [random_tree(rng, n) for n in nodes]
+        cu.copy_(int32(np.cumsum([0] + nodes)))
+        start.copy_(int32(starts))
+        flat = pack(sum(masks, []) + [0] * (total - sum(nodes)))
+        tree.copy_(flat)
         out.fill_(3.0)
         graph.replay()
         torch.cuda.synchronize()
