@@ -137,7 +137,8 @@ __device__ __forceinline__ void end_rows(RowInbox& inbox, const TreeWork& work, 
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int r = rank + i * S;
     *reinterpret_cast<float2*>(
-        out + ((static_cast<size_t>(work.row) + (r >> 2)) * kHq + work.g * kGroup + (r & 3)) * kDim +
+        out +
+        ((static_cast<size_t>(work.row) + (r >> 2)) * kHq + work.g * kGroup + (r & 3)) * kDim +
         2 * lane) = make_float2(sum.x * inv, sum.y * inv);
   }
 }
