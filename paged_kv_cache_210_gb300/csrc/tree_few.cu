@@ -380,20 +380,22 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
     if (threadIdx.x < kTokens)
       sm.mask[threadIdx.x] = prm.tree[work.row + min(static_cast<int>(threadIdx.x),
                                                      work.count - 1)];
-    // Copy engine: K and V of page j into its stage, from lanes 0 and 1.
+    // Copy engine: K and V of page j into its stage, by one lane from operands that the
+    // warp shares (those of a lane's own take a loop over the lanes).
     auto issue = [&](int j) {
       const int stage = (used + j) % kFewStages;
       const int id = __shfl_sync(0xffffffffu, ids, j & 31);
-      if (id == -1 && lane == 0) set_error(prm.err, PKV_DEV_ERR_PAGE);
-      if (lane > 1) return;
-      if (id >= 0) {
-        if (lane == 0) mbar_arrive_expect_tx(&bars[stage], 2 * kFewTileBytes);
-        __syncwarp(0x3u);   // the expected bytes are set before either copy can land
-        pkv_decode::tma_load_tile(lane == 0 ? ring.k[stage] : ring.v[stage],
-                                  lane == 0 ? &tmap_k : &tmap_v, kvh * kPage, id, &bars[stage]);
-      } else if (lane == 0) {
-        mbar_arrive(&bars[stage]);
+      if (elect_one()) {
+        if (id >= 0) {
+          mbar_arrive_expect_tx(&bars[stage], 2 * kFewTileBytes);
+          pkv_decode::tma_load_tile(ring.k[stage], &tmap_k, kvh * kPage, id, &bars[stage]);
+          pkv_decode::tma_load_tile(ring.v[stage], &tmap_v, kvh * kPage, id, &bars[stage]);
+        } else {
+          if (id == -1) set_error(prm.err, PKV_DEV_ERR_PAGE);
+          mbar_arrive(&bars[stage]);
+        }
       }
+      __syncwarp();
     };
     int issued = min(mine, kFewStages);
     uint32_t good = __ballot_sync(0xffffffffu, ids >= 0);   // of the 32 pages in `ids`
