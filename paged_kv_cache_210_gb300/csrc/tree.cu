@@ -130,16 +130,16 @@ __global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
   }
 }
 
-// Whether the kernel for few rows takes the call: where clusters of 8 or 16 blocks do,
-// or for up to 4 drafted tokens a sequence on average, 8 in short contexts. Measured (us,
-// this and the other kernel; sequences x drafted tokens, 2,000 committed): with clusters
-// 1 x 8 7.7 and 12.9, 1 x 48 12.1 and 14.8, 3 x 16 12.0 and 14.1; 1 x 8 over 8,000 14.8
-// and 17.3; on the line, or in clusters of 4, 8 x 4 12.8 and 17.1, 128 x 4 93 and 119, 32
-// x 8 39.2 and 40.1, 2 x 32 15.1 and 15.3, 1 x 64 15.4 and 15.3, 1 x 8 over 16,000 (line)
-// 21.7 and 19.6.
-bool few_rows(int max_seq_len, int batch, int total_tokens, int parts) {
-  return parts >= 8 || total_tokens <= 4ll * batch ||
-         (max_seq_len <= 2048 && total_tokens <= 8ll * batch);
+// Whether the kernel for few rows takes the call: where it does so in clusters, or for
+// up to 8 drafted tokens a sequence on average. Measured (us, this and the other kernel;
+// sequences x drafted tokens, 2,000 committed): in clusters 1 x 8 7.4 and 12.9, 1 x 64
+// 14.3 and 15.4, 3 x 16 11.6 and 14.2, 4 x 16 14.1 and 15.3, over 300 7.9 and 11.6, 1 x 8
+// over 8,000 13.6 and 17.2; on the line 16 x 8 23.5 and 25.8, 32 x 8 36.4 and 40.4, 128 x
+// 4 91 and 119, 256 x 8 over 1,000 124 and 139, 1 x 8 over 16,000 20.5 and 20.4, 8 x 8
+// 59.5 and 60.7, 2 x 8 over 100,000 87.0 and 88.4; 8 x 16 22.5 and 19.3, 32 x 16 64 and
+// 47.
+bool few_rows(int batch, int total_tokens, int parts) {
+  return parts > 0 || total_tokens <= 8ll * batch;
 }
 
 }  // namespace
@@ -175,7 +175,7 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   const long long seen = std::min<long long>(c.max_seq_len, static_cast<long long>(window) + sinks +
                                                                 kMaxTree + 2 * kPage);
   const int parts = pkv_tree_cluster(pool, batch, total_tokens, static_cast<int>(seen));
-  const bool few = few_rows(c.max_seq_len, batch, total_tokens, parts);
+  const bool few = few_rows(batch, total_tokens, parts);
   const cuuint64_t dims[3] = {kDim, kHq, static_cast<cuuint64_t>(total_tokens)};
   const cuuint64_t strides[2] = {kRowBytes, static_cast<cuuint64_t>(kHq) * kRowBytes};
   const cuuint32_t box[3] = {kDim, kGroup, kTileTokens};

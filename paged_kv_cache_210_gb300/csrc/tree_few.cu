@@ -18,11 +18,13 @@
 // BF16 terms of the weights), 8 cycles each on a quarter of an SM: three warps there
 // take a page each in about 2,000 cycles, 1,536 of them products, where the decode's
 // four rows hide under the copies. So it serves few tokens: one tree of 8 over 2,000
-// tokens 7.7 us (tcgen05 12.9), 128 trees of 4 over 2,000 93 us (119; the bytes alone
+// tokens 7.4 us (tcgen05 12.9), 128 trees of 4 over 2,000 90 us (119; the bytes alone
 // 80); which calls it takes is decided in tree.cu. Many short sequences are bound by the
 // start and the end of their tiles, some 5 us each for a block: 1,024 trees of 4 over
-// 300 tokens 136 us (the bytes 103), 4,096 of 2 over 64 321 (98). One tree of 8 over 2,000
-// tokens is latency: on the line 8.8 us, the join 2 of them, in clusters of 16 7.7.
+// 300 tokens 130 us (the bytes 103), 4,096 of 2 over 64 310 (98). One tree of 8 over 2,000
+// tokens is latency: on the line 8.3 us, the join 2 of them, in clusters of 16 7.4;
+// without the products 5.3. (Blocks of 8 warps, one an SM: 11.9, not all of their
+// clusters of 16 are resident at once.)
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -603,11 +605,10 @@ static pkv_status launch_cluster(const void* q, const CUtensorMap& tk, const CUt
 // The blocks of a tile's cluster: the largest of 16, 8 and 4 whose blocks are all
 // resident at once if the sequences bring equally many tokens, while it leaves a block
 // no more than 512 committed tokens; 0: the line. Measured (us, clusters and the line;
-// sequences x drafted tokens over committed ones): of 16 1 x 8 over 2,000 7.7 and 8.8, 1
-// x 4 over 8,000 12.2 and 13.3, over 16,000 19.5 and 16.2; of 8 4 x 8 over 2,000 10.3 and
-// 12.6, 6 x 8 12.2 and 14.7, 4 x 4 over 8,000 19.9 and 19.0; of 4 8 x 8 over 2,000 15.9
-// and 16.4, 12 x 4 14.8 and 16.6, 8 x 4 over 300 6.7 and 7.7. Too large ones: of 16 3 x 8
-// over 2,000 11.6 (of 8 10.3).
+// sequences x drafted tokens over committed ones): of 16 1 x 8 over 2,000 7.4 and 8.3, 1
+// x 4 over 8,000 10.8 and 12.8, over 16,000 16.6 and 15.9; of 8 4 x 8 over 2,000 9.7 and
+// 12.3, 6 x 8 11.6 and 14.2; of 4 8 x 8 over 2,000 14.6 and 15.6, 12 x 4 14.4 and 16.3, 8
+// x 4 over 300 6.2 and 7.2. Too large ones: of 16 3 x 8 over 2,000 11.6 (of 8 9.7).
 int pkv_tree_cluster(const pkv_pool* pool, int batch, int total_tokens, int seen_tokens) {
   const long long sequences = std::min(batch, total_tokens);
   const long long each = sequences * kFewTokens<2>;
