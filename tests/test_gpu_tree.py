@@ -133,6 +133,32 @@ def test_clusters(starts, nodes, max_seq_len, window, sinks):
     run_tree(starts, nodes, window=window, sinks=sinks, max_seq_len=max_seq_len, seed=sum(nodes))
 
 
+@pytest.mark.parametrize("start", [0, 1, 15, 17, 63, 64, 1000, 8100])
+@pytest.mark.parametrize("nodes", [17, 32, 33, 64])
+def test_large_trees_of_one_sequence(start, nodes):
+    # too long a context for clusters
+    run_tree([start], [nodes], max_seq_len=8192, window=1 << 20, seed=start + nodes)
+    run_tree([start], [nodes], max_seq_len=16384, window=5000, sinks=3, seed=start)
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 20, 0), (90, 6)])
+@pytest.mark.parametrize("max_seq_len", [2048, 4096])
+def test_trees_of_eight_on_average(max_seq_len, window, sinks):
+    starts = [121 * i for i in range(16)]
+    run_tree(starts, [1 + i % 15 for i in range(16)], max_seq_len=max_seq_len, window=window,
+             sinks=sinks, seed=sinks)
+
+
+@pytest.mark.parametrize("start", [0, 5, 380])
+def test_any_mask_of_a_long_context(start):
+    n = 50
+    rng = np.random.RandomState(start)
+    every = (1 << 64) - 1
+    masks = [0, every, 1 << 49, 2, every << 50 & every, 1] + \
+        [int(rng.randint(0, 1 << 32)) << 32 | int(rng.randint(0, 1 << 32)) for _ in range(n - 6)]
+    run_tree([start], [n], masks=[masks], max_seq_len=8192, window=45 if start > 5 else 1 << 20)
+
+
 def test_a_window_makes_clusters_of_a_long_context():
     run_tree([60000], [8], max_seq_len=65536, window=3000, sinks=20)
 
