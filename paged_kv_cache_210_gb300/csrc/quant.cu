@@ -52,8 +52,8 @@ namespace {
 // FP16 has 11 bits and a narrow range: a factor that needs 24 bits (a rotated
 // query, a weight) is the sum of two FP16 terms after a scaling by a power of
 // two, one per head: queries so that the largest of 64 dims lies in [2^14,
-// 2^15), weights p 2^ev so that the largest seen lies in [2^7, 2^15]. Terms lose
-// what lies 2^-31 and more below the largest.
+// 2^15), weights p 2^ev so that the largest up to here, as it counts now, lies in
+// [2^7, 2^15]. Terms lose what lies 2^-31 and more below the largest.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
@@ -96,6 +96,11 @@ __device__ __forceinline__ uint32_t half_terms(float x0, float x1, uint16_t m) {
 __device__ __forceinline__ float row_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// 2^n for n <= 0, exact; 0 below 2^-126.
+__device__ __forceinline__ float power_of_2(int n) {
+  return scale_of(static_cast<uint32_t>(max(n + 127, 0)));
 }
 
 // -FLT_MAX, no finite score lies below it: with it as the exponent of a row that saw
@@ -368,28 +373,37 @@ struct QuantTiles {
       }
     };
     // Taken against the state as it is. Where a row's maximum passes the exponent
-    // that p is taken against (p would pass 1), that one moves to 8 above it; where
-    // its weighted rows pass 2^15 units, the unit moves. Both are rare.
+    // that p is taken against (p would pass 1), that one moves to 8 above it, by
+    // whole powers of two; where that happens or the weighted rows pass 2^15 units,
+    // the unit is chosen anew. Both are rare.
     const float lane_top = largest(s) * q.to_log2;
     exponentials();
     const float lane_most = largest(w) * st.unit;
     if (__any_sync(0xffffffffu, lane_top > st.m_run || !(lane_most <= 32768.f))) {
       const float top = row_max(lane_top);
-      float factor = 1.f;
+      int shift = 0;                       // the sums held shrink by 2^-shift
       if (top > st.m_run) {
-        factor = fast_exp2(st.m_run - (top + kRescaleLog2));   // 0 on the first page
-        st.m_run = top + kRescaleLog2;
-        st.l_run *= factor;
+        const float m = floorf(top) + kRescaleLog2;
+        shift = static_cast<int>(fminf(m - st.m_run, 512.f));
+        st.m_run = m;
+        st.l_run *= power_of_2(-shift);    // 0 on the first page
       }
       exponentials();
       const float most = row_max(largest(w));
-      if (most * st.unit > 32768.f) {
-        // 2^(7 - floor(log2 most)): the largest then lies in [2^7, 2^8)
-        const float unit = scale_of(261u - (__float_as_uint(most) >> 23));
-        factor *= unit * inverse_scale_of(__float_as_uint(st.unit) >> 23);
-        st.unit = unit;
+      int by = 0;                          // what they are multiplied by: 2^by <= 1
+      if (shift > 0 || most * st.unit > 32768.f) {
+        // 2^(7 - floor(log2 most)) puts the group's largest into [2^7, 2^8). The unit
+        // rises as far as the sums held shrank and no further, so that of the rows that
+        // they hold none passes 2^15: the largest weighted row up to here, old or new,
+        // lies in [2^7, 2^15]. (A unit that did not rise again left rows of ordinary size
+        // nothing behind one of 2^35 whose weight had become negligible.)
+        const int was = static_cast<int>(__float_as_uint(st.unit) >> 23);
+        const int byte = min(min(261 - static_cast<int>(__float_as_uint(most) >> 23), 253),
+                             was + shift);
+        st.unit = scale_of(static_cast<uint32_t>(byte));
+        by = byte - was - shift;
       }
-      st.rescale(factor, lane);
+      st.rescale(power_of_2(by), lane);
     }
     st.l_run += sum.x + sum.y;
     const float2 unit = make_float2(st.unit, st.unit);

@@ -1,0 +1,88 @@
+"""The 8-bit decode on the GPU over the range of scores and values that a cache may
+hold, against a 64-bit restatement, with tolerances that go by what each token weighs."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_210_gb300 as pkv
+from quant_helpers import QuantCache, quantise
+from window_helpers import DIM, HKV, HQ, U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _library():
+    from paged_kv_cache_210_gb300 import build as lib_build
+    lib_build.build()
+
+
+def int32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def run_scores_and_sizes(score, size, window=2048, sinks=0, splits=1, seed=0):
+    """Token t has base-e score score[t] and V of size[t] times normal values; every
+    head's query and keys have one dim, so products and scores are exact and the rest
+    of the arithmetic can be held to what each token weighs. p the weights, V_t the
+    largest |v| of a row, A = sum p V / sum p. A weight is off by e = 3 u (|s| + |s_max| +
+    8) + 2^-21 (the exponent's argument; its base-2 exponential here and in the merge) and
+    2^-22 (two FP16 terms), or by 2^-32 of the largest weighted row and code, 2^-31
+    max p V; the sums by 2 (n / 16 + 16) u A."""
+    n = len(score)
+    c = QuantCache([n], seed=seed)
+    pool, kv = pkv.pkv_pool_create(1, c.num_pages, 1), c.pool()
+    g = torch.Generator().manual_seed(seed)
+    ks = torch.zeros(n, HKV, DIM)
+    ks[:, :, 5] = torch.as_tensor(score)[:, None]
+    vs = torch.randn(n, HKV, DIM, generator=g) * torch.as_tensor(size)[:, None, None]
+    ks, vs = ks.bfloat16(), vs.bfloat16()
+    q = torch.zeros(1, HQ, DIM, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 5] = 8.0
+    pkv.pkv_quant_fill(pool, 0, ks.cuda(), vs.cuda(), kv, c.tables, int32([0, n]), int32([0]), n)
+    out = torch.empty(1, HQ, DIM, device="cuda")
+    pkv.pkv_quant_attention(pool, 0, q, kv, c.tables, c.lens_tensor(), out, window, sinks=sinks,
+                            num_splits=splits)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    t = torch.arange(n)
+    seen = (t > n - 1 - window) | (t < sinks)
+    s = quantise(ks.double())[2][seen][:, :, 5].T                    # [8][tokens]
+    v = quantise(vs.double())[2][seen].permute(1, 0, 2)              # [8][tokens][64]
+    w = torch.exp(s - s.amax(1, keepdim=True))
+    total = w.sum(1, keepdim=True)
+    ref = (w[:, None] @ v)[:, 0] / total
+    most = v.abs().amax(2)
+    a = (w * most).sum(1, keepdim=True) / total
+    e = 3 * U * (s.abs() + s.abs().amax(1, keepdim=True) + 8) + 2.0 ** -21 + 2.0 ** -22
+    tol = ((w * e * most).sum(1, keepdim=True) + (w * e).sum(1, keepdim=True) * a) / total + \
+        2 * (seen.sum() / 16 + 16) * U * a + \
+        seen.sum() * 2.0 ** -31 * (w * most).amax(1, keepdim=True) / total
+    off = (out[0].double().cpu() - ref.repeat_interleave(HQ // HKV, 0)).abs()
+    worst = float((off / tol.repeat_interleave(HQ // HKV, 0)).amax())
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("splits", [1, 0])
+@pytest.mark.parametrize("bits,down", [(20, 72), (35, 72), (60, 72), (100, 72), (40, 16), (24, 16),
+                                       (60, 40)])
+@pytest.mark.parametrize("where", ["first", "sinks", "middle"])
+def test_large_values_whose_weights_become_small(where, bits, down, splits):
+    # every warp meets V of 2^bits with scores `down` below those that follow, whose V is
+    # of ordinary size (or, in the middle, lies on both sides)
+    n = 600
+    rng = np.random.RandomState(bits)
+    score, size = rng.randn(n), np.ones(n)
+    rows = slice(128, 256) if where == "middle" else slice(0, 128)
+    score[rows] -= down
+    size[rows] = 2.0 ** bits
+    kw = dict(window=300, sinks=100) if where == "sinks" else {}
+    run_scores_and_sizes(score, size, splits=splits, seed=bits, **kw)
+
+
+@pytest.mark.parametrize("step,bits", [(16, 20), (16, 26), (12, 30), (3, 5), (40, 20)])
+def test_values_that_shrink_as_scores_rise(step, bits):
+    # in every group of a warp again: V 2^-bits of the last one's, scores `step` above
+    group = np.arange(640) // 128
+    run_scores_and_sizes(group * step + np.random.RandomState(step).randn(640) / 4,
+                         2.0 ** (bits * (2.0 - group)), seed=bits)
