@@ -27,6 +27,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pkv.h"
 #include "pkv_quant.h"
 #include "quant.cuh"
@@ -113,6 +115,20 @@ constexpr float kNone = -0x1.fffffep127f;
 // Exact: 2^-16 2^ek is a power of two >= 2^-140.
 constexpr float kScoreUnit = 0x1p-16f;
 
+// Whether base-2 scores are rounded before the exponent m_run = x is taken from them
+// (finite, 2^24 or more). With the product kept whole, a difference that should be 0 is the
+// maximum's rounding, and its exponential 0 or infinite from scores of 2^31 on.
+__device__ __forceinline__ bool is_huge(float x) {
+  constexpr uint32_t kHuge = (24u + 127u) << 23, kInf = 0x7f800000u;
+  return (__float_as_uint(x) & 0x7fffffffu) - kHuge < kInf - kHuge;
+}
+
+// Base-2 scores s c less m, the product rounded or not. (By scalar intrinsics: those on
+// pairs may be contracted.)
+__device__ __forceinline__ float less(float s, float c, float m, bool rounded) {
+  return __fmaf_rn(rounded ? __fmul_rn(s, c) : s, rounded ? 1.f : c, -m);
+}
+
 struct QuantTiles {
   // With 3, 4 sequences of 131,072 tokens take 92 us instead of 84.
   static constexpr int kStages = 2;
@@ -138,7 +154,8 @@ struct QuantTiles {
     float m_run;     // the base-2 exponent p is taken against: p = 2^(x - m_run) <= 1
                      // (kNone: nothing seen yet)
     float l_run;     // this lane's share of the head's sum
-    float unit;      // the power of two that the weights p 2^ev are scaled by
+    float unit;      // the power of two that the weights p 2^ev are scaled by; negative
+                     // where m_run is huge
     __device__ __forceinline__ void reset() {
       #pragma unroll
       for (int c = 0; c < 4; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
@@ -361,12 +378,19 @@ struct QuantTiles {
       }
     }
     const float2 to_log2 = make_float2(q.to_log2, q.to_log2);
-    auto exponentials = [&]() {
+    auto exponentials = [&](auto may_be_huge) {
       const float2 minus = make_float2(-st.m_run, -st.m_run);
       sum = make_float2(0.f, 0.f);
       #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt) {
-        const float2 x = __ffma2_rn(s[nt], to_log2, minus);
+        float2 x;
+        if constexpr (decltype(may_be_huge)::value) {
+          const bool rounded = is_huge(st.m_run);
+          x.x = less(s[nt].x, q.to_log2, st.m_run, rounded);
+          x.y = less(s[nt].y, q.to_log2, st.m_run, rounded);
+        } else {
+          x = __ffma2_rn(s[nt], to_log2, minus);
+        }
         const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
         sum = __fadd2_rn(sum, p);
         w[nt] = __fmul2_rn(p, scale_v[nt]);
@@ -375,11 +399,13 @@ struct QuantTiles {
     // Taken against the state as it is. Where a row's maximum passes the exponent
     // that p is taken against (p would pass 1), that one moves to 8 above it, by
     // whole powers of two; where that happens or the weighted rows pass 2^15 units,
-    // the unit is chosen anew. Both are rare.
+    // the unit is chosen anew. Both are rare. Once a head's exponent is huge every group
+    // comes by here: its unit is negative, which as an integer passes too.
     const float lane_top = largest(s) * q.to_log2;
-    exponentials();
+    exponentials(std::false_type());
     const float lane_most = largest(w) * st.unit;
-    if (__any_sync(0xffffffffu, lane_top > st.m_run || !(lane_most <= 32768.f))) {
+    if (__any_sync(0xffffffffu, lane_top > st.m_run ||
+                                    __float_as_uint(lane_most) > __float_as_uint(32768.f))) {
       const float top = row_max(lane_top);
       int shift = 0;                       // the sums held shrink by 2^-shift
       if (top > st.m_run) {
@@ -388,9 +414,10 @@ struct QuantTiles {
         st.m_run = m;
         st.l_run *= power_of_2(-shift);    // 0 on the first page
       }
-      exponentials();
+      exponentials(std::true_type());
       const float most = row_max(largest(w));
       int by = 0;                          // what they are multiplied by: 2^by <= 1
+      st.unit = fabsf(st.unit);
       if (shift > 0 || most * st.unit > 32768.f) {
         // 2^(7 - floor(log2 most)) puts the group's largest into [2^7, 2^8). The unit
         // rises as far as the sums held shrank and no further, so that of the rows that
@@ -404,6 +431,11 @@ struct QuantTiles {
         by = byte - was - shift;
       }
       st.rescale(power_of_2(by), lane);
+      if (is_huge(st.m_run)) {
+        st.unit = -st.unit;
+        #pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) w[nt] = make_float2(-w[nt].x, -w[nt].y);
+      }
     }
     st.l_run += sum.x + sum.y;
     const float2 unit = make_float2(st.unit, st.unit);
@@ -475,7 +507,7 @@ struct QuantTiles {
     const int qq = lane & 3;
     st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 1);
     st.l_run += __shfl_xor_sync(0xffffffffu, st.l_run, 2);
-    st.rescale(inverse_scale_of(__float_as_uint(st.unit) >> 23), lane);
+    st.rescale(inverse_scale_of(__float_as_uint(fabsf(st.unit)) >> 23), lane);
     if (qq == 0 && g8 < kGroup) {
       sm.m[warp][g8] = st.m_run;
       sm.l[warp][g8] = st.l_run;

@@ -86,3 +86,37 @@ def test_values_that_shrink_as_scores_rise(step, bits):
     group = np.arange(640) // 128
     run_scores_and_sizes(group * step + np.random.RandomState(step).randn(640) / 4,
                          2.0 ** (bits * (2.0 - group)), seed=bits)
+
+
+@pytest.mark.parametrize("splits", [1, 0, 3])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("bits", [20, 23, 24, 30, 31, 33, 40, 77, 120])
+@pytest.mark.parametrize("least", [8, 9])      # as a largest score exact in base 2, or not
+def test_huge_scores(least, bits, sign, splits):
+    # Scores of 2^bits, all different values of a code apart and each taken by tokens of
+    # several groups: those of the largest share the output equally, the others, 2^(bits -
+    # 4) or more below it, have no part of it. Equal scores get equal weights, so what is
+    # left of the tolerance above is the sums and the terms.
+    n = 700
+    rng = np.random.RandomState(bits)
+    code = rng.randint(least, 16, n)
+    code[rng.permutation(n)[:3]] = least if sign < 0 else 15
+    c = QuantCache([n], seed=bits)
+    pool, kv = pkv.pkv_pool_create(1, c.num_pages, 1), c.pool()
+    ks = torch.zeros(n, HKV, DIM)
+    ks[:, :, 7] = torch.from_numpy(sign * code / 8.0 * 2.0 ** bits)[:, None]
+    vs = torch.randn(n, HKV, DIM, generator=torch.Generator().manual_seed(bits)).bfloat16()
+    q = torch.zeros(1, HQ, DIM, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 7] = 8.0
+    pkv.pkv_quant_fill(pool, 0, ks.bfloat16().cuda(), vs.cuda(), kv, c.tables, int32([0, n]),
+                       int32([0]), n)
+    out = torch.empty(1, HQ, DIM, device="cuda")
+    pkv.pkv_quant_attention(pool, 0, q, kv, c.tables, c.lens_tensor(), out, 2048, num_splits=splits)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    first = torch.from_numpy(code == (code.min() if sign < 0 else code.max()))
+    v = quantise(vs.double())[2][first]                              # [tokens][8][64]
+    ref, most = v.mean(0), v.abs().amax((0, 2))[:, None]
+    tol = (2.0 ** -21 + 2 * (n / 16 + 16) * U) * most
+    off = (out[0].double().cpu() - ref.repeat_interleave(HQ // HKV, 0)).abs()
+    worst = float((off / tol.repeat_interleave(HQ // HKV, 0)).amax())
+    assert worst <= 1, worst
