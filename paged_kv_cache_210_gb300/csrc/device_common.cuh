@@ -111,6 +111,20 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
   return max3(__uint_as_float(a), b, c);
 }
 
+// Whether base-2 scores are rounded before a maximum x of theirs is taken from them
+// (finite, 2^24 or more). With the product kept whole, a difference that should be 0 is the
+// maximum's rounding, and its exponential 0 or infinite from scores of 2^31 on.
+__device__ __forceinline__ bool is_huge(float x) {
+  constexpr uint32_t kHuge = (24u + 127u) << 23, kInf = 0x7f800000u;
+  return (__float_as_uint(x) & 0x7fffffffu) - kHuge < kInf - kHuge;
+}
+
+// Base-2 scores s c less m, the product rounded or not. (By scalar intrinsics: those on
+// pairs may be contracted.)
+__device__ __forceinline__ float less(float s, float c, float m, bool rounded) {
+  return __fmaf_rn(rounded ? __fmul_rn(s, c) : s, rounded ? 1.f : c, -m);
+}
+
 // Two FP32 values -> BF16 pair (element 0 in the low half), each rounded to
 // nearest, ties to even.
 __device__ __forceinline__ uint32_t float2_to_bf16x2(float e0, float e1) {

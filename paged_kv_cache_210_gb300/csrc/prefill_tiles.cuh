@@ -57,6 +57,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -495,6 +496,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
       // a warp whose rows are all past the end only keeps step with the others
       const bool idle = Job::kFewRows && warp * 8 >= work.count;
       bool s_done = false;                              // the next step's S is known to be there
+      // what a step's largest score may not pass without a closer look: m_run and what p
+      // may grow by, or less where m_run is huge
+      float limit = -INFINITY;
       int segment = 0;                                  // j % kSegment, kSegment before a join
       for (int j = 0; j < n_steps; ++j, ++steps) {
         if (!wait_phase_after(s_done, &sm.bar_s, steps & 1, abort_flag)) {
@@ -561,13 +565,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
         const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         // a row that grew its max rescales its O (P(j) V(j) cannot start before
         // this thread hands over P(j))
-        const bool grow = m_step > m_run + kRescaleLog2;   // false while nothing was visible
-        if (rarely(__any_sync(0xffffffffu, grow))) {
+        float mu = m_run;
+        if (rarely(__any_sync(0xffffffffu, m_step > limit))) {   // not while nothing was visible
           float alpha = 1.f;
-          if (grow) {
+          if (m_step > m_run + kRescaleLog2) {
             alpha = fast_exp2(m_run - m_step);
             m_run = m_step;
             l_run *= alpha;
+            limit = is_huge(m_run) ? -FLT_MAX : m_run + kRescaleLog2;
+          }
+          mu = m_run;
+          if (rarely(is_huge(mu))) {
+            // the differences themselves, in the scores' unit (a factor that is not known
+            // to the compiler, in place of c, costs every step 3 %)
+            #pragma unroll
+            for (int i = 0; i < kStepKeys; ++i)
+              sv[i] = __float_as_uint(less(__uint_as_float(sv[i]), c, mu, true) * (1.f / c));
+            mu = 0.f;
           }
           if (j > 0) {
             if (!wait_phase(&sm.p_done, (steps - 1) & 1, abort_flag)) {
@@ -591,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
         // time; into tensor memory once the last step's product has read its P.
         const bool p_free = phase_done(&sm.p_done, (steps - 1) & 1);
         const float2 c2 = make_float2(c, c);
+        if (mu == -INFINITY) mu = 0.f;
         float2 acc[2];
         auto half_of_p = [&](int h, uint32_t (&hi)[16], uint32_t (&mid)[16], uint32_t (&lo)[16]) {
-          const float mu = m_run == -INFINITY ? 0.f : m_run;
           const float2 nm2 = make_float2(-mu, -mu);
           #pragma unroll
           for (int i = 0; i < 32; i += 2) {

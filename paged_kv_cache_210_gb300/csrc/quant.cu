@@ -115,20 +115,6 @@ constexpr float kNone = -0x1.fffffep127f;
 // Exact: 2^-16 2^ek is a power of two >= 2^-140.
 constexpr float kScoreUnit = 0x1p-16f;
 
-// Whether base-2 scores are rounded before the exponent m_run = x is taken from them
-// (finite, 2^24 or more). With the product kept whole, a difference that should be 0 is the
-// maximum's rounding, and its exponential 0 or infinite from scores of 2^31 on.
-__device__ __forceinline__ bool is_huge(float x) {
-  constexpr uint32_t kHuge = (24u + 127u) << 23, kInf = 0x7f800000u;
-  return (__float_as_uint(x) & 0x7fffffffu) - kHuge < kInf - kHuge;
-}
-
-// Base-2 scores s c less m, the product rounded or not. (By scalar intrinsics: those on
-// pairs may be contracted.)
-__device__ __forceinline__ float less(float s, float c, float m, bool rounded) {
-  return __fmaf_rn(rounded ? __fmul_rn(s, c) : s, rounded ? 1.f : c, -m);
-}
-
 struct QuantTiles {
   // With 3, 4 sequences of 131,072 tokens take 92 us instead of 84.
   static constexpr int kStages = 2;

@@ -158,6 +158,7 @@ struct FewState {
   float o[kHalves][8][4];
   float m[2 * kHalves];   // base-2 exponent the row's weights are taken against, p <= 2^8
   float l[2 * kHalves];   // this lane's share of the row's sum
+  uint32_t huge;          // bit i: m[i] is (is_huge)
   __device__ __forceinline__ void reset() {
     #pragma unroll
     for (int t = 0; t < kHalves; ++t)
@@ -170,6 +171,7 @@ struct FewState {
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
+    huge = 0;
   }
 };
 
@@ -238,6 +240,7 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
       if (most > st.m[i] + pkv_decode::kRescaleLog2) {
         const float alpha = fast_exp2(st.m[i] - most);   // 0 on the first page
         st.m[i] = most;
+        st.huge = (st.huge & ~(1u << i)) | (is_huge(most) ? 1u << i : 0u);
         st.l[i] *= alpha;
         #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -247,21 +250,37 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
       }
     }
   }
+  // the exponents, in the scores' place
+  const float2 c2 = make_float2(c, c);
+  #pragma unroll
+  for (int i = 0; i < 2 * kTiles; ++i) {
+    const int t = i / 2, h = 2 * (i % 2);
+    const float mu = st.m[i] == -INFINITY ? 0.f : st.m[i];
+    const float2 minus = make_float2(-mu, -mu);
+    #pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float* x = &s[t][nt][h];
+      if (rarely(st.huge != 0)) {
+        x[0] = less(x[0], c, mu, st.huge >> i & 1u);
+        x[1] = less(x[1], c, mu, st.huge >> i & 1u);
+      } else {
+        const float2 y = __ffma2_rn(make_float2(x[0], x[1]), c2, minus);
+        x[0] = y.x;
+        x[1] = y.y;
+      }
+    }
+  }
   // weights as three BF16 terms (24 bits): A fragments of rows g, g + 8 and tokens
   // 2 q, 2 q + 1, then 8 + 2 q, 9 + 2 q, where the scores' accumulators hold them
   uint32_t p[kTiles][3][4];
-  const float2 c2 = make_float2(c, c);
   #pragma unroll
   for (int t = 0; t < kTiles; ++t)
     #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float mu = st.m[2 * t + h] == -INFINITY ? 0.f : st.m[2 * t + h];
-      const float2 minus = make_float2(-mu, -mu);
       float2 sum = make_float2(0.f, 0.f);
       #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        const float2 x = __ffma2_rn(make_float2(s[t][nt][2 * h], s[t][nt][2 * h + 1]), c2, minus);
-        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        const float2 pp = make_float2(fast_exp2(s[t][nt][2 * h]), fast_exp2(s[t][nt][2 * h + 1]));
         sum = __fadd2_rn(sum, pp);
         split3(pp.x, pp.y, p[t][0][2 * nt + h], p[t][1][2 * nt + h], p[t][2][2 * nt + h]);
       }
