@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import paged_kv_cache_210_gb300 as pkv
-from quant_helpers import QuantCache, quantise
-from window_helpers import DIM, HKV, HQ, U
+from quant_helpers import QuantCache, attend, quantise
+from window_helpers import DIM, HKV, HQ, U, check
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,33 @@ def test_huge_scores(least, bits, sign, splits):
     off = (out[0].double().cpu() - ref.repeat_interleave(HQ // HKV, 0)).abs()
     worst = float((off / tol.repeat_interleave(HQ // HKV, 0)).amax())
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("below", [0, 20, 31])
+def test_query_dims_far_below_the_largest(below):
+    # down to 2^-31 of a head's largest dim, where no key is, a query's dims keep every
+    # bit: the scores are the other dims' alone, with keys larger by as much
+    n = 300
+    c = QuantCache([n], seed=below)
+    pool, kv = pkv.pkv_pool_create(1, c.num_pages, 1), c.pool()
+    g = torch.Generator().manual_seed(below)
+    ks = (torch.randn(n, HKV, DIM, generator=g) * 2.0 ** below).bfloat16()
+    vs = torch.randn(n, HKV, DIM, generator=g).bfloat16()
+    q = (torch.rand(1, HQ, DIM, generator=g) + 1.0) * 2.0 ** -below
+    q[:, :, 0] = 1.99
+    q = q.bfloat16()
+    ks[:, :, 0] = 0
+    pkv.pkv_quant_fill(pool, 0, ks.cuda(), vs.cuda(), kv, c.tables, int32([0, n]), int32([0]), n)
+    out = torch.empty(1, HQ, DIM, device="cuda")
+    pkv.pkv_quant_attention(pool, 0, q.cuda(), kv, c.tables, c.lens_tensor(), out, 2048)
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+    ref, tol = attend(q.double(), quantise(ks.double())[2], quantise(vs.double())[2],
+                      torch.tensor([n - 1]), 2048, 0)
+    check(out.cpu(), ref, tol)
+
+
+def test_the_smallest_weights_that_count():
+    # one token's score lies 115 base-2 units below the others', its V 2^110 above
+    score, size = np.zeros(200), np.ones(200)
+    score[150], size[150] = -80.0, 2.0 ** 110
+    run_scores_and_sizes(score, size)
