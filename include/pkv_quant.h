@@ -1,8 +1,15 @@
 /*
  * pkv_quant.h - an 8-bit KV cache: keys and values quantised as they are
  * written into pages, read back, and attended over in place. It takes 0.508 of
- * the bytes of the BF16 cache; handles, block tables, the scheduler, windows
- * and rotary positions are those of pkv.h, pkv_window.h and pkv_axes.h.
+ * the bytes of the BF16 cache; handles, block tables, windows and rotary
+ * positions are those of pkv.h, pkv_window.h and pkv_axes.h, admission and
+ * release those of pkv_sched.h.
+ *
+ * What it does not share: pkv_copy_pages and pkv_compact_pages move pages of two
+ * BF16 pools and none of this one (pkv_compact_pages would rewrite the tables all
+ * the same), so the copies that pkv_sched_fork and pkv_sched_compact ask for are
+ * the caller's to make: page i is row i of the tensor, whole. Chunks of a prompt and
+ * drafted trees attend over BF16 pools alone.
  *
  * Pool: kv_pool, one uint8 tensor [num_pages][8][PKV_QUANT_TILE_BYTES] for K
  * and V together (16-byte aligned). The tile of a (page, kv head):

@@ -150,3 +150,37 @@ def test_the_smallest_weights_that_count():
     score, size = np.zeros(200), np.ones(200)
     score[150], size[150] = -80.0, 2.0 ** 110
     run_scores_and_sizes(score, size)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+def test_pages_moved_by_rows_of_the_tensor(splits):
+    # a page is row i of the tensor, whole: moved elsewhere, with the table's entries, the
+    # same outputs come bit for bit; so do those of a fork that shares all pages but its
+    # last, which was copied
+    lens = [900, 40, 2048, 5]
+    c = QuantCache(lens, seed=1, spare=9)
+    kv = c.pool()
+    pool = pkv.pkv_pool_create(1, c.num_pages, 4)
+    q = torch.randn(4, HQ, DIM, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+
+    def attend_with(kv, tables, lens):
+        out = torch.empty(4, HQ, DIM, device="cuda")
+        pkv.pkv_quant_attention(pool, 0, q, kv, tables, int32(lens), out, 1500, sinks=20,
+                                num_splits=splits)
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+        return out
+
+    want = attend_with(kv, c.tables, lens)
+    for seed in range(2):
+        to = torch.randperm(c.num_pages, generator=torch.Generator().manual_seed(seed)).cuda()
+        moved = torch.empty_like(kv)
+        moved[to] = kv
+        tables = torch.where(c.tables >= 0, to[c.tables.clamp(min=0).long()].int(), -1)
+        assert torch.equal(attend_with(moved, tables, lens), want)
+    spare = sorted(set(range(c.num_pages)) - set(c.table[c.table >= 0].tolist()))[0]
+    forked, tables = kv.clone(), c.tables.clone()
+    forked[spare] = forked[int(tables[0, 0, 56])]          # 900 tokens: the last page is 56
+    tables[0, 1, :56], tables[0, 1, 56] = tables[0, 0, :56], spare
+    q[1] = q[0]
+    out = attend_with(forked, tables, [900, 900, 2048, 5])
+    assert torch.equal(out[0], out[1]) and torch.equal(out[2], want[2])
