@@ -39,6 +39,11 @@ extern "C" {
  *     p_i = start_pos[b] + (bits that count) - 1, a tree token's position.
  * window >= 1 (any value >= max_seq_len: every committed token), sinks >= 0. A row
  * that sees nothing is 0.
+ * The window hides committed tokens only: a drafted token that bit j names is seen
+ * whatever its distance. So for window >= the drafted tokens of the longest path a
+ * verified step sees what decode steps along that path would see one by one; behind a
+ * shorter window it sees more, and no tree says otherwise (bits left out also move p_i,
+ * and with it the window).
  *
  * Pages all of whose tokens no drafted token of the sequence sees and which hold no
  * drafted token are not read, their table entries may hold anything. In a page that
