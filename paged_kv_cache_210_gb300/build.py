@@ -11,6 +11,7 @@ import concurrent.futures
 import glob
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -44,27 +45,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
-    tmp = LIBRARY + f".tmp{os.getpid()}"
     flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
     if verbose:
         flags.insert(0, "-Xptxas=-v")
 
-    def compile_one(source):
-        obj = os.path.join(BUILD_DIR, f"{os.path.basename(source)}.{os.getpid()}.o")
-        subprocess.run([nvcc(), *flags, "-c", "-o", obj, source], check=True)
-        return obj
+    # everything is made in a folder of its own, which goes whatever fails
+    with tempfile.TemporaryDirectory(dir=BUILD_DIR) as made:
+        def compile_one(source):
+            obj = os.path.join(made, f"{os.path.basename(source)}.o")
+            subprocess.run([nvcc(), *flags, "-c", "-o", obj, source], check=True)
+            return obj
 
-    objects = []
-    try:
         # one compiler per source at a time, as many as there are cores
         with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
             objects = list(pool.map(compile_one, sources()))
+        library = os.path.join(made, os.path.basename(LIBRARY))
         subprocess.run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o",
-                        tmp, *objects], check=True)
-    finally:
-        for obj in objects:
-            os.remove(obj)
-    os.replace(tmp, LIBRARY)
+                        library, *objects], check=True)
+        os.replace(library, LIBRARY)
     return LIBRARY
 
 
