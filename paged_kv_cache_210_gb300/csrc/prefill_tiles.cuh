@@ -47,8 +47,9 @@
 //                         (has_page, page, n_pages), steps (first_step, n_steps;
 //                         plain_from, plain_to and has_dead count from the first),
 //                         keys that no row sees (dead)
-//   Walk, kDrawn          tile number -> Work, numbers ever larger; drawn from a
-//                         counter by the launch's CTAs, or the walk shares them out
+//   Walk, kDrawn          tile number -> Work, numbers ever larger, drawn from a
+//                         counter by the launch's CTAs (Params: next_tile, ctas_done);
+//                         or the walk shares the tiles out and takes no number
 //   Row                   what one row sees of a page
 //   kFewRows              tiles may leave whole softmax warps without rows
 //   kParts, is_whole, ... a tile may be a part of its rows' keys
@@ -129,8 +130,6 @@ struct TileParams {
   const int32_t* start_pos;   // [batch]
   float* out;                 // [total][32][64]
   int* err;
-  unsigned long long* next_tile;   // shared by the launch's CTAs; zero before and after it
-  unsigned int* ctas_done;         // the same
   int num_pages;
   int table_stride;
   int max_seq_len;
@@ -302,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
       bool ok = true;
       int issued = 0;
       if (warp == kLoadWarp) {
-        // K, Q and the tiles themselves: the launch's CTAs draw them from one
-        // counter, in TileWalk's order, the 8 KV heads of a tile in a row
+        // K, Q and the tiles themselves, in the order of the job's Walk
         RingAt<kKStages> at;
         int n = 0;                              // tiles handed over
         int q_loads = 0;
@@ -321,14 +319,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
           return __shfl_sync(0xffffffffu, good ? 1 : 0, 0) != 0;
         };
         for (bool first = true;; first = false) {
-          // The first tile is this CTA's own (nothing to wait for); each other
-          // one is drawn once the last one's copies are all on their way, a
+          // Drawn: the first tile is this CTA's own (nothing to wait for); each other
+          // one is taken once the last one's copies are all on their way, a
           // few steps before they are used up: any earlier, and a CTA would
           // hold a tile back from those that run out of work.
           unsigned long long index = blockIdx.x;
-          if (Job::kDrawn && !first) {
-            if (lane == 0) index = gridDim.x + atomicAdd(prm.next_tile, 1ull);
-            index = __shfl_sync(0xffffffffu, index, 0);
+          if constexpr (Job::kDrawn) {
+            if (!first) {
+              if (lane == 0) index = gridDim.x + atomicAdd(prm.next_tile, 1ull);
+              index = __shfl_sync(0xffffffffu, index, 0);
+            }
           }
           Work work;
           if (!walk.next(index, prm, lane, work)) break;
@@ -366,11 +366,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
         drain(sm.bar_k, issued, kKStages);
         drain(sm.bar_q, q_loads, kQBuffers);
         // the last CTA to stop drawing leaves the counters at zero
-        if (Job::kDrawn && lane == 0) {
-          __threadfence();
-          if (atomicAdd(prm.ctas_done, 1u) == gridDim.x - 1) {
-            *prm.next_tile = 0;
-            *prm.ctas_done = 0;
+        if constexpr (Job::kDrawn) {
+          if (lane == 0) {
+            __threadfence();
+            if (atomicAdd(prm.ctas_done, 1u) == gridDim.x - 1) {
+              *prm.next_tile = 0;
+              *prm.ctas_done = 0;
+            }
           }
         }
       } else {

@@ -191,8 +191,6 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   prm.start_pos = start_pos;
   prm.out = out;
   prm.err = pool->err;
-  prm.next_tile = pool->prefill_next;
-  prm.ctas_done = reinterpret_cast<unsigned int*>(pool->prefill_next + 1);
   prm.num_pages = c.num_pages;
   prm.table_stride = stride;
   prm.max_seq_len = c.max_seq_len;

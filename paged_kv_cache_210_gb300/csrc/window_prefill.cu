@@ -55,6 +55,8 @@ using namespace pkv_tiles;
 namespace {
 
 struct WindowPrefillParams : TileParams {
+  unsigned long long* next_tile;   // shared by the launch's CTAs; zero before and after it
+  unsigned int* ctas_done;         // the same
   int tiles_max;              // tiles per sequence the launch covers
 };
 
