@@ -127,11 +127,12 @@ typedef struct pkv_pool* pkv_pool_t;
 
 /* Validates the geometry and creates a handle on the current device. The
  * handle owns only device scratch: the split-KV partials (two layer-parity
- * copies of max_batch x 32 x max_splits x (64 + 2) floats), one ticket
- * counter per (sequence, kv head) and parity, one layer counter per sequence
- * (pkv_append_attend_layers), 12 bytes per pool page (pkv_pages.h), the parts of
- * drafted trees' sums (pkv_tree.h; 128 x (64 + 2) floats for each of 4 parts per
- * SM, about 20 MB) and the sticky error flag.
+ * copies of max_batch x 32 x max_splits x (64 + 2) floats, and no less than the
+ * parts of drafted trees' sums take in the same place: 128 x (64 + 2) floats for
+ * each of 4 per SM, about 20 MB, the size for max_batch x max_splits = 1,216), one
+ * ticket counter per (sequence, kv head) and parity, one layer counter per sequence
+ * (pkv_append_attend_layers), 12 bytes per pool page (pkv_pages.h) and the sticky
+ * error flag.
  * It does not own the pools, tables or tensors. A handle's launches share
  * that scratch, so they must be ordered in one stream (calls issued to
  * several streams at once need a handle each). Returns INVALID_ARG for a

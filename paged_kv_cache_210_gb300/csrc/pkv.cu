@@ -964,7 +964,9 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
     delete pool;
     return PKV_ERR_CUDA;
   }
-  const size_t rows = static_cast<size_t>(2) * c.max_batch * kHq * c.max_splits;
+  // the decode's partials, and the parts of drafted trees in the same place
+  const size_t rows = std::max(static_cast<size_t>(2) * c.max_batch * kHq * c.max_splits,
+                               pkv_tree_slots(pool) * 128);
   bool ok = cudaMalloc(&pool->part_o, rows * kDim * sizeof(float)) == cudaSuccess;
   ok = ok && cudaMalloc(&pool->part_ml, rows * sizeof(float2)) == cudaSuccess;
   ok = ok && cudaMalloc(&pool->tickets, 2 * static_cast<size_t>(c.max_batch) * kHkv * sizeof(int)) ==
@@ -977,9 +979,6 @@ pkv_status pkv_pool_create(const pkv_pool_config* config, pkv_pool_t* out) {
                  cudaSuccess;
   ok = ok && cudaMalloc(&pool->prefill_next, 2 * sizeof(unsigned long long)) == cudaSuccess &&
        cudaMemset(pool->prefill_next, 0, 2 * sizeof(unsigned long long)) == cudaSuccess;
-  const size_t slots = pkv_tree_slots(pool);
-  ok = ok && cudaMalloc(&pool->tree_part_o, slots * 128 * kDim * sizeof(float)) == cudaSuccess;
-  ok = ok && cudaMalloc(&pool->tree_part_ml, slots * 128 * sizeof(float2)) == cudaSuccess;
   if (ok) pool->page_to = reinterpret_cast<int*>(pool->page_marks + c.num_pages);
 
   ok = ok && cudaMemset(pool->tickets, 0, 2 * static_cast<size_t>(c.max_batch) * kHkv * sizeof(int)) ==
@@ -1051,8 +1050,6 @@ pkv_status pkv_pool_destroy(pkv_pool_t pool) {
   cudaFree(pool->err);
   cudaFree(pool->seq_done);
   cudaFree(pool->page_marks);
-  cudaFree(pool->tree_part_o);
-  cudaFree(pool->tree_part_ml);
   cudaFree(pool->prefill_next);
   delete pool;
   return st;

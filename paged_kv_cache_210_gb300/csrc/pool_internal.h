@@ -25,8 +25,11 @@ struct pkv_pool {
   int cluster_blocks_per_sm;   // the same for the narrow cluster-merge kernel
   int wide_blocks_per_sm;      // the same for the wide cluster-merge kernel
   int max_cluster;     // largest cluster size (power of two <= 16) the device schedules
-  float* part_o;     // [2][max_batch][32][max_splits][64]
-  float2* part_ml;   // [2][max_batch][32][max_splits]
+  // Partial sums of one launch: of decode calls [2][max_batch][32][max_splits], of drafted
+  // trees [pkv_tree_slots][128]. A tree's attention is launched when all before it is
+  // done, and a decode writes partials once the join before it is.
+  float* part_o;     // [...][64]
+  float2* part_ml;
   int* tickets;      // [2][max_batch][8]
   int* err;          // sticky error bits (PKV_DEV_ERR_*)
   int* seq_done;     // [max_batch]: layer completions per sequence (multi-layer launch)
@@ -37,8 +40,6 @@ struct pkv_pool {
                                     // allocation
   unsigned long long* prefill_next; // windowed prefill: tiles drawn, CTAs done (zero between
                                     // launches)
-  float* tree_part_o;               // [pkv_tree_slots][128][64] parts of drafted tokens' sums
-  float2* tree_part_ml;             // [pkv_tree_slots][128]
   WindowResidency window;           // the windowed decode over BF16 pages
   WindowResidency quant;            // ... and over 8-bit pages
   std::atomic<bool> pages_written{false};   // the handle's last page or fill call (pkv_pages.h,

@@ -199,8 +199,8 @@ pkv_status pkv_tree_attention(pkv_pool_t pool, int layer, const void* q, const v
   prm.window = std::min(window, c.max_seq_len);
   prm.sinks = std::min(sinks, c.max_seq_len);
   prm.tree = reinterpret_cast<const unsigned long long*>(tree);
-  prm.part_o = pool->tree_part_o;
-  prm.part_ml = pool->tree_part_ml;
+  prm.part_o = pool->part_o;
+  prm.part_ml = pool->part_ml;
   set_wave(&prm, wave);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) return pkv_tree_few(pool, q, tk, tv, prm, parts, st);

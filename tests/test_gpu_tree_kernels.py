@@ -246,3 +246,77 @@ def test_captured_with_changing_lengths(kernel):
         expect(c, q, out, starts, nodes, masks, max_seq_len, 0)
         assert bool((out[sum(nodes):] == 3.0).all())
     assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+
+
+def test_a_handle_of_many_sequences_keeps_no_room_for_trees():
+    # the decode's partials of 32 sequences x 64 splits (34.6 MB) are room enough, so a handle
+    # takes that and what cudaMalloc rounds up; with 20 MB of its own it took 55
+    def create():
+        return pkv.pkv_pool_create(1, 64, 32, max_seq_len=2048)
+
+    first = create()                               # loads the kernels
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    handles = [create() for _ in range(8)]
+    taken = before - torch.cuda.mem_get_info()[0]
+    partials = 2 * 32 * 32 * 64 * (64 + 2) * 4
+    assert taken <= 8 * (partials + (8 << 20)), taken
+    del handles, first
+
+
+@pytest.mark.parametrize("pdl", [False, True])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_trees_between_decode_calls_that_keep_partials(kernel, pdl):
+    # trees and the decode's tickets share the handle's scratch: the same outputs bit for
+    # bit as on a handle of each, issued one right after the other and replayed
+    max_seq_len, starts, nodes = KERNELS[kernel]
+    batch, total = len(starts), sum(nodes)
+    c = Cache([s + n for s, n in zip(starts, nodes)], max_seq_len=max_seq_len, seed=10)
+    k_pool, v_pool = c.pools(lambda b: np.ones(c.lens[b], bool))
+    flags = (pkv.PKV_FLAG_PDL if pdl else 0) | (pkv.PKV_FLAG_LONG_CONTEXT if max_seq_len > 2048 else 0)
+
+    def create():
+        return pkv.pkv_pool_create(1, c.num_pages, batch, max_seq_len=max_seq_len, flags=flags)
+
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(total, HQ, DIM, generator=g).bfloat16().cuda()
+    qd = torch.randn(batch, HQ, DIM, generator=g).bfloat16().cuda()
+    rng = np.random.RandomState(10)
+    tree = pack(sum([random_tree(rng, n) for n in nodes], []))
+    cu, start, lens = int32(np.cumsum([0] + nodes)), int32(starts), c.lens_tensor()
+
+    def trees(pool, out):
+        pkv.pkv_tree_attention(pool, 0, q, k_pool, v_pool, c.tables, cu, start, tree, out, max_seq_len)
+
+    def decode(pool, out, splits):
+        pkv.pkv_window_attention(pool, 0, qd, k_pool, v_pool, c.tables, lens, out, max_seq_len,
+                                 num_splits=splits)
+
+    def outputs():
+        return [torch.empty(total if i % 2 else batch, HQ, DIM, device="cuda") for i in range(5)]
+
+    want = outputs()
+    for i, out in enumerate(want):
+        trees(create(), out) if i % 2 else decode(create(), out, (64, 0, 40)[i // 2])
+    pool, got = create(), outputs()
+
+    def run():
+        for i, out in enumerate(got):
+            trees(pool, out) if i % 2 else decode(pool, out, (64, 0, 40)[i // 2])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for _ in range(20):
+        for out in got:
+            out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert pkv.pkv_get_error(pool) == pkv.PKV_OK
