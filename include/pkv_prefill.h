@@ -40,7 +40,9 @@
  * Arithmetic: scores and outputs accumulate in FP32 on the tensor cores
  * (BF16 operands); the softmax probabilities enter the value product as
  * the sum of two BF16 terms (a high and a low part), so the result meets
- * the same tolerance as the FP32 decode path.
+ * the same tolerance as the FP32 decode path for scores below 2^30 in magnitude
+ * (past that a row may be NaN or 0; pkv_window_prefill_attention with window >=
+ * max_seq_len takes any that FP32 holds).
  */
 #ifndef PKV_PREFILL_H
 #define PKV_PREFILL_H

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
       const bool idle = Job::kFewRows && warp * 8 >= work.count;
       bool s_done = false;                              // the next step's S is known to be there
       // what a step's largest score may not pass without a closer look: m_run and what p
-      // may grow by, or less where m_run is huge
+      // may grow by, or less where m_run is huge (device_common.cuh)
       float limit = -INFINITY;
       int segment = 0;                                  // j % kSegment, kSegment before a join
       for (int j = 0; j < n_steps; ++j, ++steps) {
