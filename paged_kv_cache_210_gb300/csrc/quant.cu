@@ -364,16 +364,15 @@ struct QuantTiles {
       }
     }
     const float2 to_log2 = make_float2(q.to_log2, q.to_log2);
-    auto exponentials = [&](auto may_be_huge) {
+    auto exponentials = [&](auto rounded) {
       const float2 minus = make_float2(-st.m_run, -st.m_run);
       sum = make_float2(0.f, 0.f);
       #pragma unroll
       for (int nt = 0; nt < kTiles; ++nt) {
         float2 x;
-        if constexpr (decltype(may_be_huge)::value) {
-          const bool rounded = is_huge(st.m_run);
-          x.x = less(s[nt].x, q.to_log2, st.m_run, rounded);
-          x.y = less(s[nt].y, q.to_log2, st.m_run, rounded);
+        if constexpr (decltype(rounded)::value) {   // where m_run is huge
+          x.x = less(s[nt].x, q.to_log2, st.m_run, true);
+          x.y = less(s[nt].y, q.to_log2, st.m_run, true);
         } else {
           x = __ffma2_rn(s[nt], to_log2, minus);
         }
@@ -400,7 +399,9 @@ struct QuantTiles {
         st.m_run = m;
         st.l_run *= power_of_2(-shift);    // 0 on the first page
       }
-      exponentials(std::true_type());
+      exponentials(std::false_type());
+      const bool huge = is_huge(st.m_run);
+      if (__builtin_expect(huge, 0)) exponentials(std::true_type());
       const float most = row_max(largest(w));
       int by = 0;                          // what they are multiplied by: 2^by <= 1
       st.unit = fabsf(st.unit);
@@ -417,14 +418,10 @@ struct QuantTiles {
         by = byte - was - shift;
       }
       st.rescale(power_of_2(by), lane);
-      if (is_huge(st.m_run)) {
-        st.unit = -st.unit;
-        #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt) w[nt] = make_float2(-w[nt].x, -w[nt].y);
-      }
+      if (huge) st.unit = -st.unit;
     }
     st.l_run += sum.x + sum.y;
-    const float2 unit = make_float2(st.unit, st.unit);
+    const float2 unit = make_float2(fabsf(st.unit), fabsf(st.unit));
     const uint16_t part = lane < 16 ? 0 : kMinusOne;   // high parts in lanes 0..15
     Weights out;
     #pragma unroll
