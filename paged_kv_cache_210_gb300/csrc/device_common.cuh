@@ -111,18 +111,18 @@ __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
   return max3(__uint_as_float(a), b, c);
 }
 
-// Whether base-2 scores are rounded before a maximum x of theirs is taken from them
-// (finite, 2^24 or more). With the product kept whole, a difference that should be 0 is the
-// maximum's rounding, and its exponential 0 or infinite from scores of 2^31 on.
-__device__ __forceinline__ bool is_huge(float x) {
+// Weights are taken from base-2 scores s c less a maximum of theirs, in one multiply-add.
+// Where the maximum m is huge (finite, 2^24 or more), from less() instead: with the
+// product kept whole, a difference that should be 0 is the maximum's rounding, and its
+// exponential 0 or infinite from scores of 2^31 on.
+__device__ __forceinline__ bool is_huge(float m) {
   constexpr uint32_t kHuge = (24u + 127u) << 23, kInf = 0x7f800000u;
-  return (__float_as_uint(x) & 0x7fffffffu) - kHuge < kInf - kHuge;
+  return (__float_as_uint(m) & 0x7fffffffu) - kHuge < kInf - kHuge;
 }
-
-// Base-2 scores s c less m, the product rounded or not. (By scalar intrinsics: those on
-// pairs may be contracted.)
-__device__ __forceinline__ float less(float s, float c, float m, bool rounded) {
-  return __fmaf_rn(rounded ? __fmul_rn(s, c) : s, rounded ? 1.f : c, -m);
+// The product rounded first, as the maximum's was. (By scalar intrinsics: those on pairs
+// may be contracted.)
+__device__ __forceinline__ float less(float s, float c, float m) {
+  return __fsub_rn(__fmul_rn(s, c), m);
 }
 
 // Two FP32 values -> BF16 pair (element 0 in the low half), each rounded to

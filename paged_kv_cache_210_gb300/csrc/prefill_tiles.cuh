@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tile_attention_kernel(
             // to the compiler, in place of c, costs every step 3 %)
             #pragma unroll
             for (int i = 0; i < kStepKeys; ++i)
-              sv[i] = __float_as_uint(less(__uint_as_float(sv[i]), c, mu, true) * (1.f / c));
+              sv[i] = __float_as_uint(less(__uint_as_float(sv[i]), c, mu) * (1.f / c));
             mu = 0.f;
           }
           if (j > 0) {

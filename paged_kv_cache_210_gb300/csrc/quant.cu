@@ -371,8 +371,8 @@ struct QuantTiles {
       for (int nt = 0; nt < kTiles; ++nt) {
         float2 x;
         if constexpr (decltype(rounded)::value) {   // where m_run is huge
-          x.x = less(s[nt].x, q.to_log2, st.m_run, true);
-          x.y = less(s[nt].y, q.to_log2, st.m_run, true);
+          x.x = less(s[nt].x, q.to_log2, st.m_run);
+          x.y = less(s[nt].y, q.to_log2, st.m_run);
         } else {
           x = __ffma2_rn(s[nt], to_log2, minus);
         }

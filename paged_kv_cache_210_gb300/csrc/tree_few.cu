@@ -156,9 +156,13 @@ __device__ __forceinline__ float quad_max(float x) {
 template <int kHalves>
 struct FewState {
   float o[kHalves][8][4];
-  float m[2 * kHalves];   // base-2 exponent the row's weights are taken against, p <= 2^8
+  // Base-2 exponent the row's weights are taken against, p <= 2^8. NaN where it is huge
+  // (device_common.cuh): it is then kept in shared memory, and each page's scores are
+  // replaced by what they differ from it, where the test that a page needs anyway leads.
+  // (That costs 32 trees of 8 over 2,000 tokens 2 %; a test for each page, with a factor and a
+  // maximum to choose, 7 %; a second copy of the page's arithmetic 4 %.)
+  float m[2 * kHalves];
   float l[2 * kHalves];   // this lane's share of the row's sum
-  uint32_t huge;          // bit i: m[i] is (is_huge)
   __device__ __forceinline__ void reset() {
     #pragma unroll
     for (int t = 0; t < kHalves; ++t)
@@ -171,17 +175,16 @@ struct FewState {
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
-    huge = 0;
   }
 };
 
 // One page, K tile kt and V tile vt (swizzled). kTiles: halves that have rows. seen:
 // what each of this lane's rows sees of it, 16 bits, where not `whole`; V rows that no
-// row sees hold zeros.
+// row sees hold zeros. huge_m: the warp's rows' exponents where they are huge.
 template <int kTiles, int kHalves>
 __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt, bool whole,
                                             const uint32_t (&seen)[2 * kHalves],
-                                            const uint4 (*q)[32], int lane,
+                                            const uint4 (*q)[32], float* huge_m, int lane,
                                             FewState<kHalves>& st) {
   const int g8 = lane >> 2;
   const int qq = lane & 3;
@@ -230,17 +233,20 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
   for (int i = 0; i < 2 * kTiles; ++i) {
     const int t = i / 2, h = 2 * (i % 2);
     top[i] = fmaxf(fmaxf(s[t][0][h], s[t][0][h + 1]), fmaxf(s[t][1][h], s[t][1][h + 1])) * c;
-    grow |= top[i] > st.m[i] + pkv_decode::kRescaleLog2;
+    grow |= !(top[i] <= st.m[i] + pkv_decode::kRescaleLog2);
   }
   // a row's exponent moves only when its maximum grows by more than 2^8
   if (__any_sync(0xffffffffu, grow)) {
+    bool huge = false;
     #pragma unroll
     for (int i = 0; i < 2 * kTiles; ++i) {
       const float most = quad_max(top[i]);
-      if (most > st.m[i] + pkv_decode::kRescaleLog2) {
-        const float alpha = fast_exp2(st.m[i] - most);   // 0 on the first page
-        st.m[i] = most;
-        st.huge = (st.huge & ~(1u << i)) | (is_huge(most) ? 1u << i : 0u);
+      const float kept = huge_m[8 * i + g8];     // read in any case: no branch
+      float m = st.m[i];
+      if (m != m) m = kept;
+      if (most > m + pkv_decode::kRescaleLog2) {
+        const float alpha = fast_exp2(m - most);         // 0 on the first page
+        st.m[i] = m = most;
         st.l[i] *= alpha;
         #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -248,39 +254,41 @@ __device__ __forceinline__ void attend_rows(const uint8_t* kt, const uint8_t* vt
           st.o[i / 2][n][2 * (i % 2) + 1] *= alpha;
         }
       }
+      top[i] = m;
+      huge |= is_huge(m);
     }
-  }
-  // the exponents, in the scores' place
-  const float2 c2 = make_float2(c, c);
-  #pragma unroll
-  for (int i = 0; i < 2 * kTiles; ++i) {
-    const int t = i / 2, h = 2 * (i % 2);
-    const float mu = st.m[i] == -INFINITY ? 0.f : st.m[i];
-    const float2 minus = make_float2(-mu, -mu);
-    #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      float* x = &s[t][nt][h];
-      if (rarely(st.huge != 0)) {
-        x[0] = less(x[0], c, mu, st.huge >> i & 1u);
-        x[1] = less(x[1], c, mu, st.huge >> i & 1u);
-      } else {
-        const float2 y = __ffma2_rn(make_float2(x[0], x[1]), c2, minus);
-        x[0] = y.x;
-        x[1] = y.y;
+    if (rarely(huge)) {
+      #pragma unroll
+      for (int i = 0; i < 2 * kTiles; ++i) {
+        const float m = top[i];
+        if (!is_huge(m)) continue;
+        huge_m[8 * i + g8] = m;          // the row's four lanes agree
+        st.m[i] = NAN;
+        #pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+          #pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& x = s[i / 2][nt][2 * (i % 2) + e];
+            x = less(x, c, m) * (1.f / c);
+          }
       }
     }
   }
   // weights as three BF16 terms (24 bits): A fragments of rows g, g + 8 and tokens
   // 2 q, 2 q + 1, then 8 + 2 q, 9 + 2 q, where the scores' accumulators hold them
   uint32_t p[kTiles][3][4];
+  const float2 c2 = make_float2(c, c);
   #pragma unroll
   for (int t = 0; t < kTiles; ++t)
     #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const float mu = st.m[2 * t + h] > -INFINITY ? st.m[2 * t + h] : 0.f;
+      const float2 minus = make_float2(-mu, -mu);
       float2 sum = make_float2(0.f, 0.f);
       #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        const float2 pp = make_float2(fast_exp2(s[t][nt][2 * h]), fast_exp2(s[t][nt][2 * h + 1]));
+        const float2 x = __ffma2_rn(make_float2(s[t][nt][2 * h], s[t][nt][2 * h + 1]), c2, minus);
+        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
         sum = __fadd2_rn(sum, pp);
         split3(pp.x, pp.y, p[t][0][2 * nt + h], p[t][1][2 * nt + h], p[t][2][2 * nt + h]);
       }
@@ -459,9 +467,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
           __syncwarp();
         }
         if (kHalves == 2 && work.count > kTokens / 2)
-          attend_rows<kHalves>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
+          attend_rows<kHalves>(ring.k[stage], ring.v[stage], whole, seen, sm.q, sm.m[warp], lane,
+                               st);
         else
-          attend_rows<1>(ring.k[stage], ring.v[stage], whole, seen, sm.q, lane, st);
+          attend_rows<1>(ring.k[stage], ring.v[stage], whole, seen, sm.q, sm.m[warp], lane, st);
       }
       __syncwarp();   // every lane's reads of the stage are done before it is refilled
       const int next = j + kFewStages;
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm<kHalves>) tree_fe
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (qq == 0) {
-        sm.m[warp][r] = st.m[i];
+        if (st.m[i] == st.m[i]) sm.m[warp][r] = st.m[i];
         sm.l[warp][r] = l;
       }
       #pragma unroll
