@@ -17,12 +17,13 @@
 // with one vote per group instead of two, exponentials taken before it; 84 (6.2 TB/s,
 // 93 % of the measured copy rate, 2 us more than the copies alone) with copies issued
 // by one lane from uniform operands and two stages a warp instead of three. 256 ragged
-// sequences behind 4,096 tokens, append and rotation included, take 68 us (77 %; the
-// short sequences' blocks are latency), 64 of up to 2,048 tokens 11.6 us, of which the
-// unit search, page ids, the first copies and the merge are 8, one of 2,048 4.5 us.
+// sequences behind 4,096 tokens, append and rotation included, take 68.5 us (76 %; the
+// short sequences' blocks are latency), 64 of up to 2,048 tokens 11.9 us, of which the
+// unit search, page ids, the first copies and the merge are 8, one of 2,048 4.6 us.
 // (Inputs larger than L2 in total, launches in a graph.) Slower: five blocks an SM (by
 // 7 to 20 %), scores computed ahead beside the products before them (2 % faster over
-// long contexts, 3 to 6 % slower in ragged batches).
+// long contexts, 3 to 6 % slower in ragged batches). Units that rise again and scores of any
+// size cost the branch of each warp's first group 0.1 us apiece.
 
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -9,16 +9,17 @@
 //
 // What bounds it: over long contexts the softmax warps, as in windowed prefill: a
 // step of two CTAs takes about 2,000 cycles. Eight trees of 49 to 64 tokens over
-// 20,000 to 32,700: 205 us, 460 TFLOP/s of score and value products counted once (254
+// 20,000 to 32,700: 204 us, 462 TFLOP/s of score and value products counted once (254
 // with parts of one length for a launch, a fifth of the CTAs idle at the end; 217 with
 // the parts joined by the last of a tile, in the same launch). A small call is latency:
 // of 32 trees of up to 16 tokens over up to 2,000, 21 us, a CTA needs 4.4 before its
 // first scores (set-up, its share of the line, page ids, copies), 0.7 a step, 2 at a
 // tile's end; the join 2.
 //
-// The commit moves 128-byte rows: 256 sequences of up to 8 tokens in 16 layers 19.8 us
-// (3.8 TB/s of scattered rows; 21.8 with divisions by a launch's number of heads), one
-// of 4 tokens 1.9 us.
+// The commit moves 128-byte rows: 256 sequences of up to 8 tokens in 16 layers 20 us
+// (3.8 TB/s; 2 more with divisions by a launch's number of heads), one of 4 tokens 2.1 us.
+// What bounds it is latency: 4,096 blocks, 4.5 waves, that each wait for three loads one
+// after the other, 44 % of their items tokens past the count; HBM is at 29 %, issue at 51 %.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -134,8 +135,8 @@ __global__ void __launch_bounds__(kCommitThreads, 6) tree_commit_kernel(
 // up to 8 drafted tokens a sequence on average. Measured (us, this and the other kernel;
 // sequences x drafted tokens, 2,000 committed): in clusters 1 x 8 7.4 and 12.9, 1 x 64
 // 14.3 and 15.4, 3 x 16 11.6 and 14.2, 4 x 16 14.1 and 15.3, over 300 7.9 and 11.6, 1 x 8
-// over 8,000 13.6 and 17.2; on the line 16 x 8 23.5 and 25.8, 32 x 8 36.4 and 40.4, 128 x
-// 4 91 and 119, 256 x 8 over 1,000 124 and 139, 1 x 8 over 16,000 20.5 and 20.4, 8 x 8
+// over 8,000 13.6 and 17.2; on the line 16 x 8 23.5 and 25.8, 32 x 8 36.6 and 40.4, 128 x
+// 4 91 and 119, 256 x 8 over 1,000 126 and 139, 1 x 8 over 16,000 20.5 and 20.4, 8 x 8
 // 59.5 and 60.7, 2 x 8 over 100,000 87.0 and 88.4; 8 x 16 22.5 and 19.3, 32 x 16 64 and
 // 47.
 bool few_rows(int batch, int total_tokens, int parts) {

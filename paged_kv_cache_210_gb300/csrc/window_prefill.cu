@@ -16,7 +16,7 @@
 // takes about 2,000 cycles, against 1,024 of the tensor pipe (16 products of 32
 // cycles each); a tile's start and end cost it some 4,000 more. The products are
 // never waited for: every barrier of theirs is complete when it is first looked
-// at. Two 4,096-token chunks behind a 4,096-token window: 467 us (591 TFLOP/s of
+// at. Two 4,096-token chunks behind a 4,096-token window: 463 us (596 TFLOP/s of
 // score and value products counted once); eight prompts of up to 2,048 tokens
 // behind 512: 111 us; sixteen of 512 tokens behind 128: 44.3 us. What was measured
 // on the way, the first of these: 718 us as a plain port of the step loop; 696
@@ -29,7 +29,8 @@
 // predicated arrivals; 472 with O joined behind the first half of P, when the
 // products it waits for are long done; 483 with segments of two steps instead of
 // four; 469 with steps of any four pages; 465 with the next tile looked up under
-// the last product; 467 with no tile drawn that does not exist. The second: 159
+// the last product; 467 with no tile drawn that does not exist; 463 with the limit
+// that a step's maximum is compared with kept between steps. The second: 159
 // us up to the page ids, one CTA per tile; 134 with tiles drawn by resident CTAs,
 // V cleared by its loader and results written through shared memory; 122 with
 // word masks and a first tile that needs no draw; 112, and 111 with the last of
