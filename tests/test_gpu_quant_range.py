@@ -184,3 +184,85 @@ def test_pages_moved_by_rows_of_the_tensor(splits):
     q[1] = q[0]
     out = attend_with(forked, tables, [900, 900, 2048, 5])
     assert torch.equal(out[0], out[1]) and torch.equal(out[2], want[2])
+
+
+def test_a_context_of_a_million_tokens():
+    n = pkv.PKV_MAX_LONG_CONTEXT
+    pages = n // 16 + 3
+    pool = pkv.pkv_pool_create(1, pages, 1, max_seq_len=n, flags=pkv.PKV_FLAG_LONG_CONTEXT)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tables = torch.randperm(pages, generator=torch.Generator().manual_seed(1))[:n // 16]
+    tables = tables.int().view(1, 1, -1).cuda()
+    kv = torch.zeros(pages, HKV, pkv.PKV_QUANT_TILE_BYTES, dtype=torch.uint8, device="cuda")
+    # V grows along the context, so that a part lost or taken twice shows (2^-9 of it and more);
+    # of n / 16 additions no more than 512 come one after the other (those of a warp's pages
+    # and of the parts)
+    k = (torch.randn(n, HKV, DIM, generator=g, device="cuda") / 8).bfloat16()
+    v = (torch.arange(n, device="cuda") / n).bfloat16()[:, None, None].expand(n, HKV, DIM).contiguous()
+    q = torch.randn(1, HQ, DIM, generator=g, device="cuda").bfloat16()
+    pkv.pkv_quant_fill(pool, 0, k, v, kv, tables, int32([0, n]), int32([0]), n)
+    pkv.pkv_quant_read(pool, 0, kv, tables, int32([0, n]), int32([0]), k, v, n)
+    out = torch.empty(1, HQ, DIM, device="cuda")
+    for window, sinks in ((n, 0), (500000, 100)):
+        pkv.pkv_quant_attention(pool, 0, q, kv, tables, int32([n]), out, window, sinks=sinks)
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+        ref, tol = attend(q.double(), k.double(), v.double(), torch.tensor([n - 1], device="cuda"),
+                          window, sinks)
+        count = min(n, window + sinks)
+        check(out, ref, tol - 2 * (count / 16 - 512) * U)
+
+
+@pytest.mark.parametrize("batch,longest", [(3, 2048), (40, 1500), (200, 300)])
+def test_programmatic_steps_of_several_layers(batch, longest):
+    # prompts filled, then steps of three layers: the same bytes and outputs as with ordinary
+    # launches, one by one and in a replayed graph
+    layers, steps = 3, 4
+    rng = np.random.RandomState(batch)
+    prompt = [int(x) for x in rng.randint(1, longest - steps, batch)]
+    needed = [-(-(n + steps) // 16) for n in prompt]
+    pages = layers * sum(needed) + 5
+    table = np.full((layers, batch, 128), -1, np.int32)
+    ids = iter(rng.permutation(pages))
+    for layer in range(layers):
+        for b in range(batch):
+            table[layer, b, :needed[b]] = [next(ids) for _ in range(needed[b])]
+    tables = torch.from_numpy(table).cuda()
+    cu, zeros = int32(np.cumsum([0] + prompt).tolist()), int32([0] * batch)
+    lens = [int32([n + step + 1 for n in prompt]) for step in range(steps)]
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def rows(n, heads):
+        return torch.randn(n, heads, DIM, generator=g, device="cuda").bfloat16()
+
+    ks = [rows(sum(prompt), HKV) for _ in range(layers)]
+    new = [[rows(batch, h) for h in (HQ, HKV, HKV)] for _ in range(layers * steps)]
+
+    def run(flags, replays):
+        pool = pkv.pkv_pool_create(layers, pages, batch, flags=flags)
+        kv = torch.zeros(pages, HKV, pkv.PKV_QUANT_TILE_BYTES, dtype=torch.uint8, device="cuda")
+        outs = [torch.zeros(batch, HQ, DIM, device="cuda") for _ in new]
+
+        def go():
+            for layer, k in enumerate(ks):
+                pkv.pkv_quant_fill(pool, layer, k, k, kv, tables, cu, zeros, max(prompt))
+            for i, (q, k, v) in enumerate(new):
+                pkv.pkv_quant_append_attend(pool, i % layers, q, k, v, kv, tables, lens[i // layers],
+                                            outs[i], 2048)
+
+        go()
+        if replays:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(s):
+                with torch.cuda.graph(graph, stream=s):
+                    go()
+            for _ in range(replays):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+        return [kv, *outs]
+
+    want = run(0, 0)
+    for replays in (0, 10):
+        assert all(torch.equal(a, b) for a, b in zip(run(pkv.PKV_FLAG_PDL, replays), want))

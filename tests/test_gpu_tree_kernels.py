@@ -320,3 +320,58 @@ def test_trees_between_decode_calls_that_keep_partials(kernel, pdl):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+
+
+@pytest.mark.parametrize("nodes", [4, 40])
+def test_a_context_of_a_million_tokens(nodes):
+    start = pkv.PKV_MAX_LONG_CONTEXT - 64
+    n = start + nodes
+    # V grows along the context, so that a part lost or taken twice shows (2^-8 of it and more);
+    # of n / 16 additions no more than 512 come one after the other (those of a warp's pages
+    # or a part's segments, and of the parts)
+    c = Cache([n], max_seq_len=pkv.PKV_MAX_LONG_CONTEXT, seed=1, k_scale=0.125)
+    c.v[0] = (torch.arange(n, device="cuda") / n).bfloat16()[:, None, None].repeat(1, HKV, DIM)
+    k_pool, v_pool = c.pools(lambda b: np.ones(c.lens[b], bool))
+    pool = handle(c)
+    masks = random_tree(np.random.RandomState(1), nodes)
+    q = torch.randn(nodes, HQ, DIM, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    out = torch.empty(nodes, HQ, DIM, device="cuda")
+    for window, sinks in ((c.max_seq_len, 0), (500000, 100)):
+        pkv.pkv_tree_attention(pool, 0, q, k_pool, v_pool, c.tables, int32([0, nodes]), int32([start]),
+                               pack(masks), out, window, sinks=sinks)
+        assert pkv.pkv_get_error(pool) == pkv.PKV_OK
+        seen = seen_matrix(start, masks, window, sinks)
+        for i in (0, nodes // 2, nodes - 1):
+            ref, tol = attend(q[i:i + 1].double(), c.k[0].double(), c.v[0].double(), seen[i:i + 1])
+            check(out[i:i + 1], ref, tol - 2 * (int(seen[i].sum()) / 16 - 512) * U)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_two_handles_on_two_streams(kernel):
+    max_seq_len, starts, nodes = KERNELS[kernel]
+    total = sum(nodes)
+    tree = pack(sum([random_tree(np.random.RandomState(3), n) for n in nodes], []))
+    q = torch.randn(total, HQ, DIM, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    cu, start = int32(np.cumsum([0] + nodes)), int32(starts)
+    calls, want = [], []
+    for seed in range(2):
+        c = Cache([s + n for s, n in zip(starts, nodes)], max_seq_len=max_seq_len, seed=seed)
+        k_pool, v_pool = c.pools(lambda b: np.ones(c.lens[b], bool))
+
+        def call(out, c=c, k_pool=k_pool, v_pool=v_pool, pool=handle(c)):
+            pkv.pkv_tree_attention(pool, 0, q, k_pool, v_pool, c.tables, cu, start, tree, out,
+                                   max_seq_len)
+
+        calls.append(call)
+        want.append(torch.empty(total, HQ, DIM, device="cuda"))
+        call(want[-1])
+    outs = [[torch.empty_like(want[0]) for _ in range(20)] for _ in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for i in range(20):
+        for call, stream, out in zip(calls, streams, outs):
+            with torch.cuda.stream(stream):
+                call(out[i])
+    torch.cuda.synchronize()
+    for out, ref in zip(outs, want):
+        assert all(torch.equal(o, ref) for o in out)
