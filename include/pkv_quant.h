@@ -84,7 +84,7 @@ pkv_status pkv_quant_read(pkv_pool_t pool, int layer, const void* kv_pool,
  * cache's values: keys below 2^122 in magnitude, scores and the sums of a
  * sequence's |V| inside FP32's range. Two things end earlier than in FP32: a
  * query's dim (after rotation) is held to within 2^-39 of its head's largest, so
- * dims down to 2^-31 of that keep all bits of a BF16 value, and those below 2^-39
+ * dims down to 2^-31 of that keep all bits of a BF16 value, and those below 2^-40
  * count as 0; a token whose weight is below 2^-118 of its head's largest counts
  * as 0. */
 pkv_status pkv_quant_attention(pkv_pool_t pool, int layer, const void* q, const void* kv_pool,

@@ -17,7 +17,7 @@
 // with one vote per group instead of two, exponentials taken before it; 84 (6.2 TB/s,
 // 93 % of the measured copy rate, 2 us more than the copies alone) with copies issued
 // by one lane from uniform operands and two stages a warp instead of three. 256 ragged
-// sequences behind 4,096 tokens, append and rotation included, take 68.5 us (76 %; the
+// sequences behind 4,096 tokens, append and rotation included, take 68.5 us (77 %; the
 // short sequences' blocks are latency), 64 of up to 2,048 tokens 11.9 us, of which the
 // unit search, page ids, the first copies and the merge are 8, one of 2,048 4.6 us.
 // (Inputs larger than L2 in total, launches in a graph.) Slower: five blocks an SM (by

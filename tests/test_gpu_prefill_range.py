@@ -17,7 +17,7 @@ def _library():
 
 
 @pytest.mark.parametrize("sign", [1.0, -1.0])
-@pytest.mark.parametrize("bits", [20, 24, 27, 28])
+@pytest.mark.parametrize("bits", [20, 24, 28, 29])
 def test_large_scores(bits, sign):
     # Keys of one dim whose scores are +-9/8 .. 15/8 2^bits: the largest that a row sees are
     # equal and share its output equally, the others lie 2^(bits - 4) and more below. The
